@@ -42,6 +42,17 @@ DG_ERROR_BLOCK_BYTES = 256
 DG_FFN_COMP_ONLY = 1
 DG_FFN_FUSED_GATE = 2
 DG_FFN_SEPARATE_GATE = 4
+DG_MOE_SIGMOID = 1
+DG_MOE_RENORM = 2
+
+
+class MoEShape(ctypes.Structure):
+    """dg_moe_shape: T tokens, model dim d, expert hidden dim F, E experts, k choices per token."""
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("F", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("k", ctypes.c_int32)]
+
+
+_PMOE = ctypes.POINTER(MoEShape)
 
 SIGNATURES = {
     "dg_last_error": (ctypes.c_char_p, []),
@@ -71,6 +82,15 @@ SIGNATURES = {
     "dg_tp_linear_fwd": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dg_tp_linear_bwd": (ctypes.c_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "dg_tp_swiglu_noalloc": (ctypes.c_int, [_i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "dg_w4_quantize": (ctypes.c_int, [_i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "dg_w4_dequantize": (ctypes.c_int, [_i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "dg_w4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dg_w4_linear": (ctypes.c_int, [_i64, _i64, _i64, _i32] + [_vp] * 7 + [_sz, _vp]),
+    "dg_moe_route_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
+    "dg_moe_route": (ctypes.c_int, [_i64, _i64, _i32, _i32, _u32, _f32] + [_vp] * 5 + [_sz, _vp]),
+    "dg_moe_swiglu_workspace_bytes": (_sz, [_PMOE]),
+    "dg_moe_swiglu": (ctypes.c_int, [_PMOE] + [_vp] * 7 + [_sz, _vp]),
+    "dg_moe_swiglu_w4": (ctypes.c_int, [_PMOE, _i32] + [_vp] * 11 + [_sz, _vp]),
     "dg_trace_begin": (ctypes.c_int, []),
     "dg_trace_begin_only": (ctypes.c_int, [ctypes.c_char_p]),
     "dg_trace_end": (ctypes.c_int32, [ctypes.POINTER(TraceEntry), ctypes.c_int32]),

@@ -345,4 +345,49 @@ cudaError_t launch_combine(const void* in, void* out, int P, int B, int T, int D
 
 cudaError_t launch_debug_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 
+// ---------------------------------------------------------------- 4-bit weights (dg_w4.cu)
+
+// Weights [rows, K] bf16 <-> codes [rows, K/2], scales [rows, K/group] bf16
+// and zero points [rows, K/group] (NULL: the symmetric form).
+cudaError_t launch_w4_quantize(const void* w, void* codes, void* scales, void* zeros, int64_t rows, int64_t K,
+                               int group, cudaStream_t s);
+cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const void* zeros, void* w, int64_t rows,
+                                 int64_t K, int group, cudaStream_t s);
+
+// y [rows, N] = x [rows, K] W^T (+ bias [N]) with W [N, K] in 4 bits.
+cudaError_t launch_w4_linear(const void* x, const void* codes, const void* scales, const void* zeros,
+                             const void* bias, void* y, int rows, int K, int N, int group, const DeviceInfo& dev,
+                             cudaStream_t s);
+
+// ---------------------------------------------------------------- routed experts (dg_moe.cu)
+
+// Limits of the routed operators: (token, choice) pairs of one call, experts,
+// choices per token.
+int moe_max_pairs();
+int moe_max_experts();
+int moe_max_topk();
+
+// logits [T, E] binary32 = x [T, d] w_router [E, d]^T; then idx and gates [T, k].
+cudaError_t launch_moe_logits(const void* x, const void* wr, float* logits, int T, int d, int E, const DeviceInfo& dev,
+                              cudaStream_t s);
+cudaError_t launch_moe_topk(const float* logits, void* idx, void* gates, int T, int E, int k, bool sigmoid,
+                            bool renorm, float scale, const DeviceInfo& dev, cudaStream_t s);
+
+// An expert weight tensor: bf16 (group 0, scales and zeros NULL) or 4-bit.
+struct MoeSource {
+  const void* data;
+  const void* scales;
+  const void* zeros;
+  int group;
+};
+
+// h [T*k, F] bf16 of every pair; partial rows part [T*k, d] binary32, gate
+// applied; y [T, d] bf16, their sum for each token.
+cudaError_t launch_moe_up(const MoeSource& w13, const void* x, const void* idx, void* h, int T, int k, int E, int d,
+                          int F, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_moe_down(const MoeSource& w2, const void* h, const void* idx, const void* gates, void* part, int T,
+                            int k, int E, int d, int F, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_moe_combine(const float* part, const void* idx, void* y, int T, int k, int E, int d,
+                               const DeviceInfo& dev, cudaStream_t s);
+
 }  // namespace dg

@@ -372,6 +372,106 @@ dg_status dg_tp_linear_bwd(int64_t rows, int64_t in_features, int64_t out_featur
                            void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit weights with group scales, and their product with a few rows.
+ *
+ * A weight [rows, K] bf16 is held as
+ *   codes  uint8 [rows, K/2]        two 4-bit codes to a byte, the even column
+ *                                   in the low nibble
+ *   scales bf16  [rows, K/group]    one per `group` consecutive columns
+ *   zeros  uint8 [rows, K/group]    zero points 0..15, or NULL: 8 everywhere
+ * and stands for value = (code - zero) * scale.  group is 32, 64 or 128 and
+ * divides K.  rows may run over several weights of the same K (for example
+ * [E, 2F, d] as E*2F rows).
+ *
+ * dg_w4_quantize, for each group of a row (quotients and differences in
+ * binary32, ties to even):
+ *   zeros NULL: scale = bf16(amax / 7), code = clamp(rne(w / scale) + 8, 0, 15)
+ *   otherwise:  lo = min(w, 0), hi = max(w, 0), scale = bf16((hi - lo) / 15),
+ *               zero = clamp(rne(-lo / scale), 0, 15),
+ *               code = clamp(rne(w / scale) + zero, 0, 15)
+ * A scale that would be 0 is 1.  A group that holds a NaN or an infinity, or
+ * whose hi - lo overflows binary32, gets a NaN scale and zero and codes 8 (so
+ * every product with it is NaN).
+ * dg_w4_dequantize writes the values, rounded once to bf16.
+ *
+ * dg_w4_linear: y = x W^T (+ bias), x [rows, in_features], W [out_features,
+ * in_features] as above, bias [out_features] or NULL, y [rows, out_features].
+ * Sums in binary32; one rounding to bf16.  Meant for few rows (a decode step):
+ * W is read once per 32 rows.  For long prompts dequantise once and use
+ * dg_tp_linear_fwd.  Any out_features >= 1; in_features % group == 0;
+ * rows >= 0 (0 = nothing to do), at most 65535 * 32.
+ * ws: the error block only (dg_w4_linear_workspace_bytes = 256 bytes).
+ * These calls have no backward: the codes are not trained.
+ * ------------------------------------------------------------------------ */
+dg_status dg_w4_quantize(int64_t rows, int64_t K, int32_t group, const void* weight, void* codes, void* scales,
+                         void* zeros, void* stream);
+
+dg_status dg_w4_dequantize(int64_t rows, int64_t K, int32_t group, const void* codes, const void* scales,
+                           const void* zeros, void* weight, void* stream);
+
+size_t dg_w4_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
+
+dg_status dg_w4_linear(int64_t rows, int64_t in_features, int64_t out_features, int32_t group, const void* x,
+                       const void* codes, const void* scales, const void* zeros, const void* bias, void* y,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Routed experts for few tokens: the router, and the SwiGLU experts' products.
+ *
+ * dg_moe_route.  logits[t, e] = sum_c x[t, c] * w_router[e, c], summed without
+ * rounding and rounded once to binary32.  Each token takes its k experts with
+ * the largest logits, in falling order; among equal logits the lower index
+ * comes first, and a NaN ranks behind every number, so idx always holds k
+ * distinct experts.  Gates (binary32):
+ *   softmax (default): exp(l - max l) / sum over all experts,
+ *     with DG_MOE_RENORM / sum over the chosen ones
+ *   DG_MOE_SIGMOID: 1 / (1 + exp(-l)), with DG_MOE_RENORM / sum over the chosen
+ * times `scale`.  A token with a NaN among its logits gets NaN gates.
+ *   x [T, d] bf16, w_router [E, d] bf16, idx [T, k] int32, gates [T, k] f32
+ *   T >= 0 (0 = nothing to do), at most 65535 * 4; d % 8 == 0;
+ *   1 <= k <= min(E, 32); E <= 1024
+ *
+ * dg_moe_swiglu.  For every pair (t, j) with 0 <= idx[t, j] < E,
+ *   h = silu(w1 x_t) * (w3 x_t),   y_t = sum_j gates[t, j] * (w2 h)
+ * with the weights of expert idx[t, j].  A pair with any other idx has no
+ * expert and adds nothing (padding, experts of another rank): a token without
+ * any gets a row of zeros.  The same expert may come twice in a row.
+ *   x [T, d], w13 [E, 2F, d] (rows [w1; w3], as w13 of dg_tp_swiglu),
+ *   w2 [E, d, F], y [T, d]: bf16;  idx [T, k] int32, gates [T, k] f32
+ * Products sum in binary32; h is rounded to bf16 once, y once.
+ * Requirements: d % 8 == 0, F % 8 == 0, d and F <= 2^20, 1 <= E <= 1024,
+ * 1 <= k <= 32, T >= 0 (0 = nothing to do), T * k <= 8192 (more is
+ * DG_ERR_UNSUPPORTED: split the batch).
+ * ws (dg_moe_swiglu_workspace_bytes): the error block, then scratch for the
+ * pairs' hidden and partial rows; nothing in it outlives the call.
+ *
+ * dg_moe_swiglu_w4: the same with both weights in 4 bits (layout above, E*2F
+ * and E*d rows; both with or both without zeros); d % group == 0, F % group == 0.
+ * No backward: training uses the bf16 layers above.
+ * ------------------------------------------------------------------------ */
+#define DG_MOE_SIGMOID 1u
+#define DG_MOE_RENORM 2u
+
+typedef struct {
+  int32_t T, d, F, E, k; /* tokens, model size, hidden size of an expert, experts, choices per token */
+} dg_moe_shape;
+
+size_t dg_moe_route_workspace_bytes(int64_t T, int64_t d, int32_t E, int32_t k);
+
+dg_status dg_moe_route(int64_t T, int64_t d, int32_t E, int32_t k, uint32_t flags, float scale, const void* x,
+                       const void* w_router, void* idx, void* gates, void* ws, size_t ws_bytes, void* stream);
+
+size_t dg_moe_swiglu_workspace_bytes(const dg_moe_shape* shape);
+
+dg_status dg_moe_swiglu(const dg_moe_shape* shape, const void* x, const void* idx, const void* gates,
+                        const void* w13, const void* w2, void* y, void* ws, size_t ws_bytes, void* stream);
+
+dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void* x, const void* idx,
+                           const void* gates, const void* w13_codes, const void* w13_scales, const void* w13_zeros,
+                           const void* w2_codes, const void* w2_scales, const void* w2_zeros, void* y, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics.
  * dg_debug_wait_timeout launches one small kernel that waits, with the
  * library's bounded wait, on a barrier nothing will ever arrive at; after
