@@ -2,9 +2,37 @@
 // routed experts.  Argument checks, scratch carving and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "dg_internal.h"
 
 namespace dg {
+
+cudaError_t smem_limit_once(const void* kern, int bytes, int dev) {
+  // open addressing on the kernel's address
+  struct Slot {
+    std::atomic<const void*> kern{nullptr};
+    std::atomic<uint64_t> done{0};  // bit per device
+  };
+  constexpr int kSlots = 128;
+  static Slot slots[kSlots];
+  size_t at = (reinterpret_cast<uintptr_t>(kern) >> 4) % kSlots;
+  for (int i = 0; i < kSlots; ++i, at = (at + 1) % kSlots) {
+    const void* k = slots[at].kern.load(std::memory_order_acquire);
+    if (k == nullptr) {
+      const void* expected = nullptr;
+      if (slots[at].kern.compare_exchange_strong(expected, kern)) k = kern;
+      else k = expected;
+    }
+    if (k != kern) continue;
+    const uint64_t bit = uint64_t(1) << dev;
+    if (slots[at].done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) slots[at].done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 namespace {
 

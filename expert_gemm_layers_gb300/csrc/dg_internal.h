@@ -345,6 +345,10 @@ cudaError_t launch_combine(const void* in, void* out, int P, int B, int T, int D
 
 cudaError_t launch_debug_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 
+// Sets a kernel's dynamic shared-memory limit the first time it is launched on
+// a device (`dev` current); later calls only look it up.
+cudaError_t smem_limit_once(const void* kern, int bytes, int dev);
+
 // ---------------------------------------------------------------- 4-bit weights (dg_w4.cu)
 
 // Weights [rows, K] bf16 <-> codes [rows, K/2], scales [rows, K/group] bf16

@@ -154,9 +154,11 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
 
 // ---------------------------------------------------------------- experts
 
-constexpr int kMoeWarps = 8;
+constexpr int kMoeWarps = kRowWarps;
 constexpr int kMoeThreads = kMoeWarps * 32;
 constexpr int kMaxPairs = 8192;
+constexpr int kMoeSmemMax = 227 * 1024;
+constexpr size_t kSmSmem = 228 * 1024;
 
 // The work of a call, built by every CTA from idx: entries of one expert and
 // up to `cap` of its pairs.  Shared memory: entry_expert[n], entry_start[n],
@@ -264,6 +266,11 @@ __device__ __forceinline__ PairMap build_pair_map(uint8_t* smem, const int32_t* 
   return m;
 }
 
+// pair / k as a product: kinv = 2^18 / k + 1 is exact for pairs below 2^13 and k up to 2^5.
+static_assert(kMaxPairs <= 8192 && kMaxTopk <= 32, "token_of");
+inline uint32_t token_factor(int k) { return (1u << 18) / static_cast<uint32_t>(k) + 1u; }
+__device__ __forceinline__ int token_of(uint32_t pair, uint32_t kinv) { return static_cast<int>((pair * kinv) >> 18); }
+
 // One of the two weight tensors of the experts.
 struct MoeWeights {
   const uint8_t* data;          // [E, rows, K] bf16, or codes [E, rows, K/2]
@@ -273,132 +280,100 @@ struct MoeWeights {
 };
 
 template <int FMT>
-__device__ __forceinline__ RowPair row_pair(const MoeWeights& w, int e, int lo, int hi) {
-  const int64_t a = static_cast<int64_t>(e) * w.rows + lo, b = static_cast<int64_t>(e) * w.rows + hi;
-  if constexpr (FMT == kFmtBf16) {
-    return RowPair{w.data + a * w.K * 2, w.data + b * w.K * 2, nullptr, nullptr, nullptr, nullptr};
-  } else {
-    const int64_t half = w.K / 2, groups = w.K / FMT;
-    return RowPair{w.data + a * half,         w.data + b * half,
-                   w.scales + a * groups,     w.scales + b * groups,
-                   w.zeros ? w.zeros + a * groups : nullptr, w.zeros ? w.zeros + b * groups : nullptr};
-  }
+__device__ __forceinline__ Rows expert_rows(const MoeWeights& w, int e) {
+  const int64_t first = static_cast<int64_t>(e) * w.rows;
+  if constexpr (FMT == kFmtBf16) return Rows{w.data + first * w.K * 2, nullptr, nullptr};
+  const int64_t groups = first * (w.K / (FMT ? FMT : 1));
+  return Rows{w.data + first * (w.K / 2), w.scales + groups, w.zeros ? w.zeros + groups : nullptr};
 }
 
-// h[pair, f] = bf16(silu(a) * b): a warp's 16 rows are 8 rows of w1 and the
-// same 8 of w3, so a and b of one (pair, f) meet in one thread.  h is rounded
-// to bf16 once: it is the next product's matrix operand.
-template <int FMT, int NT>
-__device__ __forceinline__ void up_block(const MoeWeights& w, const __nv_bfloat16* x, __nv_bfloat16* h,
-                                         const uint16_t* pairs, int count, int e, int fb, int k, int F, int wk, int WK,
-                                         int warp, float* red) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int d = w.K;
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-  const int f = fb * 8 + g;
-  if (fb * 8 < F) {
-    const RowPair r = row_pair<FMT>(w, e, min(f, F - 1), F + min(f, F - 1));
-    const __nv_bfloat16* xr[NT];
+// The units of a CTA: (entry, row block) pairs blockIdx.x, + gridDim.x, ... of
+// all entries and row blocks.  A row block is 8 / WK warps' worth of rows.
+//   UP    a warp's two row tiles are 16 rows of w1 and the same 16 of w3, so a and b
+//         of one (pair, f) meet in one thread: h[pair, f] = bf16(silu(a) * b).  h is
+//         rounded to bf16 once: it is the next product's matrix operand.
+//   else  32 rows of w2: part[pair, r] = gate * (w2[e, r] . h[pair])
+template <int FMT, int NT, bool UP>
+struct MoeWork {
+  const MoeWeights& w;
+  const PairMap& m;
+  const __nv_bfloat16* in;
+  const float* gates;
+  void* out;
+  uint32_t kinv;
+  int F, d, RG, blocks, total;
+
+  __device__ int units() const {
+    const int first = blockIdx.x, step = gridDim.x;
+    return first < total ? (total - first + step - 1) / step : 0;
+  }
+  __device__ int entry(int u) const { return static_cast<int>(blockIdx.x + u * gridDim.x) / blocks; }
+  __device__ int block(int u) const { return static_cast<int>(blockIdx.x + u * gridDim.x) % blocks; }
+  __device__ Rows rows(int u) const { return expert_rows<FMT>(w, m.entry_expert[entry(u)]); }
+  __device__ int row(int u, int rg, int lane, bool& active) const {
+    const int b = block(u) * RG + rg;
+    if (UP) {
+      active = b * 16 < F;
+      const int f = min(b * 16 + (lane & 15), F - 1);
+      return lane < 16 ? f : F + f;
+    }
+    active = b * 32 < d;
+    return min(b * 32 + lane, d - 1);
+  }
+  __device__ int count(int u) const { return m.entry_count[entry(u)]; }
+  __device__ const __nv_bfloat16* xrow(int u, int i) const {
+    const int p = m.pairs[m.entry_start[entry(u)] + i];
+    return UP ? in + static_cast<int64_t>(token_of(p, kinv)) * d : in + static_cast<int64_t>(p) * F;
+  }
+  __device__ void finish(int u, int rg, const float (&acc)[kRowTiles][NT][4]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int e = entry(u), n_pairs = m.entry_count[e];
+    const uint16_t* pairs = m.pairs + m.entry_start[e];
+    const int b = block(u) * RG + rg;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      xr[n] = 8 * n + g < count ? x + static_cast<int64_t>(pairs[8 * n + g] / k) * d : nullptr;
-    const int chunks = (d + rowdot_chunk<FMT>() - 1) / rowdot_chunk<FMT>();
-    row_dot<FMT, NT>(r, xr, d, chunks * wk / WK, chunks * (wk + 1) / WK, acc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * n + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+        if (c >= n_pairs) continue;
+        const int64_t p = pairs[c];
+        if (UP) {
+          const int f = b * 16 + r;
+          const float a = acc[0][n][i], v = acc[1][n][i];
+          if (f < F) static_cast<__nv_bfloat16*>(out)[p * F + f] = __float2bfloat16_rn(a / (1.0f + expf(-a)) * v);
+        } else {
+          const float gate = gates[p];
+#pragma unroll
+          for (int tile = 0; tile < kRowTiles; ++tile) {
+            const int row = b * 32 + 16 * tile + r;
+            if (row < d) static_cast<float*>(out)[p * d + row] = gate * acc[tile][n][i];
+          }
+        }
+      }
   }
-  join_slices<NT>(acc, red, warp, wk, WK);
-  if (wk != 0 || f >= F) return;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = 8 * n + 2 * t + i;
-      if (c >= count) continue;
-      const float a = acc[n][i], b = acc[n][2 + i];
-      h[static_cast<int64_t>(pairs[c]) * F + f] = __float2bfloat16_rn(a / (1.0f + expf(-a)) * b);
-    }
-}
+};
 
-// part[pair, r] = gate * (w2[e, r] . h[pair])
+// CTAs an SM holds by registers.
 template <int FMT, int NT>
-__device__ __forceinline__ void down_block(const MoeWeights& w, const __nv_bfloat16* h, const float* gates,
-                                           float* part, const uint16_t* pairs, int count, int e, int rb, int wk,
-                                           int WK, int warp, float* red) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int F = w.K, d = w.rows;
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-  const int r0 = rb * 16;
-  if (r0 < d) {
-    const RowPair r = row_pair<FMT>(w, e, min(r0 + g, d - 1), min(r0 + g + 8, d - 1));
-    const __nv_bfloat16* xr[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      xr[n] = 8 * n + g < count ? h + static_cast<int64_t>(pairs[8 * n + g]) * F : nullptr;
-    const int chunks = (F + rowdot_chunk<FMT>() - 1) / rowdot_chunk<FMT>();
-    row_dot<FMT, NT>(r, xr, F, chunks * wk / WK, chunks * (wk + 1) / WK, acc);
-  }
-  join_slices<NT>(acc, red, warp, wk, WK);
-  if (wk != 0 || r0 >= d) return;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = 8 * n + 2 * t + (i & 1), r = r0 + g + (i >> 1) * 8;
-      if (c < count && r < d)
-        part[static_cast<int64_t>(pairs[c]) * d + r] = gates[pairs[c]] * acc[n][i];
-    }
+constexpr int moe_ctas() {
+  return FMT == kFmtBf16 && NT == 1 ? 3 : 2;
 }
 
-// Both products walk (entry, row block) units; a CTA takes units blockIdx.x,
-// + gridDim.x, ...  UP: rows are F in blocks of 8; else d in blocks of 16.
-template <int FMT, int NTMAX, bool UP>
-__global__ void __launch_bounds__(kMoeThreads)
+template <int FMT, int NT, bool UP>
+__global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NT>())
     moe_product_kernel(MoeWeights w, const __nv_bfloat16* __restrict__ in, const int32_t* __restrict__ idx,
-                       const float* __restrict__ gates, void* __restrict__ out, int npairs, int k, int E, int WK,
-                       const uint32_t* err) {
-  extern __shared__ __align__(16) uint8_t smem[];
+                       const float* __restrict__ gates, void* __restrict__ out, int npairs, uint32_t kinv, int E,
+                       int WK, const uint32_t* err) {
+  extern __shared__ __align__(128) uint8_t smem[];
   griddep_wait();
   griddep_launch_dependents();
   if (err_set(err)) return;  // the word changes only between calls: uniform over the CTA
-  float* red = reinterpret_cast<float*>(smem);
-  const PairMap m = build_pair_map(smem + kMoeWarps * NTMAX * 128 * sizeof(float), idx, npairs, E, 8 * NTMAX);
-  const int warp = threadIdx.x >> 5;
-  const int wk = warp % WK, rg = warp / WK, RG = kMoeWarps / WK;
-  const int F = UP ? w.rows / 2 : w.K;
-  const int blocks = UP ? (F + 8 * RG - 1) / (8 * RG) : (w.rows + 16 * RG - 1) / (16 * RG);
-  const int units = *m.total * blocks;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int entry = u / blocks, b = (u - entry * blocks) * RG + rg;
-    const int e = m.entry_expert[entry], count = m.entry_count[entry];
-    const uint16_t* pairs = m.pairs + m.entry_start[entry];
-    auto go = [&](auto nt) {
-      constexpr int NT = decltype(nt)::value;
-      if constexpr (UP)
-        up_block<FMT, NT>(w, in, static_cast<__nv_bfloat16*>(out), pairs, count, e, b, k, F, wk, WK, warp, red);
-      else
-        down_block<FMT, NT>(w, in, gates, static_cast<float*>(out), pairs, count, e, b, wk, WK, warp, red);
-    };
-    if constexpr (NTMAX >= 4) {
-      if (count > 16) {
-        go(std::integral_constant<int, 4>{});
-        continue;
-      }
-    }
-    if constexpr (NTMAX >= 2) {
-      if (count > 8) {
-        go(std::integral_constant<int, 2>{});
-        continue;
-      }
-    }
-    go(std::integral_constant<int, 1>{});
-  }
+  const PairMap m = build_pair_map(smem + rowdot_smem<FMT, NT>(WK), idx, npairs, E, 8 * NT);
+  const int RG = kMoeWarps / WK;
+  const int F = UP ? w.rows / 2 : w.K, d = UP ? w.K : w.rows;
+  const int blocks = UP ? (F + 16 * RG - 1) / (16 * RG) : (d + 32 * RG - 1) / (32 * RG);
+  const MoeWork<FMT, NT, UP> work{w, m, in, gates, out, kinv, F, d, RG, blocks, *m.total * blocks};
+  row_stream<FMT, NT>(work, w.K, WK, smem);
 }
 
 // y[t] = the sum of the token's partial rows in the order of its choices;
@@ -428,29 +403,31 @@ __global__ void moe_combine_kernel(const float* __restrict__ part, const int32_t
   }
 }
 
-template <int FMT, int NTMAX, bool UP>
+template <int FMT, int NT, bool UP>
 cudaError_t launch_product(const MoeWeights& w, const __nv_bfloat16* in, const int32_t* idx, const float* gates,
                            void* out, int T, int k, int E, const DeviceInfo& dev, cudaStream_t s) {
   const int npairs = T * k;
-  const int entries = max_entries(npairs, E, 8 * NTMAX);
-  const int rows = UP ? w.rows / 2 : w.rows, step = UP ? 8 : 16;
-  const int64_t tiles = static_cast<int64_t>(entries) * ((rows + step - 1) / step);
-  const int chunks = (w.K + rowdot_chunk<FMT>() - 1) / rowdot_chunk<FMT>();
-  int WK = 1;
-  while (WK < kMoeWarps && tiles * WK < 16 * dev.num_sms && chunks >= 4 * WK) WK *= 2;
-  const int RG = kMoeWarps / WK;
-  const int64_t units = static_cast<int64_t>(entries) * ((rows + step * RG - 1) / (step * RG));
-  const size_t smem = kMoeWarps * NTMAX * 128 * sizeof(float) + pair_map_bytes(npairs, E, 8 * NTMAX);
-  auto kern = moe_product_kernel<FMT, NTMAX, UP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 112 * 1024);
+  const int entries = npairs < E ? npairs : E;  // active experts, at most (more only where one fills several entries)
+  const int rows = UP ? w.rows / 2 : w.rows, step = UP ? 16 : 32;
+  const int steps = (w.K + rowdot_step<FMT>() - 1) / rowdot_step<FMT>();
+  constexpr int kMostWK = NT == 4 ? 2 : NT == 2 ? 4 : kMoeWarps;  // the slices' staged rows have to fit
+  const int64_t slots = static_cast<int64_t>(moe_ctas<FMT, NT>()) * dev.num_sms;
+  int WK = rowdot_split((rows + step - 1) / step, entries, steps, kMostWK, slots);
+  const size_t map = pair_map_bytes(npairs, E, 8 * NT);
+  while (WK > 1 && rowdot_smem<FMT, NT>(WK) + map > kMoeSmemMax) WK /= 2;
+  const size_t smem = rowdot_smem<FMT, NT>(WK) + map;
+  auto kern = moe_product_kernel<FMT, NT, UP>;
+  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), kMoeSmemMax, dev.device);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMoeThreads, smem);
-  if (e != cudaSuccess) return e;
-  int64_t grid = static_cast<int64_t>(per_sm < 1 ? 1 : per_sm) * dev.num_sms;
+  // as many CTAs as the SM's shared memory and registers hold
+  int per_sm = static_cast<int>(kSmSmem / (smem + 1024));
+  per_sm = per_sm < 1 ? 1 : per_sm > moe_ctas<FMT, NT>() ? moe_ctas<FMT, NT>() : per_sm;
+  const int rg = kMoeWarps / WK;
+  const int64_t units = static_cast<int64_t>(max_entries(npairs, E, 8 * NT)) * ((rows + step * rg - 1) / (step * rg));
+  int64_t grid = static_cast<int64_t>(per_sm) * dev.num_sms;
   if (grid > units) grid = units;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kMoeThreads), smem, s, w, in, idx, gates, out,
-                    npairs, k, E, WK, static_cast<const uint32_t*>(dev.err));
+                    npairs, token_factor(k), E, WK, static_cast<const uint32_t*>(dev.err));
 }
 
 template <int FMT, bool UP>

@@ -95,72 +95,81 @@ __global__ void w4_dequantize_kernel(const uint32_t* __restrict__ codes, const _
   w[v] = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-constexpr int kLinWarps = 8;
+// The one unit of a w4_linear CTA: up to 8*NT activation rows, 8 / WK blocks of
+// 32 weight rows.
+template <int NT>
+struct LinearWork {
+  Rows w;
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* bias;
+  __nv_bfloat16* y;
+  int nx, K, N;  // activation rows, columns, weight rows
+  int r0, n0;    // the CTA's first weight row and activation row
 
-// y = x W^T (+ bias) for up to 8*NT rows a CTA: 8 / WK groups of 16 weight
-// rows, each split over WK warps along K and joined in shared memory.
+  __device__ int units() const { return 1; }
+  __device__ Rows rows(int) const { return w; }
+  __device__ int row(int, int rg, int lane, bool& active) const {
+    const int r = r0 + rg * 16 * kRowTiles;
+    active = r < N;
+    return min(r + lane, N - 1);
+  }
+  __device__ int count(int) const { return min(nx - n0, 8 * NT); }
+  __device__ const __nv_bfloat16* xrow(int, int i) const { return x + static_cast<int64_t>(n0 + i) * K; }
+  __device__ void finish(int, int rg, const float (&acc)[kRowTiles][NT][4]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < kRowTiles; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 16 * (kRowTiles * rg + m) + g + (i >> 1) * 8;
+        if (r >= N) continue;
+        const float b = bias ? __bfloat162float(bias[r]) : 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int row = n0 + 8 * n + 2 * t + (i & 1);
+          if (row < nx) y[static_cast<int64_t>(row) * N + r] = __float2bfloat16_rn(acc[m][n][i] + b);
+        }
+      }
+  }
+};
+
 template <int GROUP, int NT>
-__global__ void __launch_bounds__(kLinWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, 2)
     w4_linear_kernel(const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ codes,
                      const __nv_bfloat16* __restrict__ scales, const uint8_t* __restrict__ zeros,
                      const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N,
                      int WK, const uint32_t* err) {
-  extern __shared__ float red[];
+  extern __shared__ __align__(128) uint8_t smem[];
   griddep_wait();
   griddep_launch_dependents();
   if (err_set(err)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const int wk = warp % WK, rg = warp / WK;
-  const int r0 = (static_cast<int>(blockIdx.x) * (kLinWarps / WK) + rg) * 16;
-  const int n0 = static_cast<int>(blockIdx.y) * 8 * NT;
-  const int groups = K / GROUP;
-  float acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-  if (r0 < N) {
-    // rows past the last one read the last one and store nothing
-    const int64_t rl = min(r0 + g, N - 1), rh = min(r0 + g + 8, N - 1);
-    const RowPair w{codes + rl * (K / 2),        codes + rh * (K / 2),        scales + rl * groups,
-                    scales + rh * groups,        zeros ? zeros + rl * groups : nullptr,
-                    zeros ? zeros + rh * groups : nullptr};
-    const __nv_bfloat16* xr[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = n0 + 8 * n + g;
-      xr[n] = row < rows ? x + static_cast<int64_t>(row) * K : nullptr;
-    }
-    const int c0 = static_cast<int>(static_cast<int64_t>(groups) * wk / WK);
-    const int c1 = static_cast<int>(static_cast<int64_t>(groups) * (wk + 1) / WK);
-    row_dot<GROUP, NT>(w, xr, K, c0, c1, acc);
-  }
-  join_slices<NT>(acc, red, warp, wk, WK);
-  if (wk != 0 || r0 >= N) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + g + (i >> 1) * 8;
-    if (r >= N) continue;
-    const float b = bias ? __bfloat162float(bias[r]) : 0.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int row = n0 + 8 * n + 2 * t + (i & 1);
-      if (row < rows) y[static_cast<int64_t>(row) * N + r] = __float2bfloat16_rn(acc[n][i] + b);
-    }
-  }
+  const LinearWork<NT> work{Rows{codes, scales, zeros},
+                            x,
+                            bias,
+                            y,
+                            rows,
+                            K,
+                            N,
+                            static_cast<int>(blockIdx.x) * (kRowWarps / WK) * 16 * kRowTiles,
+                            static_cast<int>(blockIdx.y) * 8 * NT};
+  row_stream<GROUP, NT>(work, K, WK, smem);
 }
 
 template <int GROUP, int NT>
 cudaError_t launch_linear(const void* x, const void* codes, const void* scales, const void* zeros, const void* bias,
                           void* y, int rows, int K, int N, const DeviceInfo& dev, cudaStream_t s) {
-  // split K until the grid has about 16 warps for every SM
-  const int64_t tiles = (static_cast<int64_t>(N) + 15) / 16 * ((rows + 8 * NT - 1) / (8 * NT));
-  int WK = 1;
-  while (WK < kLinWarps && tiles * WK < 16 * dev.num_sms && K / GROUP >= 2 * WK) WK *= 2;
-  const int rg = kLinWarps / WK;
-  const dim3 grid((N + 16 * rg - 1) / (16 * rg), (rows + 8 * NT - 1) / (8 * NT));
-  return launch_pdl(w4_linear_kernel<GROUP, NT>, grid, dim3(kLinWarps * 32), kLinWarps * NT * 128 * sizeof(float), s,
+  constexpr int kRows = 16 * kRowTiles;
+  constexpr int kMostWK = NT == 4 ? 2 : NT == 2 ? 4 : kRowWarps;  // the slices' staged rows have to fit
+  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(w4_linear_kernel<GROUP, NT>),
+                                  rowdot_smem<GROUP, NT>(kMostWK), dev.device);
+  if (e != cudaSuccess) return e;
+  const int row_blocks = (rows + 8 * NT - 1) / (8 * NT);
+  const int steps = (K + rowdot_step<GROUP>() - 1) / rowdot_step<GROUP>();
+  const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, row_blocks, steps, kMostWK,
+                              2 * static_cast<int64_t>(dev.num_sms));
+  const int rg = kRowWarps / WK;
+  const dim3 grid((N + kRows * rg - 1) / (kRows * rg), row_blocks);
+  return launch_pdl(w4_linear_kernel<GROUP, NT>, grid, dim3(kRowWarps * 32), rowdot_smem<GROUP, NT>(WK), s,
                     static_cast<const __nv_bfloat16*>(x), static_cast<const uint8_t*>(codes),
                     static_cast<const __nv_bfloat16*>(scales), static_cast<const uint8_t*>(zeros),
                     static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), rows, K, N, WK,
