@@ -88,7 +88,7 @@ SIGNATURES = {
     "dg_w4_linear": (ctypes.c_int, [_i64, _i64, _i64, _i32] + [_vp] * 7 + [_sz, _vp]),
     "dg_moe_route_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32]),
     "dg_moe_route": (ctypes.c_int, [_i64, _i64, _i32, _i32, _u32, _f32] + [_vp] * 5 + [_sz, _vp]),
-    "dg_moe_swiglu_workspace_bytes": (_sz, [_PMOE]),
+    "dg_moe_swiglu_workspace_bytes": (_sz, [_PMOE, _i32]),
     "dg_moe_swiglu": (ctypes.c_int, [_PMOE] + [_vp] * 7 + [_sz, _vp]),
     "dg_moe_swiglu_w4": (ctypes.c_int, [_PMOE, _i32] + [_vp] * 11 + [_sz, _vp]),
     "dg_trace_begin": (ctypes.c_int, []),

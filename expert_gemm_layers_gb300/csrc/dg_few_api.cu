@@ -67,6 +67,7 @@ dg_status launched(cudaError_t e, const char* what) {
 
 constexpr int64_t kMaxDim = 0x7fffffff;
 constexpr int64_t kMaxW4Rows = int64_t(1) << 31;
+constexpr int64_t kMaxW4LinearRows = 65535 * 32;
 
 dg_status check_w4(int64_t rows, int64_t K, int32_t group, const char* what) {
   if (group != 32 && group != 64 && group != 128)
@@ -81,8 +82,6 @@ dg_status check_w4(int64_t rows, int64_t K, int32_t group, const char* what) {
 size_t code_bytes(int64_t rows, int64_t K) { return static_cast<size_t>(rows) * (K / 2); }
 size_t scale_bytes(int64_t rows, int64_t K, int32_t group) { return static_cast<size_t>(rows) * (K / group) * 2; }
 size_t zero_bytes(int64_t rows, int64_t K, int32_t group) { return static_cast<size_t>(rows) * (K / group); }
-
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 dg_status check_moe(const dg_moe_shape* sh, const char* what) {
   if (!sh) return fail(DG_ERR_INVALID_ARGUMENT, "%s: shape is NULL", what);
@@ -100,33 +99,8 @@ dg_status check_moe(const dg_moe_shape* sh, const char* what) {
   return DG_OK;
 }
 
-size_t hidden_bytes(const dg_moe_shape& s) { return up256(static_cast<size_t>(s.T) * s.k * s.F * 2); }
-size_t partial_bytes(const dg_moe_shape& s) { return up256(static_cast<size_t>(s.T) * s.k * s.d * 4); }
-
-dg_status moe_enqueue(const dg_moe_shape& s, const MoeSource& w13, const MoeSource& w2, const void* x,
-                      const void* idx, const void* gates, void* y, void* ws, const DeviceInfo& dev, cudaStream_t st,
-                      const char* what) {
-  uint8_t* base = static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES;
-  void* h = base;
-  float* part = reinterpret_cast<float*>(base + hidden_bytes(s));
-  const double pairs = static_cast<double>(s.T) * s.k;
-  const double experts = pairs < s.E ? pairs : s.E;
-  // bytes of one weight: bf16, or a nibble and its share of the group's scale and zero point
-  const double wb = w13.group ? 0.5 + (w13.zeros ? 3.0 : 2.0) / w13.group : 2.0;
-  const double df = static_cast<double>(s.d) * s.F;
-  dg_status r;
-  {
-    TraceScope trace("moe_up", st, 4.0 * pairs * df, experts * 2.0 * df * wb + 2.0 * s.T * s.d + 2.0 * pairs * s.F);
-    r = launched(launch_moe_up(w13, x, idx, h, s.T, s.k, s.E, s.d, s.F, dev, st), what);
-    if (r != DG_OK) return r;
-  }
-  {
-    TraceScope trace("moe_down", st, 2.0 * pairs * df, experts * df * wb + 2.0 * pairs * s.F + 4.0 * pairs * s.d);
-    r = launched(launch_moe_down(w2, h, idx, gates, part, s.T, s.k, s.E, s.d, s.F, dev, st), what);
-    if (r != DG_OK) return r;
-  }
-  TraceScope trace("moe_combine", st, 0.0, 4.0 * pairs * s.d + 2.0 * s.T * s.d);
-  return launched(launch_moe_combine(part, idx, y, s.T, s.k, s.E, s.d, dev, st), what);
+size_t moe_need(const dg_moe_shape& s, int group) {
+  return DG_ERROR_BLOCK_BYTES + moe_scratch_bytes(s.T, s.k, s.E, s.d, s.F, group);
 }
 
 }  // namespace
@@ -170,10 +144,11 @@ dg_status dg_w4_dequantize(int64_t rows, int64_t K, int32_t group, const void* c
 }
 
 size_t dg_w4_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
-  (void)rows;
-  (void)in_features;
   (void)out_features;
-  return DG_ERROR_BLOCK_BYTES;
+  if (rows < 0 || in_features < 1 || rows > kMaxW4LinearRows || in_features > kMaxDim) return 0;
+  // the finest group takes the most room, staged in the workspace or by the kernel itself
+  if (w4_linear_local(rows, in_features, 32)) return DG_ERROR_BLOCK_BYTES;
+  return DG_ERROR_BLOCK_BYTES + w4_linear_scratch_bytes(rows, in_features);
 }
 
 dg_status dg_w4_linear(int64_t rows, int64_t in_f, int64_t out_f, int32_t group, const void* x, const void* codes,
@@ -182,17 +157,23 @@ dg_status dg_w4_linear(int64_t rows, int64_t in_f, int64_t out_f, int32_t group,
   if (rows < 0 || out_f < 1) return fail(DG_ERR_INVALID_ARGUMENT, "w4_linear: rows must be >= 0, out_features >= 1");
   dg_status st = check_w4(out_f, in_f, group, "w4_linear");
   if (st != DG_OK) return st;
-  if (rows > 65535 * 32) return fail(DG_ERR_UNSUPPORTED, "w4_linear: more than %d rows", 65535 * 32);
-  if (out_f > kMaxDim - 256) return fail(DG_ERR_UNSUPPORTED, "w4_linear: out_features beyond 2^31 - 256");
+  if (rows > kMaxW4LinearRows)
+    return fail(DG_ERR_UNSUPPORTED, "w4_linear: more than %d rows", static_cast<int>(kMaxW4LinearRows));
+  if (out_f > kMaxDim - 256 || in_f > kMaxDim / 4)
+    return fail(DG_ERR_UNSUPPORTED, "w4_linear: out_features beyond 2^31 - 256, or in_features beyond 2^29");
   if (rows == 0) return DG_OK;
+  const size_t need = dg_w4_linear_workspace_bytes(rows, in_f, out_f);
   const Arg args[] = {{"x", x, static_cast<size_t>(rows) * in_f * 2, false, false},
                       {"codes", codes, code_bytes(out_f, in_f), false, false},
                       {"scales", scales, scale_bytes(out_f, in_f, group), false, false},
                       {"zeros", zeros, zero_bytes(out_f, in_f, group), true, false},
                       {"bias", bias, static_cast<size_t>(out_f) * 2, true, false},
                       {"y", y, static_cast<size_t>(rows) * out_f * 2, false, true},
-                      {"ws", ws, ws ? static_cast<size_t>(DG_ERROR_BLOCK_BYTES) : 0, true, true}};
+                      {"ws", ws, ws ? need : 0, true, true}};
   if ((st = check_args("w4_linear", args)) != DG_OK) return st;
+  if ((st = check_error_block(ws, ws_bytes, "w4_linear")) != DG_OK) return st;
+  if (ws_bytes < need)
+    return fail(DG_ERR_WORKSPACE, "w4_linear: workspace has %zu bytes, needs %zu", ws_bytes, need);
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "w4_linear")) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -200,7 +181,8 @@ dg_status dg_w4_linear(int64_t rows, int64_t in_f, int64_t out_f, int32_t group,
   TraceScope trace("w4_linear", s, 2.0 * rows * kn,
                    kn * (0.5 + (zeros ? 3.0 : 2.0) / group) + 2.0 * rows * (static_cast<double>(in_f) + out_f));
   return launched(launch_w4_linear(x, codes, scales, zeros, bias, y, static_cast<int>(rows), static_cast<int>(in_f),
-                                   static_cast<int>(out_f), group, dev, s),
+                                   static_cast<int>(out_f), group, static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES,
+                                   dev, s),
                   "w4_linear");
 }
 
@@ -250,9 +232,13 @@ dg_status dg_moe_route(int64_t T, int64_t d, int32_t E, int32_t k, uint32_t flag
                   "moe_route");
 }
 
-size_t dg_moe_swiglu_workspace_bytes(const dg_moe_shape* shape) {
+size_t dg_moe_swiglu_workspace_bytes(const dg_moe_shape* shape, int32_t group) {
   if (check_moe(shape, "moe_swiglu") != DG_OK) return 0;
-  return DG_ERROR_BLOCK_BYTES + hidden_bytes(*shape) + partial_bytes(*shape);
+  if (group != 0 && group != 32 && group != 64 && group != 128) {
+    fail(DG_ERR_INVALID_ARGUMENT, "moe_swiglu: group is %d, not 0 (bf16), 32, 64 or 128", group);
+    return 0;
+  }
+  return moe_need(*shape, group);
 }
 
 dg_status dg_moe_swiglu(const dg_moe_shape* shape, const void* x, const void* idx, const void* gates,
@@ -260,7 +246,7 @@ dg_status dg_moe_swiglu(const dg_moe_shape* shape, const void* x, const void* id
   dg_status st = check_moe(shape, "moe_swiglu");
   if (st != DG_OK || shape->T == 0) return st;
   const dg_moe_shape& s = *shape;
-  const size_t need = dg_moe_swiglu_workspace_bytes(shape);
+  const size_t need = moe_need(s, 0);
   const size_t wn = static_cast<size_t>(s.E) * s.d * s.F * 2, xn = static_cast<size_t>(s.T) * s.d * 2;
   const size_t pn = static_cast<size_t>(s.T) * s.k * 4;
   const Arg args[] = {{"x", x, xn, false, false},        {"idx", idx, pn, false, false},
@@ -273,8 +259,10 @@ dg_status dg_moe_swiglu(const dg_moe_shape* shape, const void* x, const void* id
     return fail(DG_ERR_WORKSPACE, "moe_swiglu: workspace has %zu bytes, needs %zu", ws_bytes, need);
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "moe_swiglu")) != DG_OK) return st;
-  return moe_enqueue(s, MoeSource{w13, nullptr, nullptr, 0}, MoeSource{w2, nullptr, nullptr, 0}, x, idx, gates, y, ws,
-                     dev, static_cast<cudaStream_t>(stream), "moe_swiglu");
+  const MoeCall call{x, idx, gates, w13, nullptr, nullptr, w2, nullptr, nullptr, y,
+                     static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES, s.T, s.k, s.E, s.d, s.F, 0};
+  MoeTrace trace(static_cast<cudaStream_t>(stream));
+  return launched(launch_moe_swiglu(call, dev, static_cast<cudaStream_t>(stream), &trace), "moe_swiglu");
 }
 
 dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void* x, const void* idx,
@@ -291,7 +279,7 @@ dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void*
   if ((w13_zeros == nullptr) != (w2_zeros == nullptr))
     return fail(DG_ERR_INVALID_ARGUMENT, "moe_swiglu_w4: w13_zeros and w2_zeros must both be given or both be NULL");
   if (s.T == 0) return DG_OK;
-  const size_t need = dg_moe_swiglu_workspace_bytes(shape);
+  const size_t need = moe_need(s, group);
   const int64_t up_rows = static_cast<int64_t>(s.E) * 2 * s.F, down_rows = static_cast<int64_t>(s.E) * s.d;
   const size_t xn = static_cast<size_t>(s.T) * s.d * 2, pn = static_cast<size_t>(s.T) * s.k * 4;
   const Arg args[] = {{"x", x, xn, false, false},
@@ -311,9 +299,10 @@ dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void*
     return fail(DG_ERR_WORKSPACE, "moe_swiglu_w4: workspace has %zu bytes, needs %zu", ws_bytes, need);
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "moe_swiglu_w4")) != DG_OK) return st;
-  return moe_enqueue(s, MoeSource{w13_codes, w13_scales, w13_zeros, group},
-                     MoeSource{w2_codes, w2_scales, w2_zeros, group}, x, idx, gates, y, ws, dev,
-                     static_cast<cudaStream_t>(stream), "moe_swiglu_w4");
+  const MoeCall call{x, idx, gates, w13_codes, w13_scales, w13_zeros, w2_codes, w2_scales, w2_zeros, y,
+                     static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES, s.T, s.k, s.E, s.d, s.F, group};
+  MoeTrace trace(static_cast<cudaStream_t>(stream));
+  return launched(launch_moe_swiglu(call, dev, static_cast<cudaStream_t>(stream), &trace), "moe_swiglu_w4");
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <optional>
 #include <utility>
 
 #include "../../include/dg.h"
@@ -358,10 +359,13 @@ cudaError_t launch_w4_quantize(const void* w, void* codes, void* scales, void* z
 cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const void* zeros, void* w, int64_t rows,
                                  int64_t K, int group, cudaStream_t s);
 
-// y [rows, N] = x [rows, K] W^T (+ bias [N]) with W [N, K] in 4 bits.
+// y [rows, N] = x [rows, K] W^T (+ bias [N]) with W [N, K] in 4 bits.  Unless
+// w4_linear_local, scratch holds w4_linear_scratch_bytes.
+bool w4_linear_local(int64_t rows, int64_t K, int group);
+size_t w4_linear_scratch_bytes(int64_t rows, int64_t K);
 cudaError_t launch_w4_linear(const void* x, const void* codes, const void* scales, const void* zeros,
-                             const void* bias, void* y, int rows, int K, int N, int group, const DeviceInfo& dev,
-                             cudaStream_t s);
+                             const void* bias, void* y, int rows, int K, int N, int group, void* scratch,
+                             const DeviceInfo& dev, cudaStream_t s);
 
 // ---------------------------------------------------------------- routed experts (dg_moe.cu)
 
@@ -377,21 +381,28 @@ cudaError_t launch_moe_logits(const void* x, const void* wr, float* logits, int 
 cudaError_t launch_moe_topk(const float* logits, void* idx, void* gates, int T, int E, int k, bool sigmoid,
                             bool renorm, float scale, const DeviceInfo& dev, cudaStream_t s);
 
-// An expert weight tensor: bf16 (group 0, scales and zeros NULL) or 4-bit.
-struct MoeSource {
-  const void* data;
-  const void* scales;
-  const void* zeros;
-  int group;
+// One call of the routed SwiGLU experts.  group 0: bf16 weights (s*, z* NULL),
+// else 4-bit codes w*, scales s* and zero points z* (NULL: 8).
+struct MoeCall {
+  const void *x, *idx, *gates;
+  const void *w13, *s13, *z13;
+  const void *w2, *s2, *z2;
+  void *y, *scratch;  // scratch: moe_scratch_bytes
+  int T, k, E, d, F, group;
 };
+size_t moe_scratch_bytes(int T, int k, int E, int d, int F, int group);
 
-// h [T*k, F] bf16 of every pair; partial rows part [T*k, d] binary32, gate
-// applied; y [T, d] bf16, their sum for each token.
-cudaError_t launch_moe_up(const MoeSource& w13, const void* x, const void* idx, void* h, int T, int k, int E, int d,
-                          int F, const DeviceInfo& dev, cudaStream_t s);
-cudaError_t launch_moe_down(const MoeSource& w2, const void* h, const void* idx, const void* gates, void* part, int T,
-                            int k, int E, int d, int F, const DeviceInfo& dev, cudaStream_t s);
-cudaError_t launch_moe_combine(const float* part, const void* idx, void* y, int T, int k, int E, int d,
-                               const DeviceInfo& dev, cudaStream_t s);
+// Brackets the launches of a call for tracing: at most one TraceScope at a time.
+class MoeTrace {
+ public:
+  explicit MoeTrace(cudaStream_t s) : stream_(s) {}
+  void begin(const char* name, double flops, double bytes) { scope_.emplace(name, stream_, flops, bytes); }
+  void end() { scope_.reset(); }
+
+ private:
+  cudaStream_t stream_;
+  std::optional<TraceScope> scope_;
+};
+cudaError_t launch_moe_swiglu(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s, MoeTrace* trace);
 
 }  // namespace dg

@@ -9,7 +9,7 @@
 #include <cuda_bf16.h>
 
 #include "dg_internal.h"
-#include "dg_rowdot.cuh"
+#include "dg_w4dot.cuh"
 
 namespace dg {
 
@@ -157,49 +157,67 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
 constexpr int kMoeWarps = kRowWarps;
 constexpr int kMoeThreads = kMoeWarps * 32;
 constexpr int kMaxPairs = 8192;
-constexpr int kMoeSmemMax = 227 * 1024;
-constexpr size_t kSmSmem = 228 * 1024;
+constexpr int kFmtBf16 = 0;  // weight format: this, or the group size of 4-bit weights
 
-// The work of a call, built by every CTA from idx: entries of one expert and
-// up to `cap` of its pairs.  Shared memory: entry_expert[n], entry_start[n],
-// entry_count[n] and pairs[] (the pairs sorted by expert).
-//
-// Every CTA must come to the same order of an expert's pairs, since the units
-// of its entries may run on different CTAs: the sort is stable.  Warp w counts
-// and later places the w-th run of pairs, so `at[w][e]` is where its next pair
-// of expert e goes.
+// The work of a call: entries of one expert and up to `cap` of its pairs, which
+// stand one after the other in pairs[].  An expert with more pairs has several
+// entries.
 struct PairMap {
-  int* at;            // [kMoeWarps][E]
-  int* entry_expert;  // [max_entries]
-  int* entry_start;
-  int* entry_count;
-  int* total;       // number of entries
-  uint16_t* pairs;  // [npairs]
+  int* total;  // number of entries
+  int* expert;
+  int* start;
+  int* count;
+  int* pairs;
 };
 
 __host__ __device__ inline int max_entries(int npairs, int E, int cap) {
   const int active = npairs < E ? npairs : E;
   return active + npairs / cap;
 }
-
-inline size_t pair_map_bytes(int npairs, int E, int cap) {
-  return sizeof(int) * (kMoeWarps * static_cast<size_t>(E) + 1 +
-                        3 * static_cast<size_t>(max_entries(npairs, E, cap))) +
-         (2 * static_cast<size_t>(npairs) + 15) / 16 * 16;
+// Ints of a PairMap.
+__host__ __device__ inline int pair_map_ints(int npairs, int E, int cap) {
+  return 4 + 3 * max_entries(npairs, E, cap) + npairs;
+}
+__host__ __device__ inline PairMap pair_map_at(int* p, int npairs, int E, int cap) {
+  const int me = max_entries(npairs, E, cap);
+  return PairMap{p, p + 4, p + 4 + me, p + 4 + 2 * me, p + 4 + 3 * me};
 }
 
-__device__ __forceinline__ PairMap build_pair_map(uint8_t* smem, const int32_t* __restrict__ idx, int npairs, int E,
-                                                  int cap) {
-  PairMap m;
-  const int me = max_entries(npairs, E, cap);
-  m.at = reinterpret_cast<int*>(smem);
-  m.entry_expert = m.at + kMoeWarps * E;
-  m.entry_start = m.entry_expert + me;
-  m.entry_count = m.entry_start + me;
-  m.total = m.entry_count + me;
-  m.pairs = reinterpret_cast<uint16_t*>(m.total + 1);
+// Up to 32 pairs: one warp's lanes are the pairs, and every CTA does this itself
+// (to the same result: entries in the order of their first pair).
+__device__ __forceinline__ void build_small_map(const PairMap& m, const int32_t* idx, int npairs, int E, int cap) {
+  const int lane = threadIdx.x & 31;
+  int e = lane < npairs ? idx[lane] : -1;
+  if (e < 0 || e >= E) e = -1;
+  const uint32_t valid = __ballot_sync(0xffffffffu, e >= 0);
+  const uint32_t same = __match_any_sync(0xffffffffu, e) & valid, below = (1u << lane) - 1u;
+  const int rank = __popc(same & below), n = __popc(same);
+  const uint32_t starters = __ballot_sync(0xffffffffu, e >= 0 && rank % cap == 0);
+  int before = 0, entry = 0;
+  for (uint32_t s = starters; s; s &= s - 1, ++entry) {
+    const int l = __ffs(s) - 1;
+    const int s_rank = __shfl_sync(0xffffffffu, rank, l), s_n = __shfl_sync(0xffffffffu, n, l);
+    const int s_e = __shfl_sync(0xffffffffu, e, l);
+    const int size = min(cap, s_n - s_rank);
+    if (e == s_e && rank >= s_rank && rank < s_rank + size) m.pairs[before + rank - s_rank] = lane;
+    if (lane == 0) {
+      m.expert[entry] = s_e;
+      m.start[entry] = before;
+      m.count[entry] = size;
+    }
+    before += size;
+  }
+  if (lane == 0) *m.total = entry;
+}
+
+// Any number of pairs, by one CTA, entries in the order of the experts, an
+// expert's pairs in theirs (the sort is stable, so that a call repeats bit for
+// bit).  Warp w counts and later places the w-th run of pairs: at[w][e] is where
+// its next pair of expert e goes.
+__device__ __forceinline__ void build_map(const PairMap& m, int* at_all, const int32_t* __restrict__ idx, int npairs,
+                                          int E, int cap) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* at = m.at + warp * E;
+  int* at = at_all + warp * E;
   const int run = (npairs + kMoeThreads - 1) / kMoeThreads * 32;  // pairs of a warp
   const int p0 = warp * run, p1 = min(p0 + run, npairs);
   for (int e = lane; e < E; e += 32) at[e] = 0;
@@ -215,7 +233,7 @@ __device__ __forceinline__ PairMap build_pair_map(uint8_t* smem, const int32_t* 
       const int e = e0 + lane;
       int n = 0;
       if (e < E)
-        for (int w = 0; w < kMoeWarps; ++w) n += m.at[w * E + e];
+        for (int w = 0; w < kMoeWarps; ++w) n += at_all[w * E + e];
       const int ne = (n + cap - 1) / cap;
       int sn = n, se = ne;
 #pragma unroll
@@ -231,16 +249,16 @@ __device__ __forceinline__ PairMap build_pair_map(uint8_t* smem, const int32_t* 
       if (e < E) {
         int next = start;
         for (int w = 0; w < kMoeWarps; ++w) {
-          const int c = m.at[w * E + e];
-          m.at[w * E + e] = next;
+          const int c = at_all[w * E + e];
+          at_all[w * E + e] = next;
           next += c;
         }
       }
       for (int i = 0; i < ne; ++i) {
         const int to = entries_before + se - ne + i;
-        m.entry_expert[to] = e;
-        m.entry_start[to] = start + i * cap;
-        m.entry_count[to] = min(cap, n - i * cap);
+        m.expert[to] = e;
+        m.start[to] = start + i * cap;
+        m.count[to] = min(cap, n - i * cap);
       }
       pairs_before += __shfl_sync(0xffffffffu, sn, 31);
       entries_before += __shfl_sync(0xffffffffu, se, 31);
@@ -257,13 +275,65 @@ __device__ __forceinline__ PairMap build_pair_map(uint8_t* smem, const int32_t* 
     const int base = e >= 0 ? at[e] : 0;
     __syncwarp();
     if (e >= 0) {
-      m.pairs[base + before] = static_cast<uint16_t>(p);
+      m.pairs[base + before] = p;
       if (before == 0) at[e] = base + __popc(same);
     }
     __syncwarp();
   }
-  __syncthreads();
-  return m;
+}
+
+// Rows to stage for 4-bit products: [rows][K] bf16, `stride` bytes apart; the
+// staged rows may lie over them (a piece's step is written by the lanes that have
+// read it).
+struct StageArgs {
+  const uint8_t* rows;
+  uint8_t* frag;
+  float2* fx;
+  int64_t stride;
+  int n, K;
+};
+
+template <int GROUP>
+__device__ __forceinline__ void stage_rows(const StageArgs& a, int block, int blocks) {
+  const int steps = w4_steps(a.K), p = threadIdx.x & 15;
+  const int64_t total = static_cast<int64_t>(a.n) * steps, rb = w4_row_bytes(a.K);
+  for (int64_t i0 = static_cast<int64_t>(block) * 2 * kMoeWarps + (threadIdx.x >> 5) * 2; i0 < total;
+       i0 += static_cast<int64_t>(blocks) * 2 * kMoeWarps) {
+    const int64_t i = i0 + ((threadIdx.x >> 4) & 1), row = i / steps;
+    const int st = static_cast<int>(i - row * steps), k = st * kW4Step + 8 * p;
+    const bool exists = i < total;
+    float f[8];
+    unpack_piece(exists && k < a.K ? *reinterpret_cast<const uint4*>(a.rows + row * a.stride + 2 * k)
+                                   : make_uint4(0u, 0u, 0u, 0u),
+                 f);
+    w4_stage_piece<GROUP>(f, p, st, exists, a.frag + row * rb, a.fx + row * w4_fx_stride<GROUP>(a.K));
+  }
+}
+
+// The first launch of a call with more than 32 pairs: CTA 0 builds the map, the
+// others stage the tokens (4 bits).
+template <int FMT>
+__global__ void __launch_bounds__(kMoeThreads)
+    moe_plan_kernel(PairMap m, const int32_t* __restrict__ idx, int npairs, int E, int cap, StageArgs x,
+                    const uint32_t* err) {
+  extern __shared__ __align__(16) int at_all[];
+  griddep_wait();
+  griddep_launch_dependents();
+  if (err_set(err)) return;
+  if (blockIdx.x == 0) {
+    build_map(m, at_all, idx, npairs, E, cap);
+    return;
+  }
+  if constexpr (FMT != kFmtBf16) stage_rows<FMT>(x, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1);
+}
+
+// Stages the hidden rows between the two products (4 bits).
+template <int GROUP>
+__global__ void __launch_bounds__(kMoeThreads) moe_stage_kernel(StageArgs h, const uint32_t* err) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (err_set(err)) return;
+  stage_rows<GROUP>(h, blockIdx.x, gridDim.x);
 }
 
 // pair / k as a product: kinv = 2^18 / k + 1 is exact for pairs below 2^13 and k up to 2^5.
@@ -271,109 +341,170 @@ static_assert(kMaxPairs <= 8192 && kMaxTopk <= 32, "token_of");
 inline uint32_t token_factor(int k) { return (1u << 18) / static_cast<uint32_t>(k) + 1u; }
 __device__ __forceinline__ int token_of(uint32_t pair, uint32_t kinv) { return static_cast<int>((pair * kinv) >> 18); }
 
-// One of the two weight tensors of the experts.
-struct MoeWeights {
-  const uint8_t* data;          // [E, rows, K] bf16, or codes [E, rows, K/2]
-  const __nv_bfloat16* scales;  // [E, rows, K/group]
+// The operands of one product.  UP: w13 on the tokens, else w2 on the hidden rows.
+struct ProductArgs {
+  const uint8_t* weights;       // [E, rows, K] bf16, or codes [E, rows, K/2]
+  const __nv_bfloat16* scales;  // 4 bits: [E, rows, K/group]
   const uint8_t* zeros;
-  int rows, K;
+  const uint8_t* in;    // activation rows, bf16, `in_stride` bytes apart
+  const uint8_t* frag;  // 4 bits, not LOCAL: the same, staged
+  const float2* fx;
+  const int32_t* idx;
+  const float* gates;
+  uint8_t* out;  // UP: h, `out_stride` bytes a pair; else partial rows, binary32
+  PairMap map;   // not LOCAL
+  int64_t in_stride, out_stride;
+  int npairs, E, F, d, cap, WK;
+  uint32_t kinv;
 };
 
-template <int FMT>
-__device__ __forceinline__ Rows expert_rows(const MoeWeights& w, int e) {
-  const int64_t first = static_cast<int64_t>(e) * w.rows;
-  if constexpr (FMT == kFmtBf16) return Rows{w.data + first * w.K * 2, nullptr, nullptr};
-  const int64_t groups = first * (w.K / (FMT ? FMT : 1));
-  return Rows{w.data + first * (w.K / 2), w.scales + groups, w.zeros ? w.zeros + groups : nullptr};
-}
-
-// The units of a CTA: (entry, row block) pairs blockIdx.x, + gridDim.x, ... of
-// all entries and row blocks.  A row block is 8 / WK warps' worth of rows.
-//   UP    a warp's two row tiles are 16 rows of w1 and the same 16 of w3, so a and b
-//         of one (pair, f) meet in one thread: h[pair, f] = bf16(silu(a) * b).  h is
-//         rounded to bf16 once: it is the next product's matrix operand.
+// A warp's sums to memory.
+//   UP    its two row tiles are 16 rows of w1 and the same 16 of w3, so a and b of one
+//         (pair, f) meet in one thread: h[pair, f] = bf16(silu(a) * b).  h is rounded
+//         to bf16 once: it is the next product's matrix operand.
 //   else  32 rows of w2: part[pair, r] = gate * (w2[e, r] . h[pair])
-template <int FMT, int NT, bool UP>
-struct MoeWork {
-  const MoeWeights& w;
-  const PairMap& m;
-  const __nv_bfloat16* in;
-  const float* gates;
-  void* out;
-  uint32_t kinv;
-  int F, d, RG, blocks, total;
-
-  __device__ int units() const {
-    const int first = blockIdx.x, step = gridDim.x;
-    return first < total ? (total - first + step - 1) / step : 0;
-  }
-  __device__ int entry(int u) const { return static_cast<int>(blockIdx.x + u * gridDim.x) / blocks; }
-  __device__ int block(int u) const { return static_cast<int>(blockIdx.x + u * gridDim.x) % blocks; }
-  __device__ Rows rows(int u) const { return expert_rows<FMT>(w, m.entry_expert[entry(u)]); }
-  __device__ int row(int u, int rg, int lane, bool& active) const {
-    const int b = block(u) * RG + rg;
-    if (UP) {
-      active = b * 16 < F;
-      const int f = min(b * 16 + (lane & 15), F - 1);
-      return lane < 16 ? f : F + f;
-    }
-    active = b * 32 < d;
-    return min(b * 32 + lane, d - 1);
-  }
-  __device__ int count(int u) const { return m.entry_count[entry(u)]; }
-  __device__ const __nv_bfloat16* xrow(int u, int i) const {
-    const int p = m.pairs[m.entry_start[entry(u)] + i];
-    return UP ? in + static_cast<int64_t>(token_of(p, kinv)) * d : in + static_cast<int64_t>(p) * F;
-  }
-  __device__ void finish(int u, int rg, const float (&acc)[kRowTiles][NT][4]) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int e = entry(u), n_pairs = m.entry_count[e];
-    const uint16_t* pairs = m.pairs + m.entry_start[e];
-    const int b = block(u) * RG + rg;
+template <int NT, bool UP>
+__device__ __forceinline__ void store_block(const ProductArgs& a, const int* pairs, int count, int b,
+                                            const RowSums<NT>& acc) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = 8 * n + 2 * t + (i & 1), r = g + (i >> 1) * 8;
-        if (c >= n_pairs) continue;
-        const int64_t p = pairs[c];
-        if (UP) {
-          const int f = b * 16 + r;
-          const float a = acc[0][n][i], v = acc[1][n][i];
-          if (f < F) static_cast<__nv_bfloat16*>(out)[p * F + f] = __float2bfloat16_rn(a / (1.0f + expf(-a)) * v);
-        } else {
-          const float gate = gates[p];
+    for (int i = 0; i < 4; ++i) {
+      const int c = 8 * n + 2 * t + (i & 1), r = g + (i >> 1) * 8;
+      if (c >= count) continue;
+      const int64_t p = pairs[c];
+      if (UP) {
+        const int f = b * 16 + r;
+        const float u = acc[0][n][i], v = acc[1][n][i];
+        if (f < a.F)
+          reinterpret_cast<__nv_bfloat16*>(a.out + p * a.out_stride)[f] = __float2bfloat16_rn(u / (1.0f + expf(-u)) * v);
+      } else {
+        const float gate = a.gates[p];
 #pragma unroll
-          for (int tile = 0; tile < kRowTiles; ++tile) {
-            const int row = b * 32 + 16 * tile + r;
-            if (row < d) static_cast<float*>(out)[p * d + row] = gate * acc[tile][n][i];
-          }
+        for (int m = 0; m < kRowTiles; ++m) {
+          const int row = b * 32 + 16 * m + r;
+          if (row < a.d) reinterpret_cast<float*>(a.out + p * a.out_stride)[row] = gate * acc[m][n][i];
         }
       }
-  }
-};
-
-// CTAs an SM holds by registers.
-template <int FMT, int NT>
-constexpr int moe_ctas() {
-  return FMT == kFmtBf16 && NT == 1 ? 3 : 2;
+    }
 }
 
-template <int FMT, int NT, bool UP>
-__global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NT>())
-    moe_product_kernel(MoeWeights w, const __nv_bfloat16* __restrict__ in, const int32_t* __restrict__ idx,
-                       const float* __restrict__ gates, void* __restrict__ out, int npairs, uint32_t kinv, int E,
-                       int WK, const uint32_t* err) {
+// One unit: block `b` (16 rows of F, or 32 of d) of an entry's expert for a warp,
+// its `count` pairs as columns.
+template <int FMT, int NT, bool UP, bool LOCAL>
+__device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int* pairs, int count, int b, int rg,
+                                         int wk, uint8_t* smem, bool failed) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
+  const int K = UP ? a.d : a.F, rows = UP ? 2 * a.F : a.d, WK = a.WK;
+  const bool active = UP ? b * 16 < a.F : b * 32 < a.d;
+  // row i of the warp's 32; rows past the last one read the last one and store nothing
+  auto row = [&](int i) {
+    if (!UP) return min(b * 32 + i, a.d - 1);
+    const int f = min(b * 16 + (i & 15), a.F - 1);
+    return i < 16 ? f : a.F + f;
+  };
+  auto act = [&](int i) -> int64_t { return UP ? token_of(pairs[i], a.kinv) : pairs[i]; };
+  RowSums<NT> acc;
+  clear<NT>(acc);
+  if constexpr (FMT == kFmtBf16) {
+    const int steps = (K + kBfStep - 1) / kBfStep;
+    const uint8_t* base = a.weights + static_cast<int64_t>(e) * rows * K * 2 + 16 * (lane & 3);
+    const uint8_t* rp[kLaneRows];
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i) rp[i] = base + static_cast<int64_t>(row(8 * i + g)) * K * 2;
+    uint8_t* ring = smem + warp * kBfRing * kBfStepBytes;
+    uint8_t* xring = smem + kRowWarps * kBfRing * kBfStepBytes + wk * bf_x_bytes<NT>();
+    uint8_t* joins = smem + kRowWarps * kBfRing * kBfStepBytes + WK * bf_x_bytes<NT>();
+    auto xrow = [&](int i) { return reinterpret_cast<const __nv_bfloat16*>(a.in + act(i) * a.in_stride); };
+    row_dot_bf16<NT>(rp, active, xrow, count, K, steps * wk / WK, steps * (wk + 1) / WK, (steps + WK - 1) / WK, acc,
+                     ring, xring, rg * 32 + lane, 32 * (kRowWarps / WK));
+    if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
+  } else {
+    const int steps = w4_steps(K), fs = w4_fx_stride<FMT>(K);
+    const int64_t rb = w4_row_bytes(K), first = static_cast<int64_t>(e) * rows, groups = K / FMT;
+    const uint8_t* frag = a.frag;
+    const float2* fx = a.fx;
+    if constexpr (LOCAL) {  // the unit's rows, in shared memory
+      uint8_t* xs = smem + joins_bytes<NT>(WK);
+      float2* xf = reinterpret_cast<float2*>(xs + count * rb);
+      const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, total = count * steps;
+      __syncthreads();  // the last unit's rows have been read
+      for (int i0 = 0; i0 < total; i0 += 2 * kMoeWarps) {
+        const int i = i0 + hw, r = i / steps, st = i - r * steps, k = st * kW4Step + 8 * p;
+        float f[8];
+        unpack_piece(i < total && k < K ? *reinterpret_cast<const uint4*>(a.in + act(r) * a.in_stride + 2 * k)
+                                        : make_uint4(0u, 0u, 0u, 0u),
+                     f);
+        w4_stage_piece<FMT>(f, p, st, i < total, xs + r * rb, xf + r * fs);
+      }
+      __syncthreads();
+      frag = xs;
+      fx = xf;
+    }
+    if (active) {
+      const W4Rows w = w4_rows<FMT>(a.weights + first * (K / 2), a.scales + first * groups,
+                                    a.zeros ? a.zeros + first * groups : nullptr, K, row);
+      const W4Cols<NT> cols = w4_cols<FMT, NT>(frag, fx, K, count, [&](int i) { return LOCAL ? i : act(i); });
+      row_dot_w4<FMT, NT>(w, cols, K, steps * wk / WK, steps * (wk + 1) / WK, acc);
+      w4_unscale<NT>(acc);
+    }
+    if (WK > 1) join_slices<NT>(acc, smem, rg, wk, WK);
+  }
+  if (wk == 0 && active && !failed) store_block<NT, UP>(a, pairs, count, b, acc);
+}
+
+// CTAs an SM holds by registers.
+template <int FMT, int NTMAX>
+constexpr int moe_ctas() {
+  return NTMAX == 1 ? 3 : NTMAX == 2 || FMT == kFmtBf16 ? 2 : 1;
+}
+
+// Both products walk (entry, row block) units; a CTA takes units blockIdx.x,
+// + gridDim.x, ...  LOCAL: up to 32 pairs; every CTA builds the map itself (and
+// stages a unit's rows, 4 bits).
+template <int FMT, int NTMAX, bool UP, bool LOCAL>
+__global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
+    moe_product_kernel(const __grid_constant__ ProductArgs a, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int small_map[LOCAL ? 4 + 3 * 64 + 32 : 1];
   griddep_wait();
   griddep_launch_dependents();
-  if (err_set(err)) return;  // the word changes only between calls: uniform over the CTA
-  const PairMap m = build_pair_map(smem + rowdot_smem<FMT, NT>(WK), idx, npairs, E, 8 * NT);
-  const int RG = kMoeWarps / WK;
-  const int F = UP ? w.rows / 2 : w.K, d = UP ? w.K : w.rows;
-  const int blocks = UP ? (F + 16 * RG - 1) / (16 * RG) : (d + 32 * RG - 1) / (32 * RG);
-  const MoeWork<FMT, NT, UP> work{w, m, in, gates, out, kinv, F, d, RG, blocks, *m.total * blocks};
-  row_stream<FMT, NT>(work, w.K, WK, smem);
+  const bool failed = ld_volatile_u32(err) != 0u;  // looked at before anything is written
+  PairMap m = a.map;
+  if constexpr (LOCAL) {
+    m = pair_map_at(small_map, a.npairs, a.E, a.cap);
+    if (threadIdx.x < 32) build_small_map(m, a.idx, a.npairs, a.E, a.cap);
+    __syncthreads();
+  } else if (failed) {
+    return;  // there may be no map
+  }
+  const int warp = threadIdx.x >> 5;
+  const int wk = warp % a.WK, rg = warp / a.WK, RG = kMoeWarps / a.WK;
+  const int blocks = UP ? (a.F + 16 * RG - 1) / (16 * RG) : (a.d + 32 * RG - 1) / (32 * RG);
+  const int units = *m.total * blocks;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int entry = u / blocks, b = (u - entry * blocks) * RG + rg;
+    const int e = m.expert[entry], count = m.count[entry];
+    const int* pairs = m.pairs + m.start[entry];
+    if constexpr (NTMAX >= 4) {
+      if (count > 24) {
+        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        continue;
+      }
+      if (count > 16) {
+        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        continue;
+      }
+    }
+    if constexpr (NTMAX >= 2) {
+      if (count > 8) {
+        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        continue;
+      }
+    }
+    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+  }
 }
 
 // y[t] = the sum of the token's partial rows in the order of its choices;
@@ -403,57 +534,179 @@ __global__ void moe_combine_kernel(const float* __restrict__ part, const int32_t
   }
 }
 
-template <int FMT, int NT, bool UP>
-cudaError_t launch_product(const MoeWeights& w, const __nv_bfloat16* in, const int32_t* idx, const float* gates,
-                           void* out, int T, int k, int E, const DeviceInfo& dev, cudaStream_t s) {
-  const int npairs = T * k;
-  const int entries = npairs < E ? npairs : E;  // active experts, at most (more only where one fills several entries)
-  const int rows = UP ? w.rows / 2 : w.rows, step = UP ? 16 : 32;
-  const int steps = (w.K + rowdot_step<FMT>() - 1) / rowdot_step<FMT>();
-  constexpr int kMostWK = NT == 4 ? 2 : NT == 2 ? 4 : kMoeWarps;  // the slices' staged rows have to fit
-  const int64_t slots = static_cast<int64_t>(moe_ctas<FMT, NT>()) * dev.num_sms;
-  int WK = rowdot_split((rows + step - 1) / step, entries, steps, kMostWK, slots);
-  const size_t map = pair_map_bytes(npairs, E, 8 * NT);
-  while (WK > 1 && rowdot_smem<FMT, NT>(WK) + map > kMoeSmemMax) WK /= 2;
-  const size_t smem = rowdot_smem<FMT, NT>(WK) + map;
-  auto kern = moe_product_kernel<FMT, NT, UP>;
-  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), kMoeSmemMax, dev.device);
+template <int FMT, int NTMAX, bool UP, bool LOCAL>
+cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s) {
+  const int K = UP ? a.d : a.F;
+  const int blocks = UP ? (a.F + 15) / 16 : (a.d + 31) / 32;
+  const int entries = a.npairs < a.E ? a.npairs : a.E;  // active experts, at most
+  constexpr bool W4 = FMT != kFmtBf16;
+  const int steps = W4 ? w4_steps(K) : (K + kBfStep - 1) / kBfStep;
+  a.WK = rowdot_split(blocks, entries, steps, W4 ? 2 : 6, kMoeWarps / (W4 ? 1 : NTMAX), dev.num_sms);
+  int smem;
+  if constexpr (W4) smem = joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes<FMT>(a.cap, K)) : 0);
+  else smem = bf_smem<NTMAX>(a.WK);
+  auto kern = moe_product_kernel<FMT, NTMAX, UP, LOCAL>;
+  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
   if (e != cudaSuccess) return e;
-  // as many CTAs as the SM's shared memory and registers hold
-  int per_sm = static_cast<int>(kSmSmem / (smem + 1024));
-  per_sm = per_sm < 1 ? 1 : per_sm > moe_ctas<FMT, NT>() ? moe_ctas<FMT, NT>() : per_sm;
-  const int rg = kMoeWarps / WK;
-  const int64_t units = static_cast<int64_t>(max_entries(npairs, E, 8 * NT)) * ((rows + step * rg - 1) / (step * rg));
+  const int RG = kMoeWarps / a.WK;
+  const int64_t units =
+      static_cast<int64_t>(max_entries(a.npairs, a.E, a.cap)) * (UP ? (a.F + 16 * RG - 1) / (16 * RG)
+                                                                    : (a.d + 32 * RG - 1) / (32 * RG));
+  // as many CTAs as the SM's shared memory and registers hold at a time
+  int per_sm = 228 * 1024 / (smem + 1024);
+  per_sm = per_sm < 1 ? 1 : per_sm > moe_ctas<FMT, NTMAX>() ? moe_ctas<FMT, NTMAX>() : per_sm;
   int64_t grid = static_cast<int64_t>(per_sm) * dev.num_sms;
   if (grid > units) grid = units;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kMoeThreads), smem, s, w, in, idx, gates, out,
-                    npairs, token_factor(k), E, WK, static_cast<const uint32_t*>(dev.err));
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kMoeThreads), smem, s, a,
+                    static_cast<const uint32_t*>(dev.err));
 }
+
+// Shared memory of the staged rows of a unit that lets three CTAs share an SM.
+constexpr int64_t kLocalBytes = 56 * 1024;
 
 template <int FMT, bool UP>
-cudaError_t launch_product_nt(const MoeWeights& w, const __nv_bfloat16* in, const int32_t* idx, const float* gates,
-                              void* out, int T, int k, int E, const DeviceInfo& dev, cudaStream_t s) {
-  // an expert gets T*k/E of the pairs on average and at most T distinct ones
-  const int typical = (2 * T * k + E - 1) / E;
-  const int most = typical < T ? typical : T;
-  if (most <= 8) return launch_product<FMT, 1, UP>(w, in, idx, gates, out, T, k, E, dev, s);
-  if (most <= 16) return launch_product<FMT, 2, UP>(w, in, idx, gates, out, T, k, E, dev, s);
-  return launch_product<FMT, 4, UP>(w, in, idx, gates, out, T, k, E, dev, s);
+cudaError_t launch_product_nt(const ProductArgs& a, bool local, int ntmax, const DeviceInfo& dev, cudaStream_t s) {
+  if (local) return launch_product<FMT, 1, UP, true>(a, dev, s);
+  if (ntmax == 1) return launch_product<FMT, 1, UP, false>(a, dev, s);
+  if (ntmax == 2) return launch_product<FMT, 2, UP, false>(a, dev, s);
+  return launch_product<FMT, 4, UP, false>(a, dev, s);
 }
 
-template <bool UP>
-cudaError_t launch_product_fmt(int fmt, const MoeWeights& w, const __nv_bfloat16* in, const int32_t* idx,
-                               const float* gates, void* out, int T, int k, int E, const DeviceInfo& dev,
-                               cudaStream_t s) {
-  switch (fmt) {
-    case kFmtBf16: return launch_product_nt<kFmtBf16, UP>(w, in, idx, gates, out, T, k, E, dev, s);
-    case 32: return launch_product_nt<32, UP>(w, in, idx, gates, out, T, k, E, dev, s);
-    case 64: return launch_product_nt<64, UP>(w, in, idx, gates, out, T, k, E, dev, s);
-    default: return launch_product_nt<128, UP>(w, in, idx, gates, out, T, k, E, dev, s);
+// Scratch of a call: the pair map, hidden rows and partial rows of every pair, and
+// (4 bits) the staged tokens and the {factor, sum} of the hidden rows.
+struct MoeScratch {
+  int64_t map, h, part, xfrag, xfx, hfx, total;
+  int64_t h_stride;
+};
+MoeScratch moe_scratch(int T, int k, int E, int d, int F, int group) {
+  auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
+  const int64_t pairs = static_cast<int64_t>(T) * k;
+  MoeScratch m{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up(bytes);
+    return here;
+  };
+  m.h_stride = group ? w4_row_bytes(F) : 2 * static_cast<int64_t>(F);
+  const int cap = T < 8 ? (T < 1 ? 1 : T) : 8;  // the fewest pairs of an entry that a call uses
+  m.map = take(4 * static_cast<int64_t>(pair_map_ints(static_cast<int>(pairs), E, cap)));
+  m.h = take(pairs * m.h_stride);
+  m.part = take(pairs * d * 4);
+  if (group) {
+    const int64_t groups_d = static_cast<int64_t>(w4_steps(d)) * (kW4Step / group);
+    const int64_t groups_f = static_cast<int64_t>(w4_steps(F)) * (kW4Step / group);
+    m.xfrag = take(T * w4_row_bytes(d));
+    m.xfx = take(T * groups_d * 8);
+    m.hfx = take(pairs * groups_f * 8);
   }
+  m.total = at;
+  return m;
+}
+
+template <int FMT>
+cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s, MoeTrace* trace) {
+  constexpr bool W4 = FMT != kFmtBf16;
+  const int npairs = c.T * c.k;
+  const MoeScratch sc = moe_scratch(c.T, c.k, c.E, c.d, c.F, FMT);
+  uint8_t* base = static_cast<uint8_t*>(c.scratch);
+  // an expert gets T*k/E of the pairs on average and at most T distinct ones
+  const int typical = (2 * npairs + c.E - 1) / c.E, most = typical < c.T ? typical : c.T;
+  int ntmax = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+  const int cap = c.T < 8 * ntmax ? c.T : 8 * ntmax;
+  bool local = npairs <= 32 && cap <= 8;
+  if constexpr (W4)
+    local = local && w4_staged_bytes<FMT>(cap, c.d) <= kLocalBytes && w4_staged_bytes<FMT>(cap, c.F) <= kLocalBytes;
+  if (local) ntmax = 1;
+  ProductArgs a{};
+  a.idx = static_cast<const int32_t*>(c.idx);
+  a.gates = static_cast<const float*>(c.gates);
+  a.npairs = npairs;
+  a.E = c.E;
+  a.F = c.F;
+  a.d = c.d;
+  a.cap = cap;
+  a.kinv = token_factor(c.k);
+  a.map = pair_map_at(reinterpret_cast<int*>(base + sc.map), npairs, c.E, cap);
+  const uint32_t* err = dev.err;
+  cudaError_t e;
+  if (!local) {
+    trace->begin("moe_plan", 0.0, 4.0 * npairs);
+    const StageArgs x{static_cast<const uint8_t*>(c.x), base + sc.xfrag, reinterpret_cast<float2*>(base + sc.xfx),
+                      2 * static_cast<int64_t>(c.d), c.T, c.d};
+    const int64_t items = W4 ? (static_cast<int64_t>(c.T) * w4_steps(c.d) + 15) / 16 : 0;
+    const int grid = 1 + static_cast<int>(items < 4 * dev.num_sms ? items : 4 * dev.num_sms);
+    e = launch_pdl(moe_plan_kernel<FMT>, dim3(grid), dim3(kMoeThreads), kMoeWarps * c.E * sizeof(int), s, a.map, a.idx,
+                   npairs, c.E, cap, x, err);
+    trace->end();
+    if (e != cudaSuccess) return e;
+  }
+  const double df = static_cast<double>(c.d) * c.F, n_exp = npairs < c.E ? npairs : c.E;
+  const double wb = W4 ? 0.5 + (c.z13 ? 3.0 : 2.0) / (W4 ? FMT : 1) : 2.0;  // bytes of a weight
+  // up
+  a.weights = static_cast<const uint8_t*>(c.w13);
+  a.scales = static_cast<const __nv_bfloat16*>(c.s13);
+  a.zeros = static_cast<const uint8_t*>(c.z13);
+  a.in = static_cast<const uint8_t*>(c.x);
+  a.in_stride = 2 * static_cast<int64_t>(c.d);
+  a.frag = base + sc.xfrag;
+  a.fx = reinterpret_cast<const float2*>(base + sc.xfx);
+  a.out = base + sc.h;
+  a.out_stride = sc.h_stride;
+  trace->begin("moe_up", 4.0 * npairs * df, n_exp * 2.0 * df * wb + 2.0 * c.T * c.d + 2.0 * npairs * c.F);
+  e = launch_product_nt<FMT, true>(a, local, ntmax, dev, s);
+  trace->end();
+  if (e != cudaSuccess) return e;
+  if constexpr (W4) {
+    if (!local) {
+      trace->begin("moe_stage", 0.0, 4.0 * npairs * c.F);
+      const StageArgs h{base + sc.h, base + sc.h, reinterpret_cast<float2*>(base + sc.hfx), sc.h_stride, npairs, c.F};
+      const int64_t items = (static_cast<int64_t>(npairs) * w4_steps(c.F) + 15) / 16;
+      const int grid = static_cast<int>(items < 8 * dev.num_sms ? items : 8 * dev.num_sms);
+      e = launch_pdl(moe_stage_kernel<FMT>, dim3(grid), dim3(kMoeThreads), 0, s, h, err);
+      trace->end();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  // down
+  a.weights = static_cast<const uint8_t*>(c.w2);
+  a.scales = static_cast<const __nv_bfloat16*>(c.s2);
+  a.zeros = static_cast<const uint8_t*>(c.z2);
+  a.in = base + sc.h;
+  a.in_stride = sc.h_stride;
+  a.frag = base + sc.h;
+  a.fx = reinterpret_cast<const float2*>(base + sc.hfx);
+  a.out = base + sc.part;
+  a.out_stride = 4 * static_cast<int64_t>(c.d);
+  trace->begin("moe_down", 2.0 * npairs * df, n_exp * df * wb + 2.0 * npairs * c.F + 4.0 * npairs * c.d);
+  e = launch_product_nt<FMT, false>(a, local, ntmax, dev, s);
+  trace->end();
+  if (e != cudaSuccess) return e;
+  const int64_t n = static_cast<int64_t>(c.T) * (c.d / 4);
+  int64_t blocks = (n + 255) / 256;
+  if (blocks > 8 * dev.num_sms) blocks = 8 * dev.num_sms;
+  trace->begin("moe_combine", 0.0, 4.0 * npairs * c.d + 2.0 * c.T * c.d);
+  e = launch_pdl(moe_combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                 reinterpret_cast<const float*>(base + sc.part), a.idx, static_cast<__nv_bfloat16*>(c.y), c.T, c.k,
+                 c.E, c.d, err);
+  trace->end();
+  return e;
 }
 
 }  // namespace
+
+size_t moe_scratch_bytes(int T, int k, int E, int d, int F, int group) {
+  return static_cast<size_t>(moe_scratch(T, k, E, d, F, group).total);
+}
+
+cudaError_t launch_moe_swiglu(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s, MoeTrace* trace) {
+  switch (c.group) {
+    case 0: return moe_launches<kFmtBf16>(c, dev, s, trace);
+    case 32: return moe_launches<32>(c, dev, s, trace);
+    case 64: return moe_launches<64>(c, dev, s, trace);
+    default: return moe_launches<128>(c, dev, s, trace);
+  }
+}
 
 int moe_max_pairs() { return kMaxPairs; }
 int moe_max_experts() { return kMaxExperts; }
@@ -470,33 +723,6 @@ cudaError_t launch_moe_topk(const float* logits, void* idx, void* gates, int T, 
                             bool renorm, float scale, const DeviceInfo& dev, cudaStream_t s) {
   return launch_pdl(moe_topk_kernel, dim3((T + kTopkWarps - 1) / kTopkWarps), dim3(kTopkWarps * 32), 0, s, logits,
                     static_cast<int32_t*>(idx), static_cast<float*>(gates), T, E, k, sigmoid, renorm, scale,
-                    static_cast<const uint32_t*>(dev.err));
-}
-
-cudaError_t launch_moe_up(const MoeSource& w13, const void* x, const void* idx, void* h, int T, int k, int E, int d,
-                          int F, const DeviceInfo& dev, cudaStream_t s) {
-  const MoeWeights w{static_cast<const uint8_t*>(w13.data), static_cast<const __nv_bfloat16*>(w13.scales),
-                     static_cast<const uint8_t*>(w13.zeros), 2 * F, d};
-  return launch_product_fmt<true>(w13.group, w, static_cast<const __nv_bfloat16*>(x),
-                                  static_cast<const int32_t*>(idx), nullptr, h, T, k, E, dev, s);
-}
-
-cudaError_t launch_moe_down(const MoeSource& w2, const void* h, const void* idx, const void* gates, void* part, int T,
-                            int k, int E, int d, int F, const DeviceInfo& dev, cudaStream_t s) {
-  const MoeWeights w{static_cast<const uint8_t*>(w2.data), static_cast<const __nv_bfloat16*>(w2.scales),
-                     static_cast<const uint8_t*>(w2.zeros), d, F};
-  return launch_product_fmt<false>(w2.group, w, static_cast<const __nv_bfloat16*>(h),
-                                   static_cast<const int32_t*>(idx), static_cast<const float*>(gates), part, T, k, E,
-                                   dev, s);
-}
-
-cudaError_t launch_moe_combine(const float* part, const void* idx, void* y, int T, int k, int E, int d,
-                               const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t n = static_cast<int64_t>(T) * (d / 4);
-  int64_t blocks = (n + 255) / 256;
-  if (blocks > 8 * dev.num_sms) blocks = 8 * dev.num_sms;
-  return launch_pdl(moe_combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, part,
-                    static_cast<const int32_t*>(idx), static_cast<__nv_bfloat16*>(y), T, k, E, d,
                     static_cast<const uint32_t*>(dev.err));
 }
 

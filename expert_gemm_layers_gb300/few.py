@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._lib import DG_MOE_RENORM, DG_MOE_SIGMOID, MoEShape, check, load
+from ._lib import DG_ERROR_BLOCK_BYTES, DG_MOE_RENORM, DG_MOE_SIGMOID, MoEShape, check, load
 from .ops import _need, _stream, alloc_workspace, error_block
 
 __all__ = ["w4_quantize", "w4_dequantize", "w4_linear", "moe_route", "moe_swiglu", "moe_swiglu_w4", "moe_layer"]
@@ -30,6 +30,25 @@ def _launch(fn, dev: torch.device, *args) -> None:
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+_scratch_cache: dict = {}
+
+
+def _scratch(dev: torch.device, nbytes: int) -> torch.Tensor:
+    """The workspace this module gives calls that bring none: one per (device,
+    current stream), grown as needed, its error block zeroed when it is made.
+    A captured call gets one of its own, in the graph's memory, so that graphs
+    captured on one stream do not share it."""
+    if nbytes <= DG_ERROR_BLOCK_BYTES:
+        return error_block(dev)
+    if torch.cuda.is_current_stream_capturing():
+        return alloc_workspace(nbytes, dev)
+    key = (dev.index, _stream(dev))
+    ws = _scratch_cache.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _scratch_cache[key] = alloc_workspace(nbytes, dev)
+    return ws
 
 
 def _need_workspace(ws: torch.Tensor, nbytes: int, dev: torch.device) -> None:
@@ -93,7 +112,8 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
 
     Sums in binary32, one rounding to bf16.  For long prompts dequantise once
     and use tp_linear.  `ws` holds the call's error block (default: this
-    stream's error_block())."""
+    stream's own), and scratch where there are more than few short rows
+    (dg_w4_linear_workspace_bytes)."""
     lib = load()
     in_f, dev = x.shape[-1], x.device
     _need(x, "x", torch.bfloat16)
@@ -105,9 +125,10 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
         out = torch.empty((*x.shape[:-1], out_f), dtype=torch.bfloat16, device=dev)
     else:
         _need(out, "out", torch.bfloat16, (*x.shape[:-1], out_f), dev)
+    rows = x.numel() // in_f if in_f else 0
     if ws is None:
-        ws = error_block(dev)
-    _launch(lib.dg_w4_linear, dev, x.numel() // in_f if in_f else 0, in_f, out_f, group, _p(x), _p(codes), _p(scales), _p(zeros),
+        ws = _scratch(dev, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f))
+    _launch(lib.dg_w4_linear, dev, rows, in_f, out_f, group, _p(x), _p(codes), _p(scales), _p(zeros),
             _p(bias), _p(out), _p(ws), ws.numel())
     return out
 
@@ -136,7 +157,7 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     gates = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     nbytes = lib.dg_moe_route_workspace_bytes(T, d, E, top_k)
     if workspace is None:
-        workspace = alloc_workspace(nbytes, dev)
+        workspace = _scratch(dev, nbytes)
     else:
         _need_workspace(workspace, nbytes, dev)
     _launch(lib.dg_moe_route, dev, T, d, E, top_k, flags, float(scale), _p(x), _p(w_router), _p(idx), _p(gates),
@@ -144,7 +165,7 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     return idx, gates
 
 
-def _moe_args(x, idx, gates, workspace, out, F: int, E: int):
+def _moe_args(x, idx, gates, workspace, out, F: int, E: int, group: int):
     """Checks the tensors both weight formats share; returns (shape, workspace, out)."""
     _need(x, "x", torch.bfloat16)
     T, d = x.shape
@@ -153,9 +174,9 @@ def _moe_args(x, idx, gates, workspace, out, F: int, E: int):
     _need(idx, "idx", torch.int32, (T, k), dev)
     _need(gates, "gates", torch.float32, (T, k), dev)
     sh = MoEShape(T, d, F, E, k)
-    nbytes = load().dg_moe_swiglu_workspace_bytes(ctypes.byref(sh))
+    nbytes = load().dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), group)
     if workspace is None:
-        workspace = alloc_workspace(nbytes, dev)
+        workspace = _scratch(dev, nbytes)
     elif nbytes:
         _need_workspace(workspace, nbytes, dev)
     if out is None:
@@ -172,14 +193,14 @@ def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: tor
     x [T, d], w13 [E, 2F, d] (rows [w1; w3]), w2 [E, d, F] bf16; idx [T, k]
     int32 and gates [T, k] binary32 as moe_route returns them (an idx outside
     [0, E) is no expert and adds nothing).  T * k <= 8192.  `workspace`
-    (dg_moe_swiglu_workspace_bytes, its error block zeroed) saves its
-    allocation on every call."""
+    (dg_moe_swiglu_workspace_bytes, its error block zeroed; default: this
+    stream's own) is not shared by calls that run at the same time."""
     lib = load()
     d = x.shape[-1]
     E, F = w13.shape[0], w13.shape[1] // 2
     _need(w13, "w13", torch.bfloat16, (E, 2 * F, d), x.device)
     _need(w2, "w2", torch.bfloat16, (E, d, F), x.device)
-    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E)
+    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, 0)
     _launch(lib.dg_moe_swiglu, x.device, ctypes.byref(sh), _p(x), _p(idx), _p(gates), _p(w13), _p(w2), _p(out),
             _p(workspace), workspace.numel())
     return out
@@ -196,7 +217,7 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
     group = _need_w4(c13, s13, z13, (E, 2 * F), d, dev, "w13 ")
     if _need_w4(c2, s2, z2, (E, d), F, dev, "w2 ") != group:
         raise ValueError("w13 and w2 must have the same group size")
-    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E)
+    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, group)
     _launch(lib.dg_moe_swiglu_w4, dev, ctypes.byref(sh), group, _p(x), _p(idx), _p(gates), _p(c13), _p(s13), _p(z13),
             _p(c2), _p(s2), _p(z2), _p(out), _p(workspace), workspace.numel())
     return out

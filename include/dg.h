@@ -400,7 +400,10 @@ dg_status dg_tp_linear_bwd(int64_t rows, int64_t in_features, int64_t out_featur
  * W is read once per 32 rows.  For long prompts dequantise once and use
  * dg_tp_linear_fwd.  Any out_features >= 1; in_features % group == 0;
  * rows >= 0 (0 = nothing to do), at most 65535 * 32.
- * ws: the error block only (dg_w4_linear_workspace_bytes = 256 bytes).
+ * ws (dg_w4_linear_workspace_bytes): the error block, then, for all but few
+ * short rows, scratch for x in the form the kernel reads; nothing in it outlives
+ * the call.
+ * An activation that is not finite makes its row of y not finite.
  * These calls have no backward: the codes are not trained.
  * ------------------------------------------------------------------------ */
 dg_status dg_w4_quantize(int64_t rows, int64_t K, int32_t group, const void* weight, void* codes, void* scales,
@@ -461,7 +464,8 @@ size_t dg_moe_route_workspace_bytes(int64_t T, int64_t d, int32_t E, int32_t k);
 dg_status dg_moe_route(int64_t T, int64_t d, int32_t E, int32_t k, uint32_t flags, float scale, const void* x,
                        const void* w_router, void* idx, void* gates, void* ws, size_t ws_bytes, void* stream);
 
-size_t dg_moe_swiglu_workspace_bytes(const dg_moe_shape* shape);
+/* group: 0 for dg_moe_swiglu, else that of dg_moe_swiglu_w4.  0 for invalid arguments. */
+size_t dg_moe_swiglu_workspace_bytes(const dg_moe_shape* shape, int32_t group);
 
 dg_status dg_moe_swiglu(const dg_moe_shape* shape, const void* x, const void* idx, const void* gates,
                         const void* w13, const void* w2, void* y, void* ws, size_t ws_bytes, void* stream);

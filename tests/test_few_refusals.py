@@ -98,9 +98,11 @@ def test_moe_swiglu(lib, mem):
     assert call(ws=None) == WORKSPACE and call(n=256) == WORKSPACE
     assert call(T=0, x=None, i=None, g=None, a=None, b=None, y=None, ws=None) == OK
     sh = MoEShape(2, 64, 32, 4, 2)
-    assert lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh)) >= 256 + 4 * 32 * 2 + 4 * 64 * 4
+    for group in (0, 32):
+        assert lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), group) >= 256 + 4 * 32 * 2 + 4 * 64 * 4
+    assert lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), 16) == 0
     sh = MoEShape(2, 60, 32, 4, 2)
-    assert lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh)) == 0
+    assert lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), 0) == 0
 
 
 def test_moe_swiglu_w4(lib, mem):

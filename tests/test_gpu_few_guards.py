@@ -34,7 +34,8 @@ def test_w4_linear_writes_only_y(rows, K, N, group):
     g = Guarded()
     w, _ = w4_weight((), N, K, group, True, 1)
     y = g.tensor((rows, N), BF16)
-    dg.w4_linear(randn((rows, K), 2).to(DEV), *w, out=y, ws=g.workspace(256))
+    need = _lib.load().dg_w4_linear_workspace_bytes(rows, K, N)
+    dg.w4_linear(randn((rows, K), 2).to(DEV), *w, out=y, ws=g.workspace(need))
     g.check(f"w4_linear {rows, K, N, group}")
     assert torch.isfinite(y.float()).all()
 
@@ -58,7 +59,7 @@ def test_moe_swiglu_writes_only_y_and_its_workspace(T, d, F, E, k, group):
     idx, gates = (t.to(DEV) for t in routing(T, E, k, 3))
     x = randn((T, d), 1).to(DEV)
     sh = _lib.MoEShape(T, d, F, E, k)
-    ws = g.workspace(lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh)))
+    ws = g.workspace(lib.dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), group))
     y = g.tensor((T, d), BF16)
     if group:
         w13, w2 = w4_weight((E,), 2 * F, d, group, True, 4)[0], w4_weight((E,), d, F, group, True, 5)[0]
