@@ -282,32 +282,20 @@ __device__ __forceinline__ void build_map(const PairMap& m, int* at_all, const i
   }
 }
 
-// Rows to stage for 4-bit products: [rows][K] bf16, `stride` bytes apart; the
-// staged rows may lie over them (a piece's step is written by the lanes that have
-// read it).
+// Rows to stage for 4-bit products, a CTA a row: [n][K] bf16, `stride` bytes apart;
+// the staged rows may lie over them.
 struct StageArgs {
   const uint8_t* rows;
-  uint8_t* frag;
-  float2* fx;
+  Staged out;
   int64_t stride;
   int n, K;
 };
 
 template <int GROUP>
-__device__ __forceinline__ void stage_rows(const StageArgs& a, int block, int blocks) {
-  const int steps = w4_steps(a.K), p = threadIdx.x & 15;
-  const int64_t total = static_cast<int64_t>(a.n) * steps, rb = w4_row_bytes(a.K);
-  for (int64_t i0 = static_cast<int64_t>(block) * 2 * kMoeWarps + (threadIdx.x >> 5) * 2; i0 < total;
-       i0 += static_cast<int64_t>(blocks) * 2 * kMoeWarps) {
-    const int64_t i = i0 + ((threadIdx.x >> 4) & 1), row = i / steps;
-    const int st = static_cast<int>(i - row * steps), k = st * kW4Step + 8 * p;
-    const bool exists = i < total;
-    float f[8];
-    unpack_piece(exists && k < a.K ? *reinterpret_cast<const uint4*>(a.rows + row * a.stride + 2 * k)
-                                   : make_uint4(0u, 0u, 0u, 0u),
-                 f);
-    w4_stage_piece<GROUP>(f, p, st, exists, a.frag + row * rb, a.fx + row * w4_fx_stride<GROUP>(a.K));
-  }
+__device__ __forceinline__ void stage_rows(const StageArgs& a, int block, int blocks, uint32_t* shared_top) {
+  for (int r = block; r < a.n; r += blocks)
+    w4_stage_row<GROUP>(a.rows + r * a.stride, a.K, a.out.frag + r * w4_row_bytes(a.K),
+                        a.out.sums + static_cast<int64_t>(r) * w4_row_sums(a.K, GROUP), a.out.factor + r, shared_top);
 }
 
 // The first launch of a call with more than 32 pairs: CTA 0 builds the map, the
@@ -317,23 +305,28 @@ __global__ void __launch_bounds__(kMoeThreads)
     moe_plan_kernel(PairMap m, const int32_t* __restrict__ idx, int npairs, int E, int cap, StageArgs x,
                     const uint32_t* err) {
   extern __shared__ __align__(16) int at_all[];
+  __shared__ uint32_t top;
+  if (threadIdx.x == 0) top = 0u;
   griddep_wait();
-  griddep_launch_dependents();
   if (err_set(err)) return;
+  __syncthreads();
   if (blockIdx.x == 0) {
     build_map(m, at_all, idx, npairs, E, cap);
     return;
   }
-  if constexpr (FMT != kFmtBf16) stage_rows<FMT>(x, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1);
+  if constexpr (FMT != kFmtBf16)
+    stage_rows<FMT>(x, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1, &top);
 }
 
 // Stages the hidden rows between the two products (4 bits).
 template <int GROUP>
 __global__ void __launch_bounds__(kMoeThreads) moe_stage_kernel(StageArgs h, const uint32_t* err) {
+  __shared__ uint32_t top;
+  if (threadIdx.x == 0) top = 0u;
   griddep_wait();
-  griddep_launch_dependents();
   if (err_set(err)) return;
-  stage_rows<GROUP>(h, blockIdx.x, gridDim.x);
+  __syncthreads();
+  stage_rows<GROUP>(h, blockIdx.x, gridDim.x, &top);
 }
 
 // pair / k as a product: kinv = 2^18 / k + 1 is exact for pairs below 2^13 and k up to 2^5.
@@ -347,8 +340,7 @@ struct ProductArgs {
   const __nv_bfloat16* scales;  // 4 bits: [E, rows, K/group]
   const uint8_t* zeros;
   const uint8_t* in;    // activation rows, bf16, `in_stride` bytes apart
-  const uint8_t* frag;  // 4 bits, not LOCAL: the same, staged
-  const float2* fx;
+  Staged staged;        // 4 bits, not LOCAL: the same, staged
   const int32_t* idx;
   const float* gates;
   uint8_t* out;  // UP: h, `out_stride` bytes a pair; else partial rows, binary32
@@ -394,7 +386,7 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const int* pai
 // its `count` pairs as columns.
 template <int FMT, int NT, bool UP, bool LOCAL>
 __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int* pairs, int count, int b, int rg,
-                                         int wk, uint8_t* smem, bool failed) {
+                                         int wk, uint8_t* smem, uint32_t* tops, bool failed) {
   const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
   const int K = UP ? a.d : a.F, rows = UP ? 2 * a.F : a.d, WK = a.WK;
   const bool active = UP ? b * 16 < a.F : b * 32 < a.d;
@@ -421,35 +413,25 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
                      ring, xring, rg * 32 + lane, 32 * (kRowWarps / WK));
     if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   } else {
-    const int steps = w4_steps(K), fs = w4_fx_stride<FMT>(K);
-    const int64_t rb = w4_row_bytes(K), first = static_cast<int64_t>(e) * rows, groups = K / FMT;
-    const uint8_t* frag = a.frag;
-    const float2* fx = a.fx;
+    const int steps = w4_steps(K);
+    const int64_t first = static_cast<int64_t>(e) * rows, groups = K / FMT;
+    uint8_t* joins = smem + w4_ring_bytes<FMT>();
+    W4Stream<FMT> stream{w4_rows<FMT>(a.weights + first * (K / 2), a.scales + first * groups,
+                                      a.zeros ? a.zeros + first * groups : nullptr, K, row),
+                         smem + warp * w4_warp_bytes<FMT>(), K, steps * wk / WK, steps * (wk + 1) / WK};
+    if (active) stream.start();
+    Staged in = a.staged;
     if constexpr (LOCAL) {  // the unit's rows, in shared memory
-      uint8_t* xs = smem + joins_bytes<NT>(WK);
-      float2* xf = reinterpret_cast<float2*>(xs + count * rb);
-      const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, total = count * steps;
+      in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, FMT);
       __syncthreads();  // the last unit's rows have been read
-      for (int i0 = 0; i0 < total; i0 += 2 * kMoeWarps) {
-        const int i = i0 + hw, r = i / steps, st = i - r * steps, k = st * kW4Step + 8 * p;
-        float f[8];
-        unpack_piece(i < total && k < K ? *reinterpret_cast<const uint4*>(a.in + act(r) * a.in_stride + 2 * k)
-                                        : make_uint4(0u, 0u, 0u, 0u),
-                     f);
-        w4_stage_piece<FMT>(f, p, st, i < total, xs + r * rb, xf + r * fs);
-      }
-      __syncthreads();
-      frag = xs;
-      fx = xf;
+      w4_stage_local<FMT>(in, count, K, tops, [&](int i) { return a.in + act(i) * a.in_stride; });
     }
+    auto column = [&](int i) { return LOCAL ? i : act(i); };
     if (active) {
-      const W4Rows w = w4_rows<FMT>(a.weights + first * (K / 2), a.scales + first * groups,
-                                    a.zeros ? a.zeros + first * groups : nullptr, K, row);
-      const W4Cols<NT> cols = w4_cols<FMT, NT>(frag, fx, K, count, [&](int i) { return LOCAL ? i : act(i); });
-      row_dot_w4<FMT, NT>(w, cols, K, steps * wk / WK, steps * (wk + 1) / WK, acc);
-      w4_unscale<NT>(acc);
+      stream.template run<NT>(w4_cols<FMT, NT>(in, K, count, column), acc);
+      w4_unscale<NT>(acc, in.factor, count, column);
     }
-    if (WK > 1) join_slices<NT>(acc, smem, rg, wk, WK);
+    if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   }
   if (wk == 0 && active && !failed) store_block<NT, UP>(a, pairs, count, b, acc);
 }
@@ -457,7 +439,7 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
 // CTAs an SM holds by registers.
 template <int FMT, int NTMAX>
 constexpr int moe_ctas() {
-  return NTMAX == 1 ? 3 : NTMAX == 2 || FMT == kFmtBf16 ? 2 : 1;
+  return NTMAX == 1 ? 3 : 2;
 }
 
 // Both products walk (entry, row block) units; a CTA takes units blockIdx.x,
@@ -468,8 +450,8 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
     moe_product_kernel(const __grid_constant__ ProductArgs a, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int small_map[LOCAL ? 4 + 3 * 64 + 32 : 1];
+  __shared__ uint32_t tops[8];
   griddep_wait();
-  griddep_launch_dependents();
   const bool failed = ld_volatile_u32(err) != 0u;  // looked at before anything is written
   PairMap m = a.map;
   if constexpr (LOCAL) {
@@ -489,21 +471,21 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
     const int* pairs = m.pairs + m.start[entry];
     if constexpr (NTMAX >= 4) {
       if (count > 24) {
-        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
         continue;
       }
       if (count > 16) {
-        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
         continue;
       }
     }
     if constexpr (NTMAX >= 2) {
       if (count > 8) {
-        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
         continue;
       }
     }
-    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
   }
 }
 
@@ -512,7 +494,6 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
 __global__ void moe_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ idx,
                                    __nv_bfloat16* __restrict__ y, int T, int k, int E, int d, const uint32_t* err) {
   griddep_wait();
-  griddep_launch_dependents();
   if (err_set(err)) return;
   const int d4 = d / 4;
   const int64_t n = static_cast<int64_t>(T) * d4;
@@ -541,9 +522,11 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
   const int entries = a.npairs < a.E ? a.npairs : a.E;  // active experts, at most
   constexpr bool W4 = FMT != kFmtBf16;
   const int steps = W4 ? w4_steps(K) : (K + kBfStep - 1) / kBfStep;
-  a.WK = rowdot_split(blocks, entries, steps, W4 ? 2 : 6, kMoeWarps / (W4 ? 1 : NTMAX), dev.num_sms);
+  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX>(), W4 ? (NTMAX == 1 ? kMoeWarps : 2) : kMoeWarps / NTMAX,
+                      dev.num_sms);
   int smem;
-  if constexpr (W4) smem = joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes<FMT>(a.cap, K)) : 0);
+  if constexpr (W4)
+    smem = w4_ring_bytes<FMT>() + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT)) : 0);
   else smem = bf_smem<NTMAX>(a.WK);
   auto kern = moe_product_kernel<FMT, NTMAX, UP, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
@@ -562,7 +545,7 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
 }
 
 // Shared memory of the staged rows of a unit that lets three CTAs share an SM.
-constexpr int64_t kLocalBytes = 56 * 1024;
+constexpr int64_t kLocalBytes = 24 * 1024;
 
 template <int FMT, bool UP>
 cudaError_t launch_product_nt(const ProductArgs& a, bool local, int ntmax, const DeviceInfo& dev, cudaStream_t s) {
@@ -573,9 +556,10 @@ cudaError_t launch_product_nt(const ProductArgs& a, bool local, int ntmax, const
 }
 
 // Scratch of a call: the pair map, hidden rows and partial rows of every pair, and
-// (4 bits) the staged tokens and the {factor, sum} of the hidden rows.
+// (4 bits) the staged tokens and the sums and factors of the hidden rows (which are
+// staged in place).
 struct MoeScratch {
-  int64_t map, h, part, xfrag, xfx, hfx, total;
+  int64_t map, h, part, x, hsums, hfactor, total;
   int64_t h_stride;
 };
 MoeScratch moe_scratch(int T, int k, int E, int d, int F, int group) {
@@ -594,11 +578,9 @@ MoeScratch moe_scratch(int T, int k, int E, int d, int F, int group) {
   m.h = take(pairs * m.h_stride);
   m.part = take(pairs * d * 4);
   if (group) {
-    const int64_t groups_d = static_cast<int64_t>(w4_steps(d)) * (kW4Step / group);
-    const int64_t groups_f = static_cast<int64_t>(w4_steps(F)) * (kW4Step / group);
-    m.xfrag = take(T * w4_row_bytes(d));
-    m.xfx = take(T * groups_d * 8);
-    m.hfx = take(pairs * groups_f * 8);
+    m.x = take(w4_staged_bytes(T, d, group));
+    m.hsums = take(w4_sums_bytes(pairs, F, group));
+    m.hfactor = take(4 * pairs);
   }
   m.total = at;
   return m;
@@ -616,7 +598,7 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   const int cap = c.T < 8 * ntmax ? c.T : 8 * ntmax;
   bool local = npairs <= 32 && cap <= 8;
   if constexpr (W4)
-    local = local && w4_staged_bytes<FMT>(cap, c.d) <= kLocalBytes && w4_staged_bytes<FMT>(cap, c.F) <= kLocalBytes;
+    local = local && w4_staged_bytes(cap, c.d, FMT) <= kLocalBytes && w4_staged_bytes(cap, c.F, FMT) <= kLocalBytes;
   if (local) ntmax = 1;
   ProductArgs a{};
   a.idx = static_cast<const int32_t*>(c.idx);
@@ -629,13 +611,16 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   a.kinv = token_factor(c.k);
   a.map = pair_map_at(reinterpret_cast<int*>(base + sc.map), npairs, c.E, cap);
   const uint32_t* err = dev.err;
+  Staged staged_x{}, staged_h{};
+  if constexpr (W4) {
+    staged_x = w4_staged_at(base + sc.x, c.T, c.d, FMT);
+    staged_h = Staged{base + sc.h, reinterpret_cast<float*>(base + sc.hsums), reinterpret_cast<float*>(base + sc.hfactor)};
+  }
   cudaError_t e;
   if (!local) {
     trace->begin("moe_plan", 0.0, 4.0 * npairs);
-    const StageArgs x{static_cast<const uint8_t*>(c.x), base + sc.xfrag, reinterpret_cast<float2*>(base + sc.xfx),
-                      2 * static_cast<int64_t>(c.d), c.T, c.d};
-    const int64_t items = W4 ? (static_cast<int64_t>(c.T) * w4_steps(c.d) + 15) / 16 : 0;
-    const int grid = 1 + static_cast<int>(items < 4 * dev.num_sms ? items : 4 * dev.num_sms);
+    const StageArgs x{static_cast<const uint8_t*>(c.x), staged_x, 2 * static_cast<int64_t>(c.d), W4 ? c.T : 0, c.d};
+    const int grid = 1 + (x.n < 4 * dev.num_sms ? x.n : 4 * dev.num_sms);
     e = launch_pdl(moe_plan_kernel<FMT>, dim3(grid), dim3(kMoeThreads), kMoeWarps * c.E * sizeof(int), s, a.map, a.idx,
                    npairs, c.E, cap, x, err);
     trace->end();
@@ -649,8 +634,7 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   a.zeros = static_cast<const uint8_t*>(c.z13);
   a.in = static_cast<const uint8_t*>(c.x);
   a.in_stride = 2 * static_cast<int64_t>(c.d);
-  a.frag = base + sc.xfrag;
-  a.fx = reinterpret_cast<const float2*>(base + sc.xfx);
+  a.staged = staged_x;
   a.out = base + sc.h;
   a.out_stride = sc.h_stride;
   trace->begin("moe_up", 4.0 * npairs * df, n_exp * 2.0 * df * wb + 2.0 * c.T * c.d + 2.0 * npairs * c.F);
@@ -660,9 +644,8 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   if constexpr (W4) {
     if (!local) {
       trace->begin("moe_stage", 0.0, 4.0 * npairs * c.F);
-      const StageArgs h{base + sc.h, base + sc.h, reinterpret_cast<float2*>(base + sc.hfx), sc.h_stride, npairs, c.F};
-      const int64_t items = (static_cast<int64_t>(npairs) * w4_steps(c.F) + 15) / 16;
-      const int grid = static_cast<int>(items < 8 * dev.num_sms ? items : 8 * dev.num_sms);
+      const StageArgs h{base + sc.h, staged_h, sc.h_stride, npairs, c.F};
+      const int grid = npairs < 8 * dev.num_sms ? npairs : 8 * dev.num_sms;
       e = launch_pdl(moe_stage_kernel<FMT>, dim3(grid), dim3(kMoeThreads), 0, s, h, err);
       trace->end();
       if (e != cudaSuccess) return e;
@@ -674,8 +657,7 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   a.zeros = static_cast<const uint8_t*>(c.z2);
   a.in = base + sc.h;
   a.in_stride = sc.h_stride;
-  a.frag = base + sc.h;
-  a.fx = reinterpret_cast<const float2*>(base + sc.hfx);
+  a.staged = staged_h;
   a.out = base + sc.part;
   a.out_stride = 4 * static_cast<int64_t>(c.d);
   trace->begin("moe_down", 2.0 * npairs * df, n_exp * df * wb + 2.0 * npairs * c.F + 4.0 * npairs * c.d);

@@ -85,17 +85,21 @@ static __device__ __forceinline__ void clear(RowSums<NT>& acc) {
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 }
 
-// How many ways to split K over a CTA's warps: the split with the least time,
-// counting the units that fall to an SM times the steps of a unit's slice, and
-// `fixed` steps' worth for beginning and ending a unit.  The CTAs of an SM share
-// its pipes, so it is SMs that have to come out even, not CTAs.
-static inline int rowdot_split(int64_t blocks_per_entry, int64_t entries, int steps, int fixed, int most,
+// How many ways to split K over a CTA's warps: the split with the least time.  It
+// counts the units that fall to an SM times the steps of a unit's slice (and one
+// for ending the unit), over the rate of an SM with that many CTAs at a time.
+// The CTAs of an SM share its pipes, so it is SMs that have to come out even.
+static inline int rowdot_split(int64_t blocks_per_entry, int64_t entries, int steps, int ctas, int most,
                                int num_sms) {
+  // measured on the 4-bit products: of the rate with 24 warps, 8 warps reach about half, 16 about 85%
+  constexpr int kRate[4] = {0, 50, 85, 100};
   int best = 1;
-  int64_t least = 0;
+  double least = 0.0;
   for (int WK = 1; WK <= most && (WK == 1 || steps >= 2 * WK); WK *= 2) {
     const int64_t units = entries * ((blocks_per_entry * WK + kRowWarps - 1) / kRowWarps);
-    const int64_t cost = (units + num_sms - 1) / num_sms * ((steps + WK - 1) / WK + fixed);
+    const int64_t rounds = (units + num_sms - 1) / num_sms;
+    const int at_a_time = static_cast<int>(rounds < ctas ? rounds : ctas);
+    const double cost = static_cast<double>(rounds) * ((steps + WK - 1) / WK + 1) / kRate[at_a_time];
     if (WK == 1 || cost < least) {
       least = cost;
       best = WK;

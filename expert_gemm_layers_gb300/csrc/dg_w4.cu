@@ -95,78 +95,59 @@ __global__ void w4_dequantize_kernel(const uint32_t* __restrict__ codes, const _
   w[v] = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Activation rows staged once for all CTAs of the product (w4_stage_piece): half
-// a warp a (row, step).
+// Activation rows staged once for all CTAs of the product, a CTA a row.
 template <int GROUP>
 __global__ void __launch_bounds__(256)
-    w4_stage_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ frag, float2* __restrict__ fx, int rows,
-                    int K, const uint32_t* err) {
+    w4_stage_kernel(const __nv_bfloat16* __restrict__ x, Staged out, int rows, int K, const uint32_t* err) {
+  __shared__ uint32_t top;
+  if (threadIdx.x == 0) top = 0u;
   griddep_wait();
-  griddep_launch_dependents();
   if (err_set(err)) return;
-  const int steps = w4_steps(K), p = threadIdx.x & 15;
-  const int64_t total = static_cast<int64_t>(rows) * steps, rb = w4_row_bytes(K);
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; i0 < total;
-       i0 += static_cast<int64_t>(gridDim.x) * 16) {
-    const int64_t i = i0 + ((threadIdx.x >> 4) & 1), row = i / steps;
-    const int st = static_cast<int>(i - row * steps), k = st * kW4Step + 8 * p;
-    const bool exists = i < total;
-    float f[8];
-    unpack_piece(exists && k < K ? *reinterpret_cast<const uint4*>(x + row * K + k) : make_uint4(0u, 0u, 0u, 0u), f);
-    w4_stage_piece<GROUP>(f, p, st, exists, frag + row * rb, fx + row * w4_fx_stride<GROUP>(K));
-  }
+  __syncthreads();
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    w4_stage_row<GROUP>(reinterpret_cast<const uint8_t*>(x + r * K), K, out.frag + r * w4_row_bytes(K),
+                        out.sums + r * w4_row_sums(K, GROUP), out.factor + r, &top);
 }
 
 // y = x W^T (+ bias): a CTA takes 8 / WK blocks of 32 weight rows and up to 8*NT
-// activation rows.  LOCAL: it stages those itself, in shared memory (x); else they
-// come staged (frag, fx).
+// activation rows.  LOCAL: it stages those itself, in shared memory; else `in` has
+// them.
 template <int GROUP, int NT, bool LOCAL>
-__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : NT == 2 ? 2 : 1)
-    w4_linear_kernel(const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ frag,
-                     const float2* __restrict__ fx, const uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
+    w4_linear_kernel(const __nv_bfloat16* __restrict__ x, Staged in, const uint8_t* __restrict__ codes,
                      const __nv_bfloat16* __restrict__ scales, const uint8_t* __restrict__ zeros,
-                     const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N, int WK, const uint32_t* err) {
+                     const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N,
+                     int WK, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t tops[8];
   griddep_wait();
-  griddep_launch_dependents();
   const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wk = warp % WK, rg = warp / WK;
   const int r0 = (static_cast<int>(blockIdx.x) * (kRowWarps / WK) + rg) * 16 * kRowTiles;
   const int n0 = static_cast<int>(blockIdx.y) * 8 * NT, count = min(rows - n0, 8 * NT);
-  const int64_t rb = w4_row_bytes(K);
-  const int fs = w4_fx_stride<GROUP>(K), steps = w4_steps(K);
-  uint8_t* joins = smem;
+  const int steps = w4_steps(K);
+  uint8_t* joins = smem + w4_ring_bytes<GROUP>();
+  // rows past the last one read the last one and store nothing
+  W4Stream<GROUP> stream{w4_rows<GROUP>(codes, scales, zeros, K, [&](int i) { return min(r0 + i, N - 1); }),
+                         smem + warp * w4_warp_bytes<GROUP>(), K, steps * wk / WK, steps * (wk + 1) / WK};
+  if (r0 < N) stream.start();
   if constexpr (LOCAL) {
-    uint8_t* xs = smem + joins_bytes<NT>(WK);
-    float2* xf = reinterpret_cast<float2*>(xs + count * rb);
-    const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, total = count * steps;
-    for (int i0 = 0; i0 < total; i0 += 16) {
-      const int i = i0 + hw, row = i / steps, st = i - row * steps, k = st * kW4Step + 8 * p;
-      float f[8];
-      unpack_piece(i < total && k < K ? *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(n0 + row) * K + k)
-                                      : make_uint4(0u, 0u, 0u, 0u),
-                   f);
-      w4_stage_piece<GROUP>(f, p, st, i < total, xs + row * rb, xf + row * fs);
-    }
-    frag = xs;
-    fx = xf;
-    __syncthreads();
+    in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
+    w4_stage_local<GROUP>(in, count, K, tops,
+                          [&](int i) { return reinterpret_cast<const uint8_t*>(x + static_cast<int64_t>(n0 + i) * K); });
   } else {
-    frag += n0 * rb;
-    fx += static_cast<int64_t>(n0) * fs;
+    in.frag += n0 * w4_row_bytes(K);
+    in.sums += static_cast<int64_t>(n0) * w4_row_sums(K, GROUP);
+    in.factor += n0;
   }
   RowSums<NT> acc;
   clear<NT>(acc);
-  if (r0 < N) {
-    // rows past the last one read the last one and store nothing
-    const W4Rows r = w4_rows<GROUP>(codes, scales, zeros, K, [&](int i) { return min(r0 + i, N - 1); });
-    const W4Cols<NT> cols = w4_cols<GROUP, NT>(frag, fx, K, count, [](int i) { return i; });
-    row_dot_w4<GROUP, NT>(r, cols, K, steps * wk / WK, steps * (wk + 1) / WK, acc);
-  }
+  auto act = [](int i) { return i; };
+  if (r0 < N) stream.template run<NT>(w4_cols<GROUP, NT>(in, K, count, act), acc);
   if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   if (wk != 0 || r0 >= N || failed != 0u) return;
-  w4_unscale<NT>(acc);
+  w4_unscale<NT>(acc, in.factor, count, act);
 #pragma unroll
   for (int m = 0; m < kRowTiles; ++m)
 #pragma unroll
@@ -189,39 +170,38 @@ struct W4Weight {
 };
 
 template <int GROUP, int NT, bool LOCAL>
-cudaError_t launch_linear(const void* x, const uint8_t* frag, const float2* fx, const W4Weight& w, const void* bias,
-                          void* y, int rows, int K, int N, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t launch_linear(const void* x, const Staged& in, const W4Weight& w, const void* bias, void* y, int rows,
+                          int K, int N, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int kRows = 16 * kRowTiles;
   const int x_blocks = (rows + 8 * NT - 1) / (8 * NT);
-  const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), 2, kRowWarps,
-                              dev.num_sms);
-  const int smem = joins_bytes<NT>(WK) + (LOCAL ? static_cast<int>(w4_staged_bytes<GROUP>(rows, K)) : 0);
+  // more slices of K mean that the warps of a CTA share less of the staged rows in L1
+  const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), NT == 1 ? 3 : 2,
+                              NT == 1 ? kRowWarps : 2, dev.num_sms);
+  const int smem = w4_ring_bytes<GROUP>() + joins_bytes<NT>(WK) +
+                   (LOCAL ? static_cast<int>(w4_staged_bytes(rows, K, GROUP)) : 0);
   auto kern = w4_linear_kernel<GROUP, NT, LOCAL>;
-  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 64 * 1024, dev.device);
+  cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
   if (e != cudaSuccess) return e;
   const int a_cta = kRowWarps / WK * kRows;
   return launch_pdl(kern, dim3((N + a_cta - 1) / a_cta, x_blocks), dim3(kRowWarps * 32), smem, s,
-                    static_cast<const __nv_bfloat16*>(x), frag, fx, w.codes, w.scales, w.zeros,
-                    static_cast<const __nv_bfloat16*>(bias),
-                    static_cast<__nv_bfloat16*>(y), rows, K, N, WK, static_cast<const uint32_t*>(dev.err));
+                    static_cast<const __nv_bfloat16*>(x), in, w.codes, w.scales, w.zeros,
+                    static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), rows, K, N, WK,
+                    static_cast<const uint32_t*>(dev.err));
 }
 
 template <int GROUP>
 cudaError_t launch_linear_g(const void* x, const W4Weight& w, const void* bias, void* y, int rows, int K, int N,
                             void* scratch, const DeviceInfo& dev, cudaStream_t s) {
   if (w4_linear_local(rows, K, GROUP))
-    return launch_linear<GROUP, 1, true>(x, nullptr, nullptr, w, bias, y, rows, K, N, dev, s);
-  uint8_t* frag = static_cast<uint8_t*>(scratch);
-  float2* fx = reinterpret_cast<float2*>(frag + rows * w4_row_bytes(K));
-  const int64_t items = (static_cast<int64_t>(rows) * w4_steps(K) + 15) / 16;
-  const int grid = static_cast<int>(items < 8 * dev.num_sms ? items : 8 * dev.num_sms);
+    return launch_linear<GROUP, 1, true>(x, Staged{}, w, bias, y, rows, K, N, dev, s);
+  const Staged in = w4_staged_at(static_cast<uint8_t*>(scratch), rows, K, GROUP);
+  const int grid = rows < 8 * dev.num_sms ? rows : 8 * dev.num_sms;
   cudaError_t e = launch_pdl(w4_stage_kernel<GROUP>, dim3(grid), dim3(256), 0, s,
-                             static_cast<const __nv_bfloat16*>(x), frag, fx, rows, K,
-                             static_cast<const uint32_t*>(dev.err));
+                             static_cast<const __nv_bfloat16*>(x), in, rows, K, static_cast<const uint32_t*>(dev.err));
   if (e != cudaSuccess) return e;
-  if (rows <= 8) return launch_linear<GROUP, 1, false>(x, frag, fx, w, bias, y, rows, K, N, dev, s);
-  if (rows <= 16) return launch_linear<GROUP, 2, false>(x, frag, fx, w, bias, y, rows, K, N, dev, s);
-  return launch_linear<GROUP, 4, false>(x, frag, fx, w, bias, y, rows, K, N, dev, s);
+  if (rows <= 8) return launch_linear<GROUP, 1, false>(x, in, w, bias, y, rows, K, N, dev, s);
+  if (rows <= 16) return launch_linear<GROUP, 2, false>(x, in, w, bias, y, rows, K, N, dev, s);
+  return launch_linear<GROUP, 4, false>(x, in, w, bias, y, rows, K, N, dev, s);
 }
 
 template <int GROUP>
@@ -263,15 +243,12 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const vo
 // Up to 8 rows whose staged form takes no more than 32 KB are staged by every CTA
 // itself: reading 1 to 8 short rows costs less than another launch.
 bool w4_linear_local(int64_t rows, int64_t K, int group) {
-  const int k = static_cast<int>(K);
-  return rows <= 8 && K <= 32768 &&
-         (group == 32 ? w4_staged_bytes<32>(rows, k) : group == 64 ? w4_staged_bytes<64>(rows, k)
-                                                                   : w4_staged_bytes<128>(rows, k)) <= 32 * 1024;
+  return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group) <= 32 * 1024;
 }
 
 size_t w4_linear_scratch_bytes(int64_t rows, int64_t K) {
   // of the finest group; the group is not known to the query
-  return static_cast<size_t>(w4_staged_bytes<32>(rows, static_cast<int>(K)));
+  return static_cast<size_t>(w4_staged_bytes(rows, static_cast<int>(K), 32));
 }
 
 cudaError_t launch_w4_linear(const void* x, const void* codes, const void* scales, const void* zeros,

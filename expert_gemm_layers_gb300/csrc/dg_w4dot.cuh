@@ -9,18 +9,17 @@
 //    2^-24, and the tensor cores take such numbers exactly.  word & 0x00f000f0 is
 //    (16 q1, 16 q5) * 2^-24.  With word >> 8 that makes 5 operations for 8 codes
 //    (inserting an exponent and subtracting the zero point would take 11).
-//  - The activations are brought to that form once (w4_stage_piece): each group of
-//    a row is scaled by a power of two to magnitudes below 2^15, rounded to fp16,
-//    columns 1 3 5 7 divided by 16, in the order the lanes take them.  A bf16
-//    number has 8 significant bits, so it fits fp16's 11 exactly unless it is 2^28
-//    times smaller than the group's largest; then it is off by at most 2^-40 of
-//    that largest, far below one unit of the binary32 sum.
+//  - The activations are brought to that form once (w4_stage_row): a row is scaled
+//    by a power of two to magnitudes below 2^15, rounded to fp16, columns 1 3 5 7
+//    of 8 divided by 16, in the order the lanes take them.  A bf16 number has 8
+//    significant bits, so it fits fp16's 11 exactly unless it is 2^28 times smaller
+//    than the row's largest; then it is off by at most 2^-40 of that largest, far
+//    below one unit of the binary32 sum.
 //  - The zero point is taken out of the group's sum at the end:
 //    sum (q - z) x = sum q x - z * sum x, the second sum made with the scaling.
 //
-// A step is 128 columns: 64 bytes of codes a row, loaded straight into registers
-// one step ahead.  A lane takes a quarter of each group, so an mma never mixes
-// groups.
+// A step is 128 columns: 64 bytes of codes a row.  A lane takes a quarter of each
+// group, so an mma never mixes groups.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -32,44 +31,60 @@ namespace dg {
 constexpr int kW4Step = 128;
 
 // Staged activations: of every row and step 256 bytes of fp16 (pieces of 8
-// columns, [piece of a lane][lane t]), and of every row and group {factor, sum}.
-// Rows are padded by 64 bytes against bank conflicts in shared memory.
+// columns, [piece of a lane][lane t]); of every row and group the sum of its scaled
+// columns; of every row the inverse of its scale.  Rows are padded by 64 bytes
+// against bank conflicts in shared memory.
+struct Staged {
+  uint8_t* frag;
+  float* sums;
+  float* factor;
+};
 __host__ __device__ inline int w4_steps(int K) { return (K + kW4Step - 1) / kW4Step; }
 __host__ __device__ inline int64_t w4_row_bytes(int K) { return 256 * static_cast<int64_t>(w4_steps(K)) + 64; }
-template <int GROUP>
-__host__ __device__ inline int w4_fx_stride(int K) {  // {factor, sum} pairs of a row
-  return w4_steps(K) * (kW4Step / GROUP);
+__host__ __device__ inline int w4_row_sums(int K, int group) { return w4_steps(K) * (kW4Step / group); }
+__host__ __device__ inline int64_t w4_sums_bytes(int64_t rows, int K, int group) {
+  return (4 * rows * w4_row_sums(K, group) + 15) / 16 * 16;
 }
-template <int GROUP>
-__host__ __device__ inline int64_t w4_staged_bytes(int64_t rows, int K) {
-  return rows * (w4_row_bytes(K) + 8 * w4_fx_stride<GROUP>(K));
+__host__ __device__ inline int64_t w4_staged_bytes(int64_t rows, int K, int group) {
+  return rows * w4_row_bytes(K) + w4_sums_bytes(rows, K, group) + (4 * rows + 15) / 16 * 16;
+}
+__host__ __device__ inline Staged w4_staged_at(uint8_t* p, int64_t rows, int K, int group) {
+  float* sums = reinterpret_cast<float*>(p + rows * w4_row_bytes(K));
+  return Staged{p, sums, sums + w4_sums_bytes(rows, K, group) / 4};
 }
 
-// Stages one piece: 8 columns (word: as bf16 pairs, or f as binary32 when IS_F32)
-// of step `st` of a row.  The 16 lanes of half a warp hold the 16 pieces of one
-// step (p: this lane's); all lanes of the warp call together.  frag, fx: the
-// row's; nothing is written where !exists.
-template <int GROUP>
-static __device__ __forceinline__ void w4_stage_piece(float (&f)[8], int p, int st, bool exists, uint8_t* frag,
-                                                      float2* fx) {
-  constexpr int W = GROUP / 32;  // code words of a group a lane takes
-  // the largest finite magnitude of the group; what is not finite stays so
+// The largest finite magnitude of a piece of 8 columns, as bits; what is not
+// finite stays so and has no part in the scale.
+static __device__ __forceinline__ uint32_t w4_top(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
-    top = max(top, a < 0x7f800000u ? a : 0u);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
+    top = max(top, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
   }
+  return top;
+}
+// Exponent E of a row's scale 2^(14 - E); the scale is at most 2^114, so that it and
+// its inverse are normal numbers.
+static __device__ __forceinline__ int w4_exponent(uint32_t top) { return max(static_cast<int>(top >> 7) - 127, -100); }
+
+// Stages pieces p of steps `st` of a row: the 16 lanes of half a warp hold the 16
+// pieces of one step; all lanes of the warp call together.  Nothing is written
+// where !exists.
+template <int GROUP>
+static __device__ __forceinline__ void w4_stage_piece(const uint4& v, int E, int p, int st, bool exists,
+                                                      uint8_t* frag, float* sums) {
+  constexpr int W = GROUP / 32;  // code words of a group a lane takes
+  const float scale = __int_as_float((127 + 14 - E) << 23);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float f[8], sum = 0.0f;
 #pragma unroll
-  for (int o = 2 * W; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // the factor 2^(14 - E), at most 2^114, so that it and its inverse are normal numbers
-  const int E = max(static_cast<int>(top >> 23) - 127, -100);
-  const float scale = __int_as_float((127 + 14 - E) << 23), inverse = __int_as_float((127 - 14 + E) << 23);
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] *= scale;
-    sum += f[i];
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = unpack_bf16x2(w[i]);
+    f[2 * i] = a.x * scale;
+    f[2 * i + 1] = a.y * scale;
+    sum += f[2 * i] + f[2 * i + 1];
   }
 #pragma unroll
   for (int o = 2 * W; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -82,36 +97,102 @@ static __device__ __forceinline__ void w4_stage_piece(float (&f)[8], int p, int 
   }
   if (!exists) return;
   // piece p lies with lane t = p / W % 4, as its piece p / 4W * W + p % W
-  *reinterpret_cast<uint4*>(frag + st * 256 + (p / (4 * W) * W + p % W) * 64 + (p / W) % 4 * 16) =
-      make_uint4(out[0], out[1], out[2], out[3]);
-  if (p % (4 * W) == 0)
-    fx[st * (kW4Step / GROUP) + p / (4 * W)] = make_float2(inverse, sum * __int_as_float((127 - 24) << 23));
+  *reinterpret_cast<uint4*>(frag + static_cast<int64_t>(st) * 256 + (p / (4 * W) * W + p % W) * 64 +
+                            (p / W) % 4 * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+  if (p % (4 * W) == 0) sums[st * (kW4Step / GROUP) + p / (4 * W)] = sum * __int_as_float((127 - 24) << 23);
 }
 
-static __device__ __forceinline__ void unpack_piece(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Stages one row [K] bf16 by the 256 threads of a CTA; `shared_top`: a word that is
+// 0 and is left 0.  frag may lie over x: a step's pieces are written by the lanes
+// that have read them.  Synchronises the CTA.
+template <int GROUP>
+static __device__ __forceinline__ void w4_stage_row(const uint8_t* x, int K, uint8_t* frag, float* sums, float* factor,
+                                                    uint32_t* shared_top) {
+  const int p = threadIdx.x & 15, steps = w4_steps(K);
+  auto piece = [&](int st) {
+    const int k = st * kW4Step + 8 * p;
+    return st < steps && k < K ? *reinterpret_cast<const uint4*>(x + 2 * static_cast<int64_t>(k))
+                               : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint32_t top = 0u;
+  for (int st = threadIdx.x >> 4; st < steps; st += 16) top = max(top, w4_top(piece(st)));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = unpack_bf16x2(w[i]);
-    f[2 * i] = a.x;
-    f[2 * i + 1] = a.y;
+  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((threadIdx.x & 31) == 0) atomicMax(shared_top, top);
+  __syncthreads();
+  const int E = w4_exponent(*shared_top);
+  for (int s0 = 0; s0 < steps; s0 += 16) {
+    const int st = s0 + (threadIdx.x >> 4);
+    w4_stage_piece<GROUP>(piece(st), E, p, st, st < steps, frag, sums);
   }
+  if (threadIdx.x == 0) *factor = __int_as_float((127 - 14 + E) << 23);
+  __syncthreads();
+  if (threadIdx.x == 0) *shared_top = 0u;
+  __syncthreads();
 }
 
+// Stages up to 8 rows in shared memory by the 256 threads of a CTA, one after the
+// other in time only where their scales are concerned.  row(i): row i.  tops: 8
+// words.  Synchronises the CTA.
+template <int GROUP, typename Row>
+static __device__ __forceinline__ void w4_stage_local(const Staged& out, int count, int K, uint32_t* tops, Row row) {
+  const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, steps = w4_steps(K), total = count * steps;
+  if (threadIdx.x < 8) tops[threadIdx.x] = 0u;
+  __syncthreads();
+  auto piece = [&](int i, int& r, int& st) {
+    r = count == 1 ? 0 : i / steps;
+    st = i - r * steps;
+    const int k = st * kW4Step + 8 * p;
+    return i < total && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * k) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  for (int i = hw; i < total; i += 16) {
+    int r, st;
+    uint32_t top = w4_top(piece(i, r, st));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), top, o));
+    if (p == 0) atomicMax(&tops[r], top);
+  }
+  __syncthreads();
+  const int64_t rb = w4_row_bytes(K);
+  const int fs = w4_row_sums(K, GROUP);
+  for (int i0 = 0; i0 < total; i0 += 16) {
+    const int i = i0 + hw;
+    int r, st;
+    const uint4 v = piece(i, r, st);
+    w4_stage_piece<GROUP>(v, w4_exponent(i < total ? tops[r] : 0u), p, st, i < total, out.frag + r * rb,
+                          out.sums + r * fs);
+  }
+  if (threadIdx.x < count) out.factor[threadIdx.x] = __int_as_float((127 - 14 + w4_exponent(tops[threadIdx.x])) << 23);
+  __syncthreads();
+}
+
+// c += a b, or c = a b.  PINNED keeps the order of the source: without it the loads
+// of all pieces are moved to the front of a step, for which NT > 2 has no registers.
+template <bool FIRST, bool PINNED>
 static __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+#define DG_MMA "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+#define DG_IN "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1)
+  if constexpr (FIRST && PINNED)
+    asm volatile(DG_MMA "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : DG_IN, "f"(0.0f));
+  else if constexpr (FIRST)
+    asm(DG_MMA "{%10, %10, %10, %10};" : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : DG_IN, "f"(0.0f));
+  else if constexpr (PINNED)
+    asm volatile(DG_MMA "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : DG_IN);
+  else
+    asm(DG_MMA "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : DG_IN);
+#undef DG_MMA
+#undef DG_IN
 }
-// The same from a zero accumulator.
-static __device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+
+template <bool PINNED>
+static __device__ __forceinline__ uint4 ld_piece(const uint8_t* p) {
+  if constexpr (!PINNED) return *reinterpret_cast<const uint4*>(p);
+  uint4 v;
+  asm volatile("ld.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
 // A warp's rows of a 4-bit weight.
@@ -124,129 +205,206 @@ struct W4Rows {
 };
 
 // Staged activation rows as a lane reads them: frag[n] is the row of its column
-// 8n + g, in 16-byte units from xs; fx[n][i] that of column 8n + 2t + i, in
-// {factor, sum} pairs from xf.
+// 8n + g, in 16-byte units from xs; sums[n][i] that of column 8n + 2t + i, in
+// numbers from xsums.
 template <int NT>
 struct W4Cols {
   const uint8_t* xs;
-  const float2* xf;
-  uint32_t frag[NT], fx[NT][2];
+  const float* xsums;
+  uint32_t frag[NT], sums[NT][2];
 };
 
-// What a lane loads of a step: the code words of its four rows, and scale (high
-// half) and zero point (low byte) of the groups of row `lane`.
+// Each warp keeps kW4Ring - 1 steps of its rows' codes on the way from HBM in a
+// ring of its own, filled by 16-byte asynchronous copies.  A row's 64 bytes of a
+// step are swizzled by pieces of 16, so that reads of a piece, half a piece or a
+// word a lane all spread over the banks.
+constexpr int kW4Ring = 3;
+constexpr int kW4StepBytes = kLaneRows * 512;
+// Behind the codes: {-zero point, scale} of the warp's 32 rows, [G][32], two steps.
 template <int GROUP>
-struct W4Step {
-  uint32_t code[kLaneRows][4];
-  uint32_t sz[kW4Step / GROUP];
-};
+constexpr int w4_warp_bytes() {
+  return kW4Ring * kW4StepBytes + 2 * 256 * (kW4Step / GROUP);
+}
+template <int GROUP>
+constexpr int w4_ring_bytes() {  // of a CTA
+  return kRowWarps * w4_warp_bytes<GROUP>();
+}
 
-template <int GROUP>
-static __device__ __forceinline__ void w4_load(const W4Rows& w, int c, int groups, W4Step<GROUP>& v) {
+// One step's product.  slot: its codes; zs: {-zero point, scale} of the warp's rows.
+template <int GROUP, int NT>
+static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Cols<NT>& x, int c,
+                                              int groups, RowSums<NT>& acc) {
   constexpr int G = kW4Step / GROUP;  // groups a step
   constexpr int W = GROUP / 32;       // code words of a row and group a lane takes
-  const int t = threadIdx.x & 3;
-  const uint8_t* p0 = w.codes + static_cast<int64_t>(c) * 64 + 4 * W * t;
-  const uint8_t* p1 = w.codes1 + static_cast<int64_t>(c) * 64 + 4 * W * t;
-  const uint8_t* p[kLaneRows] = {p0, p0 + w.next0, p1, p1 + w.next1};
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int swz = (g >> 1) & 3;
+  // sums of the columns 8n + 2t and 8n + 2t + 1, all groups of the step
+  float xsum[NT][2][G];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* p = x.xsums + static_cast<uint64_t>(x.sums[n][i]) + c * G;
+      if constexpr (G == 4) *reinterpret_cast<float4*>(xsum[n][i]) = *reinterpret_cast<const float4*>(p);
+      else if constexpr (G == 2) *reinterpret_cast<float2*>(xsum[n][i]) = *reinterpret_cast<const float2*>(p);
+      else xsum[n][i][0] = *p;
+    }
 #pragma unroll
   for (int q = 0; q < G; ++q) {
     if (G == 1 || c * G + q < groups) {  // a group is whole or absent
+      // this lane's words of the group: piece and offset within the row's 64 bytes
+      const int piece = GROUP == 128 ? t : GROUP == 64 ? 2 * q + (t >> 1) : q;
+      const int off = GROUP == 128 ? 0 : GROUP == 64 ? 8 * (t & 1) : 4 * t;
+      const uint8_t* from = slot + g * 64 + (piece ^ swz) * 16 + off;
+      // one row tile at a time where both would not fit the registers
+      constexpr int kTogether = NT > 2 ? 1 : kRowTiles;
 #pragma unroll
-      for (int i = 0; i < kLaneRows; ++i) {
-        if constexpr (W == 4)
-          asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.code[i][0]), "=r"(v.code[i][1]), "=r"(v.code[i][2]), "=r"(v.code[i][3])
-                       : "l"(p[i]));
-        else if constexpr (W == 2)
-          asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
-                       : "=r"(v.code[i][2 * q]), "=r"(v.code[i][2 * q + 1])
-                       : "l"(p[i] + 32 * q));
-        else
-          asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v.code[i][q]) : "l"(p[i] + 16 * q));
-      }
-      const uint32_t z = w.zeros ? w.zeros[c * G + q] : 8u;
-      v.sz[q] = (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(w.scales + c * G + q)) << 16) | z;
-    }
-  }
-}
-
-template <int GROUP, int NT>
-static __device__ __forceinline__ void w4_use(const W4Step<GROUP>& v, const W4Cols<NT>& x, int c, int groups,
-                                              RowSums<NT>& acc) {
-  constexpr int G = kW4Step / GROUP;
-  constexpr int W = GROUP / 32;
-  const int g = (threadIdx.x & 31) >> 2;
+      for (int m0 = 0; m0 < kRowTiles; m0 += kTogether) {
+        float part[kTogether][NT][4];
+        uint32_t code[2 * kTogether][W];
 #pragma unroll
-  for (int q = 0; q < G; ++q) {
-    if (G == 1 || c * G + q < groups) {
-      RowSums<NT> part;
+        for (int i = 0; i < 2 * kTogether; ++i) {
+          const uint8_t* p = from + (2 * m0 + i) * 512;
+          if constexpr (W == 4) *reinterpret_cast<uint4*>(code[i]) = *reinterpret_cast<const uint4*>(p);
+          else if constexpr (W == 2) *reinterpret_cast<uint2*>(code[i]) = *reinterpret_cast<const uint2*>(p);
+          else code[i][0] = *reinterpret_cast<const uint32_t*>(p);
+        }
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        uint4 b[NT];
+        for (int j = 0; j < W; ++j) {
+          uint4 b[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          b[n] = *reinterpret_cast<const uint4*>(x.xs + (static_cast<uint64_t>(x.frag[n]) + 16 * c) * 16 +
-                                                 (q * W + j) * 64);
+          for (int n = 0; n < NT; ++n)
+            b[n] = ld_piece<(NT > 2)>(x.xs + (static_cast<uint64_t>(x.frag[n]) + 16 * c) * 16 + (q * W + j) * 64);
 #pragma unroll
-        for (int m = 0; m < kRowTiles; ++m) {
-          const uint32_t l = v.code[2 * m][q * W + j], h = v.code[2 * m + 1][q * W + j];
-          const uint32_t l8 = l >> 8, h8 = h >> 8;
+          for (int m = 0; m < kTogether; ++m) {
+            const uint32_t l = code[2 * m][j], h = code[2 * m + 1][j];
+            const uint32_t l8 = l >> 8, h8 = h >> 8;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (j == 0)
+                mma_f16<true, (NT > 2)>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
+                                        h & 0x00f000f0u, b[n].x, b[n].y);
+              else
+                mma_f16<false, (NT > 2)>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
+                                         h & 0x00f000f0u, b[n].x, b[n].y);
+              mma_f16<false, (NT > 2)>(part[m][n], l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u,
+                                       h8 & 0x00f000f0u, b[n].z, b[n].w);
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < kTogether; ++m) {
+          const uint8_t* p = zs + q * 256 + (16 * (m0 + m) + g) * 8;
+          const float2 l = *reinterpret_cast<const float2*>(p), h = *reinterpret_cast<const float2*>(p + 64);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (j == 0)
-              mma_f16_first(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u, h & 0x00f000f0u, b[n].x,
-                            b[n].y);
-            else
-              mma_f16(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u, h & 0x00f000f0u, b[n].x,
-                      b[n].y);
-            mma_f16(part[m][n], l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u, h8 & 0x00f000f0u, b[n].z,
-                    b[n].w);
+            float(&to)[4] = acc[m0 + m][n];
+            to[0] = fmaf(l.y, fmaf(l.x, xsum[n][0][q], part[m][n][0]), to[0]);
+            to[1] = fmaf(l.y, fmaf(l.x, xsum[n][1][q], part[m][n][1]), to[1]);
+            to[2] = fmaf(h.y, fmaf(h.x, xsum[n][0][q], part[m][n][2]), to[2]);
+            to[3] = fmaf(h.y, fmaf(h.x, xsum[n][1][q], part[m][n][3]), to[3]);
           }
         }
       }
-      float s[kLaneRows], z[kLaneRows];
-#pragma unroll
-      for (int i = 0; i < kLaneRows; ++i) {
-        const uint32_t sz = __shfl_sync(0xffffffffu, v.sz[q], 8 * i + g);
-        s[i] = __uint_as_float(sz & 0xffff0000u);
-        z[i] = 8388608.0f - __uint_as_float(0x4b000000u | (sz & 15u));  // -z, by way of a binary32 significand
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 x0 = x.xf[static_cast<uint64_t>(x.fx[n][0]) + c * G + q];
-        const float2 x1 = x.xf[static_cast<uint64_t>(x.fx[n][1]) + c * G + q];
-#pragma unroll
-        for (int m = 0; m < kRowTiles; ++m) {
-          const float sl = s[2 * m], sh = s[2 * m + 1], zl = z[2 * m], zh = z[2 * m + 1];
-          acc[m][n][0] = fmaf(sl * x0.x, fmaf(zl, x0.y, part[m][n][0]), acc[m][n][0]);
-          acc[m][n][1] = fmaf(sl * x1.x, fmaf(zl, x1.y, part[m][n][1]), acc[m][n][1]);
-          acc[m][n][2] = fmaf(sh * x0.x, fmaf(zh, x0.y, part[m][n][2]), acc[m][n][2]);
-          acc[m][n][3] = fmaf(sh * x1.x, fmaf(zh, x1.y, part[m][n][3]), acc[m][n][3]);
-        }
-      }
     }
   }
 }
 
-// acc += steps [c0, c1), in units of 2^-24, of the product of a warp's 32 rows
-// with up to 8*NT staged activation rows.  Thread (g, t) ends with acc[m][n] =
-// (row g of tile m, columns 8n + 2t, 8n + 2t + 1; row g + 8, the same).
-template <int GROUP, int NT>
-static __device__ __forceinline__ void row_dot_w4(const W4Rows& w, const W4Cols<NT>& x, int K, int c0, int c1,
-                                                  RowSums<NT>& acc) {
-  const int groups = K / GROUP;
-  W4Step<GROUP> a, b;
-  if (c0 < c1) w4_load<GROUP>(w, c0, groups, a);
-#pragma unroll 1
-  for (int c = c0; c < c1; c += 2) {
-    if (c + 1 < c1) w4_load<GROUP>(w, c + 1, groups, b);
-    w4_use<GROUP, NT>(a, x, c, groups, acc);
-    if (c + 1 >= c1) break;
-    if (c + 2 < c1) w4_load<GROUP>(w, c + 2, groups, a);
-    w4_use<GROUP, NT>(b, x, c + 1, groups, acc);
+// The codes and scales of steps [c0, c1) of a warp's rows.  start() is apart from
+// run(), so that a kernel can ask for them before it has its activations.
+template <int GROUP>
+struct W4Stream {
+  static constexpr int G = kW4Step / GROUP;
+  W4Rows w;
+  uint8_t* ring;  // this warp's w4_warp_bytes
+  int K, c0, c1;
+  // scales and zero points of row `lane`, of the step after the last one decoded, as they lie in memory
+  uint32_t s[2], z;
+
+  __device__ __forceinline__ void fill(int c, int u) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const bool in = c < c1 && c * kW4Step + 32 * t < K;
+    const int64_t at = in ? static_cast<int64_t>(c) * 64 + 16 * t : 0;
+    const uint32_t dst = smem_u32(ring) + u * kW4StepBytes + g * 64 + (t ^ ((g >> 1) & 3)) * 16;
+    cp_async16(dst, w.codes + at, in);
+    cp_async16(dst + 512, w.codes + w.next0 + at, in);
+    cp_async16(dst + 1024, w.codes1 + at, in);
+    cp_async16(dst + 1536, w.codes1 + w.next1 + at, in);
+    cp_async_commit();
   }
-}
+  __device__ __forceinline__ void load_scales(int c) {
+    if (c >= c1) return;
+    const int64_t at = static_cast<int64_t>(c) * G;
+    if (G == 1 || K % kW4Step == 0) {  // every row's scales start on a boundary of the vector
+      if constexpr (G == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(w.scales + at);
+        s[0] = v.x;
+        s[1] = v.y;
+        if (w.zeros) z = *reinterpret_cast<const uint32_t*>(w.zeros + at);
+      } else if constexpr (G == 2) {
+        s[0] = *reinterpret_cast<const uint32_t*>(w.scales + at);
+        if (w.zeros) z = *reinterpret_cast<const uint16_t*>(w.zeros + at);
+      } else {
+        s[0] = *reinterpret_cast<const uint16_t*>(w.scales + at);
+        if (w.zeros) z = w.zeros[at];
+      }
+    } else {
+      s[0] = s[1] = z = 0u;
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+        if ((c * G + q) * GROUP < K) {
+          s[q / 2] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(w.scales + at + q)) << (16 * (q % 2));
+          if (w.zeros) z |= static_cast<uint32_t>(w.zeros[at + q]) << (8 * q);
+        }
+    }
+  }
+  __device__ __forceinline__ uint8_t* decoded(int parity) const {
+    return ring + kW4Ring * kW4StepBytes + parity * 256 * G;
+  }
+  __device__ __forceinline__ void decode(int parity) const {
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+      // -z by way of a binary32 significand
+      const float nz = w.zeros ? 8388608.0f - __uint_as_float(0x4b000000u | ((z >> (8 * q)) & 15u)) : -8.0f;
+      const uint32_t two = s[q / 2];
+      *reinterpret_cast<float2*>(decoded(parity) + q * 256 + (threadIdx.x & 31) * 8) =
+          make_float2(nz, __uint_as_float(q % 2 ? two & 0xffff0000u : two << 16));
+    }
+  }
+  __device__ __forceinline__ void start() {
+    load_scales(c0);
+#pragma unroll
+    for (int u = 0; u < kW4Ring - 1; ++u) fill(c0 + u, u);
+  }
+  // acc += the product, in units of 2^-24 / factor, with up to 8*NT staged activation
+  // rows.  Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t,
+  // 8n + 2t + 1; row g + 8, the same).
+  template <int NT>
+  __device__ __forceinline__ void run(const W4Cols<NT>& x, RowSums<NT>& acc) {
+    const int groups = K / GROUP;
+    decode(0);
+    load_scales(c0 + 1);
+    int parity = 0;
+#pragma unroll 1
+    for (int c = c0; c < c1; c += kW4Ring) {
+#pragma unroll
+      for (int u = 0; u < kW4Ring; ++u) {
+        if (c + u >= c1) break;
+        cp_async_wait<kW4Ring - 2>();
+        // the other lanes' copies and scales are in place, and what the step before has read is free
+        __syncwarp();
+        fill(c + u + kW4Ring - 1, (u + kW4Ring - 1) % kW4Ring);
+        const uint8_t* zs = decoded(parity);
+        parity ^= 1;
+        decode(parity);
+        load_scales(c + u + 2);
+        w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, x, c + u, groups, acc);
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+  }
+};
 
 // The rows of a warp, by `row(i)`: index (in `codes`, a matrix of 4-bit rows) of
 // row i of the warp's 32, a valid one for every i.
@@ -266,31 +424,37 @@ static __device__ __forceinline__ W4Rows w4_rows(const uint8_t* codes, const __n
 // The columns of a warp, by `act(i)`: index of the staged row of column i, for i < count.
 // Columns without a row read the last one and are not used.
 template <int GROUP, int NT, typename Act>
-static __device__ __forceinline__ W4Cols<NT> w4_cols(const uint8_t* xs, const float2* xf, int K, int count, Act act) {
+static __device__ __forceinline__ W4Cols<NT> w4_cols(const Staged& in, int K, int count, Act act) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   W4Cols<NT> x;
-  x.xs = xs;
-  x.xf = xf;
+  x.xs = in.frag;
+  x.xsums = in.sums;
   const uint32_t rb = static_cast<uint32_t>(w4_row_bytes(K) / 16);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     x.frag[n] = static_cast<uint32_t>(act(min(8 * n + g, count - 1))) * rb + t;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      x.fx[n][i] = static_cast<uint32_t>(act(min(8 * n + 2 * t + i, count - 1))) * w4_fx_stride<GROUP>(K);
+      x.sums[n][i] = static_cast<uint32_t>(act(min(8 * n + 2 * t + i, count - 1))) * w4_row_sums(K, GROUP);
   }
   return x;
 }
 
-// The sums are in units of 2^-24, those of the codes.
-template <int NT>
-static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc) {
+// The sums are in units of 2^-24, those of the codes, and of their row's scale.
+template <int NT, typename Act>
+static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc, const float* factor, int count, Act act) {
+  const int t = threadIdx.x & 3;
 #pragma unroll
-  for (int m = 0; m < kRowTiles; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < 2; ++i) {
+      const float f = factor[act(min(8 * n + 2 * t + i, count - 1))];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] *= 16777216.0f;
+      for (int m = 0; m < kRowTiles; ++m) {
+        acc[m][n][i] = acc[m][n][i] * 16777216.0f * f;
+        acc[m][n][2 + i] = acc[m][n][2 + i] * 16777216.0f * f;
+      }
+    }
 }
 
 }  // namespace dg
