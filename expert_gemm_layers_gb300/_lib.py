@@ -109,6 +109,8 @@ class DGError(RuntimeError):
 def load():
     """Load libdg.so (once); raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

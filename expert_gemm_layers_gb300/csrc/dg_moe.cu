@@ -8,6 +8,8 @@
 // rows are read once and meet all of its tokens in registers (dg_rowdot.cuh).
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "dg_internal.h"
 #include "dg_w4dot.cuh"
 
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(kMoeThreads)
   __shared__ uint32_t top;
   if (threadIdx.x == 0) top = 0u;
   griddep_wait();
+  griddep_launch_dependents();
   if (err_set(err)) return;
   __syncthreads();
   if (blockIdx.x == 0) {
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(kMoeThreads) moe_stage_kernel(StageArgs h, con
   __shared__ uint32_t top;
   if (threadIdx.x == 0) top = 0u;
   griddep_wait();
+  griddep_launch_dependents();
   if (err_set(err)) return;
   __syncthreads();
   stage_rows<GROUP>(h, blockIdx.x, gridDim.x, &top);
@@ -415,10 +419,11 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
   } else {
     const int steps = w4_steps(K);
     const int64_t first = static_cast<int64_t>(e) * rows, groups = K / FMT;
-    uint8_t* joins = smem + w4_ring_bytes<FMT>();
-    W4Stream<FMT> stream{w4_rows<FMT>(a.weights + first * (K / 2), a.scales + first * groups,
-                                      a.zeros ? a.zeros + first * groups : nullptr, K, row),
-                         smem + warp * w4_warp_bytes<FMT>(), K, steps * wk / WK, steps * (wk + 1) / WK};
+    uint8_t* joins = smem + w4_ring_bytes<FMT, NT>(WK);
+    W4Stream<FMT, NT> stream{w4_rows<FMT>(a.weights + first * (K / 2), a.scales + first * groups,
+                                          a.zeros ? a.zeros + first * groups : nullptr, K, row),
+                             active, smem + warp * w4_warp_bytes<FMT, NT>(), K, steps * wk / WK,
+                             steps * (wk + 1) / WK};
     if (active) stream.start();
     Staged in = a.staged;
     if constexpr (LOCAL) {  // the unit's rows, in shared memory
@@ -427,10 +432,14 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
       w4_stage_local<FMT>(in, count, K, tops, [&](int i) { return a.in + act(i) * a.in_stride; });
     }
     auto column = [&](int i) { return LOCAL ? i : act(i); };
-    if (active) {
-      stream.template run<NT>(w4_cols<FMT, NT>(in, K, count, column), acc);
-      w4_unscale<NT>(acc, in.factor, count, column);
+    if constexpr (NT > 1) {
+      stream.run_wide(in, count, column,
+                      smem + kRowWarps * w4_warp_bytes<FMT, NT>() + wk * w4_xring_bytes<FMT, NT>(), rg * 32 + lane,
+                      32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
+    } else if (active) {
+      stream.run(w4_cols<FMT, NT>(in, K, count, column), acc);
     }
+    if (active) w4_unscale<NT>(acc, in.factor, count, column);
     if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   }
   if (wk == 0 && active && !failed) store_block<NT, UP>(a, pairs, count, b, acc);
@@ -494,6 +503,7 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
 __global__ void moe_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ idx,
                                    __nv_bfloat16* __restrict__ y, int T, int k, int E, int d, const uint32_t* err) {
   griddep_wait();
+  griddep_launch_dependents();
   if (err_set(err)) return;
   const int d4 = d / 4;
   const int64_t n = static_cast<int64_t>(T) * d4;
@@ -515,6 +525,15 @@ __global__ void moe_combine_kernel(const float* __restrict__ part, const int32_t
   }
 }
 
+// The rings of whichever NT up to NTMAX a unit runs with.
+template <int FMT, int NTMAX>
+int moe_w4_ring(int WK) {
+  int most = w4_ring_bytes<FMT, 1>(WK);
+  if constexpr (NTMAX > 1) most = std::max(most, w4_ring_bytes<FMT, 2>(WK));
+  if constexpr (NTMAX > 2) most = std::max({most, w4_ring_bytes<FMT, 3>(WK), w4_ring_bytes<FMT, 4>(WK)});
+  return most;
+}
+
 template <int FMT, int NTMAX, bool UP, bool LOCAL>
 cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s) {
   const int K = UP ? a.d : a.F;
@@ -522,11 +541,10 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
   const int entries = a.npairs < a.E ? a.npairs : a.E;  // active experts, at most
   constexpr bool W4 = FMT != kFmtBf16;
   const int steps = W4 ? w4_steps(K) : (K + kBfStep - 1) / kBfStep;
-  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX>(), W4 ? (NTMAX == 1 ? kMoeWarps : 2) : kMoeWarps / NTMAX,
-                      dev.num_sms);
+  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX>(), W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
   int smem;
   if constexpr (W4)
-    smem = w4_ring_bytes<FMT>() + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT)) : 0);
+    smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT)) : 0);
   else smem = bf_smem<NTMAX>(a.WK);
   auto kern = moe_product_kernel<FMT, NTMAX, UP, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(256)
   __shared__ uint32_t top;
   if (threadIdx.x == 0) top = 0u;
   griddep_wait();
+  griddep_launch_dependents();
   if (err_set(err)) return;
   __syncthreads();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
@@ -127,10 +128,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
   const int r0 = (static_cast<int>(blockIdx.x) * (kRowWarps / WK) + rg) * 16 * kRowTiles;
   const int n0 = static_cast<int>(blockIdx.y) * 8 * NT, count = min(rows - n0, 8 * NT);
   const int steps = w4_steps(K);
-  uint8_t* joins = smem + w4_ring_bytes<GROUP>();
+  uint8_t* joins = smem + w4_ring_bytes<GROUP, NT>(WK);
   // rows past the last one read the last one and store nothing
-  W4Stream<GROUP> stream{w4_rows<GROUP>(codes, scales, zeros, K, [&](int i) { return min(r0 + i, N - 1); }),
-                         smem + warp * w4_warp_bytes<GROUP>(), K, steps * wk / WK, steps * (wk + 1) / WK};
+  W4Stream<GROUP, NT> stream{w4_rows<GROUP>(codes, scales, zeros, K, [&](int i) { return min(r0 + i, N - 1); }),
+                             r0 < N, smem + warp * w4_warp_bytes<GROUP, NT>(), K, steps * wk / WK,
+                             steps * (wk + 1) / WK};
   if (r0 < N) stream.start();
   if constexpr (LOCAL) {
     in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
@@ -144,7 +146,14 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
   RowSums<NT> acc;
   clear<NT>(acc);
   auto act = [](int i) { return i; };
-  if (r0 < N) stream.template run<NT>(w4_cols<GROUP, NT>(in, K, count, act), acc);
+  if constexpr (NT > 1) {
+    stream.run_wide(in, count, act,
+                    smem + kRowWarps * w4_warp_bytes<GROUP, NT>() + wk * w4_xring_bytes<GROUP, NT>(), rg * 32 + lane,
+                    32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
+  } else if (r0 < N) {
+    stream.run(w4_cols<GROUP, NT>(in, K, count, act), acc);
+  }
+  griddep_launch_dependents();
   if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   if (wk != 0 || r0 >= N || failed != 0u) return;
   w4_unscale<NT>(acc, in.factor, count, act);
@@ -174,10 +183,9 @@ cudaError_t launch_linear(const void* x, const Staged& in, const W4Weight& w, co
                           int K, int N, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int kRows = 16 * kRowTiles;
   const int x_blocks = (rows + 8 * NT - 1) / (8 * NT);
-  // more slices of K mean that the warps of a CTA share less of the staged rows in L1
   const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), NT == 1 ? 3 : 2,
-                              NT == 1 ? kRowWarps : 2, dev.num_sms);
-  const int smem = w4_ring_bytes<GROUP>() + joins_bytes<NT>(WK) +
+                              w4_most_split<NT>(), dev.num_sms);
+  const int smem = w4_ring_bytes<GROUP, NT>(WK) + joins_bytes<NT>(WK) +
                    (LOCAL ? static_cast<int>(w4_staged_bytes(rows, K, GROUP)) : 0);
   auto kern = w4_linear_kernel<GROUP, NT, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
@@ -199,9 +207,14 @@ cudaError_t launch_linear_g(const void* x, const W4Weight& w, const void* bias, 
   cudaError_t e = launch_pdl(w4_stage_kernel<GROUP>, dim3(grid), dim3(256), 0, s,
                              static_cast<const __nv_bfloat16*>(x), in, rows, K, static_cast<const uint32_t*>(dev.err));
   if (e != cudaSuccess) return e;
-  if (rows <= 8) return launch_linear<GROUP, 1, false>(x, in, w, bias, y, rows, K, N, dev, s);
-  if (rows <= 16) return launch_linear<GROUP, 2, false>(x, in, w, bias, y, rows, K, N, dev, s);
-  return launch_linear<GROUP, 4, false>(x, in, w, bias, y, rows, K, N, dev, s);
+  // blocks of up to four column tiles, as even as it goes
+  const int tiles = (rows + 7) / 8, blocks = (tiles + 3) / 4;
+  switch ((tiles + blocks - 1) / blocks) {
+    case 1: return launch_linear<GROUP, 1, false>(x, in, w, bias, y, rows, K, N, dev, s);
+    case 2: return launch_linear<GROUP, 2, false>(x, in, w, bias, y, rows, K, N, dev, s);
+    case 3: return launch_linear<GROUP, 3, false>(x, in, w, bias, y, rows, K, N, dev, s);
+    default: return launch_linear<GROUP, 4, false>(x, in, w, bias, y, rows, K, N, dev, s);
+  }
 }
 
 template <int GROUP>

@@ -166,33 +166,20 @@ static __device__ __forceinline__ void w4_stage_local(const Staged& out, int cou
   __syncthreads();
 }
 
-// c += a b, or c = a b.  PINNED keeps the order of the source: without it the loads
-// of all pieces are moved to the front of a step, for which NT > 2 has no registers.
-template <bool FIRST, bool PINNED>
+// c += a b, or (FIRST) c = a b.
+template <bool FIRST>
 static __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-#define DG_MMA "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-#define DG_IN "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1)
-  if constexpr (FIRST && PINNED)
-    asm volatile(DG_MMA "{%10, %10, %10, %10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : DG_IN, "f"(0.0f));
-  else if constexpr (FIRST)
-    asm(DG_MMA "{%10, %10, %10, %10};" : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : DG_IN, "f"(0.0f));
-  else if constexpr (PINNED)
-    asm volatile(DG_MMA "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : DG_IN);
+  if constexpr (FIRST)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
   else
-    asm(DG_MMA "{%0, %1, %2, %3};" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : DG_IN);
-#undef DG_MMA
-#undef DG_IN
-}
-
-template <bool PINNED>
-static __device__ __forceinline__ uint4 ld_piece(const uint8_t* p) {
-  if constexpr (!PINNED) return *reinterpret_cast<const uint4*>(p);
-  uint4 v;
-  asm volatile("ld.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // A warp's rows of a 4-bit weight.
@@ -214,29 +201,50 @@ struct W4Cols {
   uint32_t frag[NT], sums[NT][2];
 };
 
-// Each warp keeps kW4Ring - 1 steps of its rows' codes on the way from HBM in a
+// Each warp keeps w4_ring - 1 steps of its rows' codes on the way from HBM in a
 // ring of its own, filled by 16-byte asynchronous copies.  A row's 64 bytes of a
 // step are swizzled by pieces of 16, so that reads of a piece, half a piece or a
 // word a lane all spread over the banks.
-constexpr int kW4Ring = 3;
+template <int NT>
+constexpr int w4_ring() {
+  return NT > 2 ? 2 : 3;  // two CTAs an SM
+}
 constexpr int kW4StepBytes = kLaneRows * 512;
 // Behind the codes: {-zero point, scale} of the warp's 32 rows, [G][32], two steps.
-template <int GROUP>
+template <int GROUP, int NT>
 constexpr int w4_warp_bytes() {
-  return kW4Ring * kW4StepBytes + 2 * 256 * (kW4Step / GROUP);
+  return w4_ring<NT>() * kW4StepBytes + 2 * 256 * (kW4Step / GROUP);
 }
-template <int GROUP>
-constexpr int w4_ring_bytes() {  // of a CTA
-  return kRowWarps * w4_warp_bytes<GROUP>();
+// NT > 1: the staged activations of a slice of K, brought to shared memory once for
+// its warps, by steps: fragments in the order the lanes take them, [4][NT][32 lanes]
+// of 16 bytes, and the sums, [8*NT][G].
+template <int GROUP, int NT>
+constexpr int w4_xstep_bytes() {
+  return NT * 2048 + 8 * NT * 4 * (kW4Step / GROUP);
+}
+template <int GROUP, int NT>
+constexpr int w4_xring_bytes() {
+  return NT > 1 ? w4_ring<NT>() * w4_xstep_bytes<GROUP, NT>() : 0;
+}
+// The rings of a CTA whose warps split K WK ways.
+template <int GROUP, int NT>
+constexpr int w4_ring_bytes(int WK) {
+  return kRowWarps * w4_warp_bytes<GROUP, NT>() + WK * w4_xring_bytes<GROUP, NT>();
+}
+// More slices of K would need more room than two CTAs an SM have.
+template <int NT>
+constexpr int w4_most_split() {
+  return NT == 1 ? kRowWarps : 2;
 }
 
-// One step's product.  slot: its codes; zs: {-zero point, scale} of the warp's rows.
+// One step's product.  slot: its codes; zs: {-zero point, scale} of the warp's rows;
+// xstep (NT > 1): the step's activations in shared memory.
 template <int GROUP, int NT>
-static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Cols<NT>& x, int c,
-                                              int groups, RowSums<NT>& acc) {
+static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Cols<NT>& x,
+                                              const uint8_t* xstep, int c, int groups, RowSums<NT>& acc) {
   constexpr int G = kW4Step / GROUP;  // groups a step
   constexpr int W = GROUP / 32;       // code words of a row and group a lane takes
-  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int swz = (g >> 1) & 3;
   // sums of the columns 8n + 2t and 8n + 2t + 1, all groups of the step
   float xsum[NT][2][G];
@@ -244,7 +252,8 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* p = x.xsums + static_cast<uint64_t>(x.sums[n][i]) + c * G;
+      const float* p = NT > 1 ? reinterpret_cast<const float*>(xstep + NT * 2048) + (8 * n + 2 * t + i) * G
+                              : x.xsums + static_cast<uint64_t>(x.sums[n][i]) + c * G;
       if constexpr (G == 4) *reinterpret_cast<float4*>(xsum[n][i]) = *reinterpret_cast<const float4*>(p);
       else if constexpr (G == 2) *reinterpret_cast<float2*>(xsum[n][i]) = *reinterpret_cast<const float2*>(p);
       else xsum[n][i][0] = *p;
@@ -274,7 +283,9 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
           uint4 b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = ld_piece<(NT > 2)>(x.xs + (static_cast<uint64_t>(x.frag[n]) + 16 * c) * 16 + (q * W + j) * 64);
+            b[n] = *reinterpret_cast<const uint4*>(
+                NT > 1 ? xstep + ((q * W + j) * NT + n) * 512 + lane * 16
+                       : x.xs + (static_cast<uint64_t>(x.frag[n]) + 16 * c) * 16 + (q * W + j) * 64);
 #pragma unroll
           for (int m = 0; m < kTogether; ++m) {
             const uint32_t l = code[2 * m][j], h = code[2 * m + 1][j];
@@ -282,12 +293,12 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               if (j == 0)
-                mma_f16<true, (NT > 2)>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
+                mma_f16<true>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
                                         h & 0x00f000f0u, b[n].x, b[n].y);
               else
-                mma_f16<false, (NT > 2)>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
+                mma_f16<false>(part[m][n], l & 0x000f000fu, h & 0x000f000fu, l & 0x00f000f0u,
                                          h & 0x00f000f0u, b[n].x, b[n].y);
-              mma_f16<false, (NT > 2)>(part[m][n], l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u,
+              mma_f16<false>(part[m][n], l8 & 0x000f000fu, h8 & 0x000f000fu, l8 & 0x00f000f0u,
                                        h8 & 0x00f000f0u, b[n].z, b[n].w);
             }
           }
@@ -310,12 +321,15 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
   }
 }
 
-// The codes and scales of steps [c0, c1) of a warp's rows.  start() is apart from
-// run(), so that a kernel can ask for them before it has its activations.
-template <int GROUP>
+// The codes and scales of steps [c0, c1) of a warp's rows, for up to 8*NT columns.
+// start() is apart from run(), so that a kernel with NT = 1 can ask for them before
+// it has its activations.
+template <int GROUP, int NT>
 struct W4Stream {
   static constexpr int G = kW4Step / GROUP;
+  static constexpr int R = w4_ring<NT>();
   W4Rows w;
+  bool active;    // the warp has rows
   uint8_t* ring;  // this warp's w4_warp_bytes
   int K, c0, c1;
   // scales and zero points of row `lane`, of the step after the last one decoded, as they lie in memory
@@ -323,17 +337,17 @@ struct W4Stream {
 
   __device__ __forceinline__ void fill(int c, int u) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const bool in = c < c1 && c * kW4Step + 32 * t < K;
+    const bool in = active && c < c1 && c * kW4Step + 32 * t < K;
     const int64_t at = in ? static_cast<int64_t>(c) * 64 + 16 * t : 0;
     const uint32_t dst = smem_u32(ring) + u * kW4StepBytes + g * 64 + (t ^ ((g >> 1) & 3)) * 16;
     cp_async16(dst, w.codes + at, in);
     cp_async16(dst + 512, w.codes + w.next0 + at, in);
     cp_async16(dst + 1024, w.codes1 + at, in);
     cp_async16(dst + 1536, w.codes1 + w.next1 + at, in);
-    cp_async_commit();
+    if (NT == 1) cp_async_commit();
   }
   __device__ __forceinline__ void load_scales(int c) {
-    if (c >= c1) return;
+    if (!active || c >= c1) return;
     const int64_t at = static_cast<int64_t>(c) * G;
     if (G == 1 || K % kW4Step == 0) {  // every row's scales start on a boundary of the vector
       if constexpr (G == 4) {
@@ -359,7 +373,7 @@ struct W4Stream {
     }
   }
   __device__ __forceinline__ uint8_t* decoded(int parity) const {
-    return ring + kW4Ring * kW4StepBytes + parity * 256 * G;
+    return ring + R * kW4StepBytes + parity * 256 * G;
   }
   __device__ __forceinline__ void decode(int parity) const {
 #pragma unroll
@@ -373,36 +387,91 @@ struct W4Stream {
   }
   __device__ __forceinline__ void start() {
     load_scales(c0);
+    if constexpr (NT == 1) {
 #pragma unroll
-    for (int u = 0; u < kW4Ring - 1; ++u) fill(c0 + u, u);
+      for (int u = 0; u < R - 1; ++u) fill(c0 + u, u);
+    }
   }
-  // acc += the product, in units of 2^-24 / factor, with up to 8*NT staged activation
-  // rows.  Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t,
-  // 8n + 2t + 1; row g + 8, the same).
-  template <int NT>
+  // acc += the product with staged activation rows, in units of 2^-24 / factor.
+  // Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t, 8n + 2t + 1;
+  // row g + 8, the same).  NT = 1: an active warp by itself, the lanes read `x`.
   __device__ __forceinline__ void run(const W4Cols<NT>& x, RowSums<NT>& acc) {
     const int groups = K / GROUP;
     decode(0);
     load_scales(c0 + 1);
     int parity = 0;
 #pragma unroll 1
-    for (int c = c0; c < c1; c += kW4Ring) {
+    for (int c = c0; c < c1; c += R) {
 #pragma unroll
-      for (int u = 0; u < kW4Ring; ++u) {
+      for (int u = 0; u < R; ++u) {
         if (c + u >= c1) break;
-        cp_async_wait<kW4Ring - 2>();
+        cp_async_wait<R - 2>();
         // the other lanes' copies and scales are in place, and what the step before has read is free
         __syncwarp();
-        fill(c + u + kW4Ring - 1, (u + kW4Ring - 1) % kW4Ring);
+        fill(c + u + R - 1, (u + R - 1) % R);
         const uint8_t* zs = decoded(parity);
         parity ^= 1;
         decode(parity);
         load_scales(c + u + 2);
-        w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, x, c + u, groups, acc);
+        w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, x, nullptr, c + u, groups, acc);
       }
     }
     cp_async_wait<0>();
     __syncwarp();
+  }
+  // The same for NT > 1: all warps of the CTA together, with the same `steps` >=
+  // c1 - c0.  xring: the w4_xring_bytes of this warp's slice, filled by its `nx`
+  // threads, of which this is number `ix`.  act(i): index of the staged row of column
+  // i, for i < count; other columns get the last one and are not used.
+  template <typename Act>
+  __device__ __forceinline__ void run_wide(const Staged& in, int count, Act act, uint8_t* xring, int ix, int nx,
+                                           int steps, RowSums<NT>& acc) {
+    constexpr int kX = w4_xstep_bytes<GROUP, NT>();
+    const int groups = K / GROUP, tiles = (count + 7) / 8;
+    const int64_t rb = w4_row_bytes(K);
+    const int fs = w4_row_sums(K, GROUP);
+    auto fill_all = [&](int c, int u) {
+      fill(c, u);
+      if (c < c1) {
+        const uint32_t to = smem_u32(xring) + u * kX;
+        for (int i = ix; i < tiles * 128; i += nx) {  // 16 pieces a row, as they lie in the staged row
+          const int row = i / 16, p = i % 16;         // p = 4 * (piece of a lane) + t
+          cp_async16(to + ((p / 4) * NT + row / 8) * 512 + ((row % 8) * 4 + p % 4) * 16,
+                     in.frag + act(min(row, count - 1)) * rb + static_cast<int64_t>(c) * 256 + p * 16, true);
+        }
+        for (int row = ix; row < tiles * 8; row += nx) {
+          const float* from = in.sums + act(min(row, count - 1)) * static_cast<int64_t>(fs) + c * G;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + NT * 2048 + row * 4 * G), "l"(from),
+                       "n"(4 * G)
+                       : "memory");
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int u = 0; u < R - 1; ++u) fill_all(c0 + u, u);
+    decode(0);
+    load_scales(c0 + 1);
+    int parity = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < steps; s0 += R) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        if (s0 + u >= steps) break;
+        const int c = c0 + s0 + u;
+        cp_async_wait<R - 2>();
+        __syncthreads();  // the step is in place, and what the step before has read is free
+        fill_all(c + R - 1, (u + R - 1) % R);
+        const uint8_t* zs = decoded(parity);
+        parity ^= 1;
+        decode(parity);
+        load_scales(c + 2);
+        if (active && c < c1)
+          w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, W4Cols<NT>{}, xring + u * kX, c, groups, acc);
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // the rings may be filled again
   }
 };
 

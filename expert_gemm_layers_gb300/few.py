@@ -9,23 +9,38 @@ require gradients are taken as constants.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from ._lib import DG_ERROR_BLOCK_BYTES, DG_MOE_RENORM, DG_MOE_SIGMOID, MoEShape, check, load
-from .ops import _need, _stream, alloc_workspace, error_block
+from .ops import _need, alloc_workspace
 
 __all__ = ["w4_quantize", "w4_dequantize", "w4_linear", "moe_route", "moe_swiglu", "moe_swiglu_w4", "moe_layer"]
 
 
-def _launch(fn, dev: torch.device, *args) -> None:
-    """fn(*args, stream) with `dev` current."""
-    if torch.cuda.current_device() == dev.index:
-        check(fn(*args, _stream(dev)))
+# A decode step makes many of these calls, each a few microseconds of GPU work,
+# so what the host does per call is kept short: one expression per tensor (the
+# slow, exact check runs only to say what is wrong) and the stream as a number.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+BF16, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+
+
+def _check(t, name: str, dtype, shape, like: torch.Tensor) -> None:
+    """_need(t, name, dtype, shape, like.device), fast where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == like.get_device() and t.is_cuda and t.is_contiguous()):
+        _need(t, name, dtype, shape, like.device)
+
+
+def _launch(fn, index: int, *args) -> None:
+    """fn(*args, current stream) with device `index` current."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            check(fn(*args, _stream(dev)))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        check(status)
 
 
 def _p(t):
@@ -35,40 +50,38 @@ def _p(t):
 _scratch_cache: dict = {}
 
 
-def _scratch(dev: torch.device, nbytes: int) -> torch.Tensor:
+def _scratch(index: int, nbytes: int) -> torch.Tensor:
     """The workspace this module gives calls that bring none: one per (device,
     current stream), grown as needed, its error block zeroed when it is made.
     A captured call gets one of its own, in the graph's memory, so that graphs
     captured on one stream do not share it."""
-    if nbytes <= DG_ERROR_BLOCK_BYTES:
-        return error_block(dev)
-    if torch.cuda.is_current_stream_capturing():
-        return alloc_workspace(nbytes, dev)
-    key = (dev.index, _stream(dev))
+    key = (index, _raw_stream(index))
     ws = _scratch_cache.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _scratch_cache[key] = alloc_workspace(nbytes, dev)
+    if ws is None or ws.numel() < nbytes or torch.cuda.is_current_stream_capturing():
+        ws = alloc_workspace(max(nbytes, DG_ERROR_BLOCK_BYTES), torch.device("cuda", index))
+        if not torch.cuda.is_current_stream_capturing():
+            _scratch_cache[key] = ws
     return ws
 
 
-def _need_workspace(ws: torch.Tensor, nbytes: int, dev: torch.device) -> None:
-    _need(ws, "workspace", torch.uint8, None, dev)
+def _need_workspace(ws: torch.Tensor, nbytes: int, like: torch.Tensor) -> None:
+    _check(ws, "workspace", U8, ws.shape if isinstance(ws, torch.Tensor) else None, like)
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")
 
 
 # ------------------------------------------------------------------ 4-bit weights
 
-def _need_w4(codes, scales, zeros, lead: tuple, K: int, dev, what: str) -> int:
+def _need_w4(codes, scales, zeros, lead: tuple, K: int, like, what: str) -> int:
     """Checks one 4-bit weight [*lead, K]; returns its group size."""
-    _need(codes, f"{what}codes", torch.uint8, (*lead, K // 2), dev)
-    if not isinstance(scales, torch.Tensor) or scales.dim() != codes.dim() or scales.shape[-1] < 1 \
-            or K % scales.shape[-1]:
+    _check(codes, what + "codes", U8, (*lead, K // 2), like)
+    groups = scales.shape[-1] if isinstance(scales, torch.Tensor) and scales.dim() == codes.dim() else 0
+    if groups < 1 or K % groups:
         raise ValueError(f"{what}scales must be [..., K/group] beside codes [..., K/2]")
-    _need(scales, f"{what}scales", torch.bfloat16, (*lead, scales.shape[-1]), dev)
+    _check(scales, what + "scales", BF16, (*lead, groups), like)
     if zeros is not None:
-        _need(zeros, f"{what}zeros", torch.uint8, scales.shape, dev)
-    return K // scales.shape[-1]
+        _check(zeros, what + "zeros", U8, scales.shape, like)
+    return K // groups
 
 
 def w4_quantize(weight: torch.Tensor, group: int = 128, zero_points: bool = False):
@@ -87,7 +100,7 @@ def w4_quantize(weight: torch.Tensor, group: int = 128, zero_points: bool = Fals
     scales = torch.empty((*lead, K // group), dtype=torch.bfloat16, device=dev)
     zeros = torch.empty((*lead, K // group), dtype=torch.uint8, device=dev) if zero_points else None
     rows = weight.numel() // K if K else 0
-    _launch(lib.dg_w4_quantize, dev, rows, K, group, _p(weight), _p(codes), _p(scales), _p(zeros))
+    _launch(lib.dg_w4_quantize, weight.get_device(), rows, K, group, _p(weight), _p(codes), _p(scales), _p(zeros))
     return codes, scales, zeros
 
 
@@ -97,11 +110,12 @@ def w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
     lib = load()
     _need(codes, "codes", torch.uint8)
     K, lead, dev = 2 * codes.shape[-1], codes.shape[:-1], codes.device
-    group = _need_w4(codes, scales, zeros, tuple(lead), K, dev, "")
+    group = _need_w4(codes, scales, zeros, tuple(lead), K, codes, "")
     if out is None:
         out = torch.empty((*lead, K), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, (*lead, K), dev)
-    _launch(lib.dg_w4_dequantize, dev, out.numel() // K if K else 0, K, group, _p(codes), _p(scales), _p(zeros), _p(out))
+    else:
+        _need(out, "out", torch.bfloat16, (*lead, K), dev)
+    _launch(lib.dg_w4_dequantize, codes.get_device(), out.numel() // K if K else 0, K, group, _p(codes), _p(scales), _p(zeros), _p(out))
     return out
 
 
@@ -115,21 +129,20 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     stream's own), and scratch where there are more than few short rows
     (dg_w4_linear_workspace_bytes)."""
     lib = load()
-    in_f, dev = x.shape[-1], x.device
-    _need(x, "x", torch.bfloat16)
-    out_f = codes.shape[0]
-    group = _need_w4(codes, scales, zeros, (out_f,), in_f, dev, "")
+    lead, in_f, out_f = x.shape[:-1], x.shape[-1], codes.shape[0]
+    _check(x, "x", BF16, x.shape, x)
+    group = _need_w4(codes, scales, zeros, (out_f,), in_f, x, "")
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, (out_f,), dev)
+        _check(bias, "bias", BF16, (out_f,), x)
     if out is None:
-        out = torch.empty((*x.shape[:-1], out_f), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((*lead, out_f), dtype=BF16, device=x.device)
     else:
-        _need(out, "out", torch.bfloat16, (*x.shape[:-1], out_f), dev)
-    rows = x.numel() // in_f if in_f else 0
+        _check(out, "out", BF16, (*lead, out_f), x)
+    rows, index = x.numel() // in_f if in_f else 0, x.get_device()
     if ws is None:
-        ws = _scratch(dev, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f))
-    _launch(lib.dg_w4_linear, dev, rows, in_f, out_f, group, _p(x), _p(codes), _p(scales), _p(zeros),
-            _p(bias), _p(out), _p(ws), ws.numel())
+        ws = _scratch(index, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f))
+    _launch(lib.dg_w4_linear, index, rows, in_f, out_f, group, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            _p(zeros), _p(bias), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -148,41 +161,40 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     lib = load()
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    _need(x, "x", torch.bfloat16)
     T, d = x.shape
-    E, dev = w_router.shape[0], x.device
-    _need(w_router, "w_router", torch.bfloat16, (E, d), dev)
+    E, dev, index = w_router.shape[0], x.device, x.get_device()
+    _check(x, "x", BF16, (T, d), x)
+    _check(w_router, "w_router", BF16, (E, d), x)
     flags = (DG_MOE_SIGMOID if score == "sigmoid" else 0) | (DG_MOE_RENORM if renormalize else 0)
-    idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    gates = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    idx = torch.empty((T, top_k), dtype=I32, device=dev)
+    gates = torch.empty((T, top_k), dtype=F32, device=dev)
     nbytes = lib.dg_moe_route_workspace_bytes(T, d, E, top_k)
     if workspace is None:
-        workspace = _scratch(dev, nbytes)
+        workspace = _scratch(index, nbytes)
     else:
-        _need_workspace(workspace, nbytes, dev)
-    _launch(lib.dg_moe_route, dev, T, d, E, top_k, flags, float(scale), _p(x), _p(w_router), _p(idx), _p(gates),
-            _p(workspace), workspace.numel())
+        _need_workspace(workspace, nbytes, x)
+    _launch(lib.dg_moe_route, index, T, d, E, top_k, flags, scale, x.data_ptr(), w_router.data_ptr(), idx.data_ptr(),
+            gates.data_ptr(), workspace.data_ptr(), workspace.numel())
     return idx, gates
 
 
 def _moe_args(x, idx, gates, workspace, out, F: int, E: int, group: int):
     """Checks the tensors both weight formats share; returns (shape, workspace, out)."""
-    _need(x, "x", torch.bfloat16)
     T, d = x.shape
-    dev = x.device
     k = idx.shape[-1]
-    _need(idx, "idx", torch.int32, (T, k), dev)
-    _need(gates, "gates", torch.float32, (T, k), dev)
+    _check(x, "x", BF16, (T, d), x)
+    _check(idx, "idx", I32, (T, k), x)
+    _check(gates, "gates", F32, (T, k), x)
     sh = MoEShape(T, d, F, E, k)
-    nbytes = load().dg_moe_swiglu_workspace_bytes(ctypes.byref(sh), group)
+    nbytes = load().dg_moe_swiglu_workspace_bytes(sh, group)
     if workspace is None:
-        workspace = _scratch(dev, nbytes)
+        workspace = _scratch(x.get_device(), nbytes)
     elif nbytes:
-        _need_workspace(workspace, nbytes, dev)
+        _need_workspace(workspace, nbytes, x)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _need(out, "out", torch.bfloat16, (T, d), dev)
+        _check(out, "out", BF16, (T, d), x)
     return sh, workspace, out
 
 
@@ -198,11 +210,11 @@ def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: tor
     lib = load()
     d = x.shape[-1]
     E, F = w13.shape[0], w13.shape[1] // 2
-    _need(w13, "w13", torch.bfloat16, (E, 2 * F, d), x.device)
-    _need(w2, "w2", torch.bfloat16, (E, d, F), x.device)
+    _check(w13, "w13", BF16, (E, 2 * F, d), x)
+    _check(w2, "w2", BF16, (E, d, F), x)
     sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, 0)
-    _launch(lib.dg_moe_swiglu, x.device, ctypes.byref(sh), _p(x), _p(idx), _p(gates), _p(w13), _p(w2), _p(out),
-            _p(workspace), workspace.numel())
+    _launch(lib.dg_moe_swiglu, x.get_device(), sh, x.data_ptr(), idx.data_ptr(), gates.data_ptr(), w13.data_ptr(),
+            w2.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -211,15 +223,16 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
     """moe_swiglu with 4-bit experts: w13 and w2 are (codes, scales, zeros) of [E, 2F, d] and [E, d, F]
     (w4_quantize of the bf16 tensors), of one group size, both with zero points or both without."""
     lib = load()
-    d, dev = x.shape[-1], x.device
+    d = x.shape[-1]
     (c13, s13, z13), (c2, s2, z2) = w13, w2
     E, F = c13.shape[0], c13.shape[1] // 2
-    group = _need_w4(c13, s13, z13, (E, 2 * F), d, dev, "w13 ")
-    if _need_w4(c2, s2, z2, (E, d), F, dev, "w2 ") != group:
+    group = _need_w4(c13, s13, z13, (E, 2 * F), d, x, "w13 ")
+    if _need_w4(c2, s2, z2, (E, d), F, x, "w2 ") != group:
         raise ValueError("w13 and w2 must have the same group size")
     sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, group)
-    _launch(lib.dg_moe_swiglu_w4, dev, ctypes.byref(sh), group, _p(x), _p(idx), _p(gates), _p(c13), _p(s13), _p(z13),
-            _p(c2), _p(s2), _p(z2), _p(out), _p(workspace), workspace.numel())
+    _launch(lib.dg_moe_swiglu_w4, x.get_device(), sh, group, x.data_ptr(), idx.data_ptr(), gates.data_ptr(),
+            c13.data_ptr(), s13.data_ptr(), _p(z13), c2.data_ptr(), s2.data_ptr(), _p(z2), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return out
 
 
