@@ -390,7 +390,7 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const int* pai
 // its `count` pairs as columns.
 template <int FMT, int NT, bool UP, bool LOCAL>
 __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int* pairs, int count, int b, int rg,
-                                         int wk, uint8_t* smem, uint32_t* tops, bool failed) {
+                                         int wk, uint8_t* smem, bool failed) {
   const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
   const int K = UP ? a.d : a.F, rows = UP ? 2 * a.F : a.d, WK = a.WK;
   const bool active = UP ? b * 16 < a.F : b * 32 < a.d;
@@ -429,7 +429,7 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
     if constexpr (LOCAL) {  // the unit's rows, in shared memory
       in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, FMT);
       __syncthreads();  // the last unit's rows have been read
-      w4_stage_local<FMT>(in, count, K, tops, [&](int i) { return a.in + act(i) * a.in_stride; });
+      w4_stage_local<FMT>(in, count, K, [&](int i) { return a.in + act(i) * a.in_stride; });
     }
     auto column = [&](int i) { return LOCAL ? i : act(i); };
     if constexpr (NT > 1) {
@@ -437,9 +437,9 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
                       smem + kRowWarps * w4_warp_bytes<FMT, NT>() + wk * w4_xring_bytes<FMT, NT>(), rg * 32 + lane,
                       32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
     } else if (active) {
-      stream.run(w4_cols<FMT, NT>(in, K, count, column), acc);
+      stream.template run<LOCAL>(w4_cols<FMT, NT>(in, K, count, column), acc);
     }
-    if (active) w4_unscale<NT>(acc, in.factor, count, column);
+    if (active) w4_unscale<NT>(acc, LOCAL ? nullptr : in.factor, count, column);
     if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   }
   if (wk == 0 && active && !failed) store_block<NT, UP>(a, pairs, count, b, acc);
@@ -459,7 +459,6 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
     moe_product_kernel(const __grid_constant__ ProductArgs a, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int small_map[LOCAL ? 4 + 3 * 64 + 32 : 1];
-  __shared__ uint32_t tops[8];
   griddep_wait();
   const bool failed = ld_volatile_u32(err) != 0u;  // looked at before anything is written
   PairMap m = a.map;
@@ -480,21 +479,21 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
     const int* pairs = m.pairs + m.start[entry];
     if constexpr (NTMAX >= 4) {
       if (count > 24) {
-        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
+        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
       if (count > 16) {
-        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
+        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
     }
     if constexpr (NTMAX >= 2) {
       if (count > 8) {
-        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
+        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
     }
-    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, tops, failed);
+    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
   }
 }
 
@@ -544,7 +543,7 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
   a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX>(), W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
   int smem;
   if constexpr (W4)
-    smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT)) : 0);
+    smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT, true)) : 0);
   else smem = bf_smem<NTMAX>(a.WK);
   auto kern = moe_product_kernel<FMT, NTMAX, UP, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
@@ -616,7 +615,8 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   const int cap = c.T < 8 * ntmax ? c.T : 8 * ntmax;
   bool local = npairs <= 32 && cap <= 8;
   if constexpr (W4)
-    local = local && w4_staged_bytes(cap, c.d, FMT) <= kLocalBytes && w4_staged_bytes(cap, c.F, FMT) <= kLocalBytes;
+    local = local && w4_staged_bytes(cap, c.d, FMT, true) <= kLocalBytes &&
+            w4_staged_bytes(cap, c.F, FMT, true) <= kLocalBytes;
   if (local) ntmax = 1;
   ProductArgs a{};
   a.idx = static_cast<const int32_t*>(c.idx);

@@ -120,7 +120,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
                      const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N,
                      int WK, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t tops[8];
   griddep_wait();
   const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
   if (r0 < N) stream.start();
   if constexpr (LOCAL) {
     in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
-    w4_stage_local<GROUP>(in, count, K, tops,
+    w4_stage_local<GROUP>(in, count, K,
                           [&](int i) { return reinterpret_cast<const uint8_t*>(x + static_cast<int64_t>(n0 + i) * K); });
   } else {
     in.frag += n0 * w4_row_bytes(K);
@@ -151,12 +150,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
                     smem + kRowWarps * w4_warp_bytes<GROUP, NT>() + wk * w4_xring_bytes<GROUP, NT>(), rg * 32 + lane,
                     32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
   } else if (r0 < N) {
-    stream.run(w4_cols<GROUP, NT>(in, K, count, act), acc);
+    stream.template run<LOCAL>(w4_cols<GROUP, NT>(in, K, count, act), acc);
   }
   griddep_launch_dependents();
   if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
   if (wk != 0 || r0 >= N || failed != 0u) return;
-  w4_unscale<NT>(acc, in.factor, count, act);
+  w4_unscale<NT>(acc, LOCAL ? nullptr : in.factor, count, act);
 #pragma unroll
   for (int m = 0; m < kRowTiles; ++m)
 #pragma unroll
@@ -186,7 +185,7 @@ cudaError_t launch_linear(const void* x, const Staged& in, const W4Weight& w, co
   const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), NT == 1 ? 3 : 2,
                               w4_most_split<NT>(), dev.num_sms);
   const int smem = w4_ring_bytes<GROUP, NT>(WK) + joins_bytes<NT>(WK) +
-                   (LOCAL ? static_cast<int>(w4_staged_bytes(rows, K, GROUP)) : 0);
+                   (LOCAL ? static_cast<int>(w4_staged_bytes(rows, K, GROUP, true)) : 0);
   auto kern = w4_linear_kernel<GROUP, NT, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
   if (e != cudaSuccess) return e;
@@ -256,7 +255,7 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const vo
 // Up to 8 rows whose staged form takes no more than 32 KB are staged by every CTA
 // itself: reading 1 to 8 short rows costs less than another launch.
 bool w4_linear_local(int64_t rows, int64_t K, int group) {
-  return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group) <= 32 * 1024;
+  return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group, true) <= 32 * 1024;
 }
 
 size_t w4_linear_scratch_bytes(int64_t rows, int64_t K) {

@@ -9,8 +9,8 @@
 //    2^-24, and the tensor cores take such numbers exactly.  word & 0x00f000f0 is
 //    (16 q1, 16 q5) * 2^-24.  With word >> 8 that makes 5 operations for 8 codes
 //    (inserting an exponent and subtracting the zero point would take 11).
-//  - The activations are brought to that form once (w4_stage_row): a row is scaled
-//    by a power of two to magnitudes below 2^15, rounded to fp16, columns 1 3 5 7
+//  - The activations are brought to that form once (w4_stage_row, w4_stage_local): a
+//    row, or 128 columns of it, is scaled by a power of two to magnitudes below 2^15, rounded to fp16, columns 1 3 5 7
 //    of 8 divided by 16, in the order the lanes take them.  A bf16 number has 8
 //    significant bits, so it fits fp16's 11 exactly unless it is 2^28 times smaller
 //    than the row's largest; then it is off by at most 2^-40 of that largest, far
@@ -32,8 +32,9 @@ constexpr int kW4Step = 128;
 
 // Staged activations: of every row and step 256 bytes of fp16 (pieces of 8
 // columns, [piece of a lane][lane t]); of every row and group the sum of its scaled
-// columns; of every row the inverse of its scale.  Rows are padded by 64 bytes
-// against bank conflicts in shared memory.
+// columns; of every row (or, staged by the product's own CTA, every step of a row)
+// the inverse of its scale.  Rows are padded by 64 bytes against bank conflicts in
+// shared memory.
 struct Staged {
   uint8_t* frag;
   float* sums;
@@ -45,8 +46,9 @@ __host__ __device__ inline int w4_row_sums(int K, int group) { return w4_steps(K
 __host__ __device__ inline int64_t w4_sums_bytes(int64_t rows, int K, int group) {
   return (4 * rows * w4_row_sums(K, group) + 15) / 16 * 16;
 }
-__host__ __device__ inline int64_t w4_staged_bytes(int64_t rows, int K, int group) {
-  return rows * w4_row_bytes(K) + w4_sums_bytes(rows, K, group) + (4 * rows + 15) / 16 * 16;
+__host__ __device__ inline int64_t w4_staged_bytes(int64_t rows, int K, int group, bool step_factors = false) {
+  return rows * w4_row_bytes(K) + w4_sums_bytes(rows, K, group) +
+         (4 * rows * (step_factors ? w4_steps(K) : 1) + 15) / 16 * 16;
 }
 __host__ __device__ inline Staged w4_staged_at(uint8_t* p, int64_t rows, int K, int group) {
   float* sums = reinterpret_cast<float*>(p + rows * w4_row_bytes(K));
@@ -131,38 +133,26 @@ static __device__ __forceinline__ void w4_stage_row(const uint8_t* x, int K, uin
   __syncthreads();
 }
 
-// Stages up to 8 rows in shared memory by the 256 threads of a CTA, one after the
-// other in time only where their scales are concerned.  row(i): row i.  tops: 8
-// words.  Synchronises the CTA.
+// Stages up to 8 rows in shared memory by the 256 threads of a CTA.  row(i): row i.
+// Here every step has a scale of its own (factors[row * steps + step]): the row's
+// largest would take another pass and a barrier.  Synchronises the CTA.
 template <int GROUP, typename Row>
-static __device__ __forceinline__ void w4_stage_local(const Staged& out, int count, int K, uint32_t* tops, Row row) {
+static __device__ __forceinline__ void w4_stage_local(const Staged& out, int count, int K, Row row) {
   const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, steps = w4_steps(K), total = count * steps;
-  if (threadIdx.x < 8) tops[threadIdx.x] = 0u;
-  __syncthreads();
-  auto piece = [&](int i, int& r, int& st) {
-    r = count == 1 ? 0 : i / steps;
-    st = i - r * steps;
-    const int k = st * kW4Step + 8 * p;
-    return i < total && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * k) : make_uint4(0u, 0u, 0u, 0u);
-  };
-  for (int i = hw; i < total; i += 16) {
-    int r, st;
-    uint32_t top = w4_top(piece(i, r, st));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), top, o));
-    if (p == 0) atomicMax(&tops[r], top);
-  }
-  __syncthreads();
   const int64_t rb = w4_row_bytes(K);
   const int fs = w4_row_sums(K, GROUP);
   for (int i0 = 0; i0 < total; i0 += 16) {
-    const int i = i0 + hw;
-    int r, st;
-    const uint4 v = piece(i, r, st);
-    w4_stage_piece<GROUP>(v, w4_exponent(i < total ? tops[r] : 0u), p, st, i < total, out.frag + r * rb,
-                          out.sums + r * fs);
+    const int i = i0 + hw, r = count == 1 ? 0 : i / steps, st = i - r * steps, k = st * kW4Step + 8 * p;
+    const bool exists = i < total;
+    const uint4 v =
+        exists && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * k) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t top = w4_top(v);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int E = w4_exponent(top);
+    w4_stage_piece<GROUP>(v, E, p, st, exists, out.frag + r * rb, out.sums + r * fs);
+    if (exists && p == 0) out.factor[i] = __int_as_float((127 - 14 + E) << 23);
   }
-  if (threadIdx.x < count) out.factor[threadIdx.x] = __int_as_float((127 - 14 + w4_exponent(tops[threadIdx.x])) << 23);
   __syncthreads();
 }
 
@@ -198,7 +188,9 @@ template <int NT>
 struct W4Cols {
   const uint8_t* xs;
   const float* xsums;
+  const float* factors;  // of every step of a row, if every step has one
   uint32_t frag[NT], sums[NT][2];
+  int frow[2];  // rows of the columns 2t and 2t + 1, in steps from factors
 };
 
 // Each warp keeps w4_ring - 1 steps of its rows' codes on the way from HBM in a
@@ -239,7 +231,8 @@ constexpr int w4_most_split() {
 
 // One step's product.  slot: its codes; zs: {-zero point, scale} of the warp's rows;
 // xstep (NT > 1): the step's activations in shared memory.
-template <int GROUP, int NT>
+// STEP_FACTORS (NT = 1): the activations' factor of the step is applied too.
+template <int GROUP, int NT, bool STEP_FACTORS>
 static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Cols<NT>& x,
                                               const uint8_t* xstep, int c, int groups, RowSums<NT>& acc) {
   constexpr int G = kW4Step / GROUP;  // groups a step
@@ -258,6 +251,11 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
       else if constexpr (G == 2) *reinterpret_cast<float2*>(xsum[n][i]) = *reinterpret_cast<const float2*>(p);
       else xsum[n][i][0] = *p;
     }
+  float f0 = 1.0f, f1 = 1.0f;
+  if constexpr (STEP_FACTORS) {
+    f0 = x.factors[x.frow[0] + c];
+    f1 = x.factors[x.frow[1] + c];
+  }
 #pragma unroll
   for (int q = 0; q < G; ++q) {
     if (G == 1 || c * G + q < groups) {  // a group is whole or absent
@@ -310,10 +308,10 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float(&to)[4] = acc[m0 + m][n];
-            to[0] = fmaf(l.y, fmaf(l.x, xsum[n][0][q], part[m][n][0]), to[0]);
-            to[1] = fmaf(l.y, fmaf(l.x, xsum[n][1][q], part[m][n][1]), to[1]);
-            to[2] = fmaf(h.y, fmaf(h.x, xsum[n][0][q], part[m][n][2]), to[2]);
-            to[3] = fmaf(h.y, fmaf(h.x, xsum[n][1][q], part[m][n][3]), to[3]);
+            to[0] = fmaf(STEP_FACTORS ? l.y * f0 : l.y, fmaf(l.x, xsum[n][0][q], part[m][n][0]), to[0]);
+            to[1] = fmaf(STEP_FACTORS ? l.y * f1 : l.y, fmaf(l.x, xsum[n][1][q], part[m][n][1]), to[1]);
+            to[2] = fmaf(STEP_FACTORS ? h.y * f0 : h.y, fmaf(h.x, xsum[n][0][q], part[m][n][2]), to[2]);
+            to[3] = fmaf(STEP_FACTORS ? h.y * f1 : h.y, fmaf(h.x, xsum[n][1][q], part[m][n][3]), to[3]);
           }
         }
       }
@@ -395,6 +393,7 @@ struct W4Stream {
   // acc += the product with staged activation rows, in units of 2^-24 / factor.
   // Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t, 8n + 2t + 1;
   // row g + 8, the same).  NT = 1: an active warp by itself, the lanes read `x`.
+  template <bool STEP_FACTORS>
   __device__ __forceinline__ void run(const W4Cols<NT>& x, RowSums<NT>& acc) {
     const int groups = K / GROUP;
     decode(0);
@@ -413,7 +412,7 @@ struct W4Stream {
         parity ^= 1;
         decode(parity);
         load_scales(c + u + 2);
-        w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, x, nullptr, c + u, groups, acc);
+        w4_use<GROUP, NT, STEP_FACTORS>(ring + u * kW4StepBytes, zs, x, nullptr, c + u, groups, acc);
       }
     }
     cp_async_wait<0>();
@@ -467,7 +466,7 @@ struct W4Stream {
         decode(parity);
         load_scales(c + 2);
         if (active && c < c1)
-          w4_use<GROUP, NT>(ring + u * kW4StepBytes, zs, W4Cols<NT>{}, xring + u * kX, c, groups, acc);
+          w4_use<GROUP, NT, false>(ring + u * kW4StepBytes, zs, W4Cols<NT>{}, xring + u * kX, c, groups, acc);
       }
     }
     cp_async_wait<0>();
@@ -498,6 +497,8 @@ static __device__ __forceinline__ W4Cols<NT> w4_cols(const Staged& in, int K, in
   W4Cols<NT> x;
   x.xs = in.frag;
   x.xsums = in.sums;
+  x.factors = in.factor;
+  for (int i = 0; i < 2; ++i) x.frow[i] = static_cast<int>(act(min(2 * t + i, count - 1))) * w4_steps(K);
   const uint32_t rb = static_cast<uint32_t>(w4_row_bytes(K) / 16);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -509,7 +510,8 @@ static __device__ __forceinline__ W4Cols<NT> w4_cols(const Staged& in, int K, in
   return x;
 }
 
-// The sums are in units of 2^-24, those of the codes, and of their row's scale.
+// The sums are in units of 2^-24, those of the codes, and of their row's scale
+// (factor NULL: that has been applied).
 template <int NT, typename Act>
 static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc, const float* factor, int count, Act act) {
   const int t = threadIdx.x & 3;
@@ -517,7 +519,7 @@ static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc, const float*
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float f = factor[act(min(8 * n + 2 * t + i, count - 1))];
+      const float f = factor ? factor[act(min(8 * n + 2 * t + i, count - 1))] : 1.0f;
 #pragma unroll
       for (int m = 0; m < kRowTiles; ++m) {
         acc[m][n][i] = acc[m][n][i] * 16777216.0f * f;
