@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dg_internal.h"
 #include "dg_w4dot.cuh"
@@ -21,65 +22,147 @@ __device__ __forceinline__ bool err_set(const uint32_t* err) { return ld_volatil
 
 // ---------------------------------------------------------------- router
 
+// Two binary32 numbers at a time (packed arithmetic: half the instructions).
+struct Pair {
+  uint64_t v;
+};
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 floats_of(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) {
+  Pair r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // s + p without error: s becomes the rounded sum, c collects what was lost
 // (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(Pair& s, Pair& c, Pair p) {
+  const Pair t = s + p, z = t - s;
+  c = c + ((s - (t - z)) + (p - z));
+  s = t;
+}
 __device__ __forceinline__ void two_sum(float& s, float& c, float p) {
-  const float t = __fadd_rn(s, p);
-  const float z = __fsub_rn(t, s);
+  const float t = __fadd_rn(s, p), z = __fsub_rn(t, s);
   c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z)));
   s = t;
 }
 
 constexpr int kLogitWarps = 8;
 constexpr int kLogitTokens = 4;
+constexpr int kLogitExperts = 2;
 
-// logits[t, e]: a warp per expert and kLogitTokens tokens.  The choice of
-// experts hangs on the order of the logits, so the sums are kept in two words
-// (a bf16 product is exact in binary32, two_sum loses nothing) and rounded to
+// logits[t, e]: a warp takes kLogitExperts experts and kLogitTokens tokens, and one
+// of KS slices of d (KS > 1 where there are too few of both to fill the GPU).  The
+// choice of experts hangs on the order of the logits, so the sums are kept in two
+// words (a bf16 product is exact in binary32, two_sum loses nothing) and rounded to
 // binary32 once.
+template <int KS>
 __global__ void __launch_bounds__(kLogitWarps * 32)
     moe_logits_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr,
                       float* __restrict__ logits, int T, int d, int E, const uint32_t* err) {
+  __shared__ float2 slices[KS > 1 ? kLogitWarps : 1][kLogitExperts * kLogitTokens];
   griddep_wait();
   griddep_launch_dependents();
   if (err_set(err)) return;
-  const int lane = threadIdx.x & 31;
-  const int e = static_cast<int>(blockIdx.x) * kLogitWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e0 = (static_cast<int>(blockIdx.x) * (kLogitWarps / KS) + warp / KS) * kLogitExperts;
   const int t0 = static_cast<int>(blockIdx.y) * kLogitTokens;
-  if (e >= E) return;
-  const __nv_bfloat16* w = wr + static_cast<int64_t>(e) * d;
-  float s[kLogitTokens], c[kLogitTokens];
+  Pair s[kLogitExperts][kLogitTokens], c[kLogitExperts][kLogitTokens];
 #pragma unroll
-  for (int i = 0; i < kLogitTokens; ++i) s[i] = c[i] = 0.0f;
-  for (int k = 8 * lane; k < d; k += 256) {
-    const uint4 wv = *reinterpret_cast<const uint4*>(w + k);
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+  for (int j = 0; j < kLogitExperts; ++j)
 #pragma unroll
-    for (int i = 0; i < kLogitTokens; ++i) {
-      if (t0 + i >= T) break;
-      const uint4 xv = *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t0 + i) * d + k);
-      const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+    for (int i = 0; i < kLogitTokens; ++i) s[j][i] = c[j][i] = pair_of(0.0f, 0.0f);
+  // rows past the last one read the last one and are not stored
+  const __nv_bfloat16 *wp[kLogitExperts], *xp[kLogitTokens];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = unpack_bf16x2(ww[j]), b = unpack_bf16x2(xx[j]);
-        two_sum(s[i], c[i], __fmul_rn(a.x, b.x));
-        two_sum(s[i], c[i], __fmul_rn(a.y, b.y));
+  for (int j = 0; j < kLogitExperts; ++j) wp[j] = wr + static_cast<int64_t>(min(e0 + j, E - 1)) * d;
+#pragma unroll
+  for (int i = 0; i < kLogitTokens; ++i) xp[i] = x + static_cast<int64_t>(min(t0 + i, T - 1)) * d;
+  const int tokens = min(T - t0, kLogitTokens);
+  auto products = [&](auto full) {  // without branches where all tokens are there
+    constexpr bool kFull = decltype(full)::value;
+#pragma unroll 2
+    for (int k = 8 * (lane + 32 * (warp % KS)); k < d; k += 256 * KS) {
+      uint4 wv[kLogitExperts], xv[kLogitTokens];
+#pragma unroll
+      for (int j = 0; j < kLogitExperts; ++j) wv[j] = *reinterpret_cast<const uint4*>(wp[j] + k);
+#pragma unroll
+      for (int i = 0; i < kLogitTokens; ++i)
+        if (kFull || i < tokens) xv[i] = *reinterpret_cast<const uint4*>(xp[i] + k);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        auto two = [&](const uint4& v) {
+          const uint32_t u = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
+          return pair_of(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        };
+        Pair wq[kLogitExperts];
+#pragma unroll
+        for (int j = 0; j < kLogitExperts; ++j) wq[j] = two(wv[j]);
+#pragma unroll
+        for (int i = 0; i < kLogitTokens; ++i) {
+          if (kFull || i < tokens) {
+            const Pair xq = two(xv[i]);
+#pragma unroll
+            for (int j = 0; j < kLogitExperts; ++j) two_sum(s[j][i], c[j][i], wq[j] * xq);
+          }
+        }
       }
     }
+  };
+  if (e0 < E) {
+    if (tokens == kLogitTokens) products(std::true_type{});
+    else products(std::false_type{});
   }
 #pragma unroll
-  for (int i = 0; i < kLogitTokens; ++i) {
+  for (int j = 0; j < kLogitExperts; ++j)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float so = __shfl_xor_sync(0xffffffffu, s[i], o);
-      const float co = __shfl_xor_sync(0xffffffffu, c[i], o);
-      two_sum(s[i], c[i], so);
-      c[i] += co;
+    for (int i = 0; i < kLogitTokens; ++i) {
+      if (i >= tokens) continue;
+      const float2 s2 = floats_of(s[j][i]), c2 = floats_of(c[j][i]);
+      float sum = s2.x, low = c2.x + c2.y;
+      two_sum(sum, low, s2.y);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float so = __shfl_xor_sync(0xffffffffu, sum, o), lo = __shfl_xor_sync(0xffffffffu, low, o);
+        two_sum(sum, low, so);
+        low += lo;
+      }
+      if constexpr (KS > 1) {
+        if (lane == 0) slices[warp][j * kLogitTokens + i] = make_float2(sum, low);
+      } else if (lane == 0 && e0 + j < E) {
+        // an overflowed or non-finite sum makes its correction NaN: keep the sum itself
+        logits[static_cast<int64_t>(t0 + i) * E + e0 + j] = isfinite(sum) ? sum + low : sum;
+      }
     }
-    // an overflowed or non-finite sum makes its correction NaN: keep the sum itself
-    const float sum = s[i] + c[i];
-    if (lane == 0 && t0 + i < T)
-      logits[static_cast<int64_t>(t0 + i) * E + e] = isfinite(s[i]) ? sum : s[i];
+  if constexpr (KS > 1) {
+    __syncthreads();
+    const int v = lane, j = v / kLogitTokens, i = v % kLogitTokens;
+    if (warp % KS == 0 && v < kLogitExperts * kLogitTokens && e0 + j < E && i < tokens) {
+      float sum = slices[warp][v].x, low = slices[warp][v].y;
+      for (int k = 1; k < KS; ++k) {
+        two_sum(sum, low, slices[warp + k][v].x);
+        low += slices[warp + k][v].y;
+      }
+      logits[static_cast<int64_t>(t0 + i) * E + e0 + j] = isfinite(sum) ? sum + low : sum;
+    }
   }
 }
 
@@ -714,9 +797,14 @@ int moe_max_topk() { return kMaxTopk; }
 
 cudaError_t launch_moe_logits(const void* x, const void* wr, float* logits, int T, int d, int E, const DeviceInfo& dev,
                               cudaStream_t s) {
-  const dim3 grid((E + kLogitWarps - 1) / kLogitWarps, (T + kLogitTokens - 1) / kLogitTokens);
-  return launch_pdl(moe_logits_kernel, grid, dim3(kLogitWarps * 32), 0, s, static_cast<const __nv_bfloat16*>(x),
-                    static_cast<const __nv_bfloat16*>(wr), logits, T, d, E, static_cast<const uint32_t*>(dev.err));
+  const int pairs = (E + kLogitExperts - 1) / kLogitExperts, blocks = (T + kLogitTokens - 1) / kLogitTokens;
+  // a warp for every pair of experts and block of tokens; fewer than four warps an SM: eight
+  const bool split = static_cast<int64_t>(pairs) * blocks < 4 * dev.num_sms;
+  const int a_cta = split ? 1 : kLogitWarps;
+  return launch_pdl(split ? moe_logits_kernel<kLogitWarps> : moe_logits_kernel<1>,
+                    dim3((pairs + a_cta - 1) / a_cta, blocks), dim3(kLogitWarps * 32), 0, s,
+                    static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(wr), logits, T, d, E,
+                    static_cast<const uint32_t*>(dev.err));
 }
 
 cudaError_t launch_moe_topk(const float* logits, void* idx, void* gates, int T, int E, int k, bool sigmoid,

@@ -16,83 +16,162 @@ namespace {
 
 __device__ __forceinline__ bool err_set(const uint32_t* err) { return ld_volatile_u32(err) != 0u; }
 
-constexpr int kVecCols = 8;  // columns a thread handles: 16 bytes of bf16, 4 bytes of codes
+constexpr int kVecCols = 8;  // columns of a piece: 16 bytes of bf16, 4 bytes of codes
+constexpr int kQuantPieces = 4;  // pieces a thread has in flight
 
-// One thread per 8 columns; the GROUP / 8 lanes of a group agree on its scale
-// by shuffles.  A group with a NaN or an infinity, or whose range overflows
-// binary32, gets a NaN scale.
-template <int GROUP, bool ZEROS>
-__global__ void w4_quantize_kernel(const uint4* __restrict__ w, uint32_t* __restrict__ codes,
-                                   __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ zeros, int64_t vecs) {
-  griddep_wait();
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  // vecs is a multiple of the GROUP / 8 lanes of a group, so groups are whole;
-  // lanes past the end only keep the shuffles convergent
-  const bool in = v < vecs;
-  const uint4 raw = in ? __ldg(w + v) : make_uint4(0u, 0u, 0u, 0u);
-  const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
-  float f[8];
-  float lo = 0.0f, hi = 0.0f;
-  uint32_t top = 0u;  // largest magnitude, as bits: NaN > inf > finite
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack_bf16x2(word[i]);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
-    lo = fminf(lo, fminf(p.x, p.y));
-    hi = fmaxf(hi, fmaxf(p.x, p.y));
-    top = max(top, max(word[i] & 0x7fffu, (word[i] >> 16) & 0x7fffu));
-  }
-#pragma unroll
-  for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
-  if (!in) return;
-  const float quot = ZEROS ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(fmaxf(-lo, hi), 7.0f);
-  const bool finite = top < 0x7f80u && isfinite(quot);
-  __nv_bfloat16 sb = __float2bfloat16_rn(quot);
-  float s = __bfloat162float(sb);
-  if (s == 0.0f) s = 1.0f;
-  if (!finite) s = __int_as_float(0x7fc00000);
-  sb = __float2bfloat16_rn(s);
-  float z = 8.0f;
-  if (ZEROS && finite) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The codes of a piece: clamp(rne(w / s) + z, 0, 15), the quotient that of binary32
+// division, without dividing.  w and s have 8 significant bits, so w / s either is
+// n + 1/2 exactly or lies at least 2^-11 from it (|w / s| <= 16).  w * (1 / s) is
+// within 2^-18 of w / s.  Adding 768 rounds it to a multiple of 2^-14, which
+// restores the exact halves and moves nothing across one; adding 2^23 + 2^22 - 768
+// rounds that to an integer, halves to even, in the low bits.
+__device__ __forceinline__ uint32_t codes_of(const uint4& v, float inv, float z) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint64_t inv2 = f32x2(inv, inv), snap = f32x2(768.0f, 768.0f);
+  const float whole = 12582912.0f - 768.0f;
+  const uint64_t whole2 = f32x2(whole, whole);
+  const int zi = static_cast<int>(z);
   uint32_t code = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = finite ? fminf(fmaxf(rintf(__fdiv_rn(f[i], s)) + z, 0.0f), 15.0f) : z;
-    code |= static_cast<uint32_t>(q) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_bf16x2(w[i]);
+    const uint64_t n = add2(add2(mul2(f32x2(p.x, p.y), inv2), snap), whole2);
+    const int lo = static_cast<int>(static_cast<uint32_t>(n)) - 0x4b400000 + zi;
+    const int hi = static_cast<int>(static_cast<uint32_t>(n >> 32)) - 0x4b400000 + zi;
+    code |= static_cast<uint32_t>(min(max(lo, 0), 15)) << (8 * i);
+    code |= static_cast<uint32_t>(min(max(hi, 0), 15)) << (8 * i + 4);
   }
-  codes[v] = code;
-  if (v % (GROUP / kVecCols) == 0) {
-    const int64_t g = v / (GROUP / kVecCols);
-    scales[g] = sb;
-    if (ZEROS) zeros[g] = static_cast<uint8_t>(z);
+  return code;
+}
+
+// A thread takes pieces of 8 columns; the GROUP / 8 lanes of a group agree on its
+// scale by shuffles.  A group with a NaN or an infinity, or whose range overflows
+// binary32, gets a NaN scale.
+template <int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(256)
+    w4_quantize_kernel(const uint4* __restrict__ w, uint32_t* __restrict__ codes, __nv_bfloat16* __restrict__ scales,
+                       uint8_t* __restrict__ zeros, int64_t pieces) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kQuantPieces) + threadIdx.x;
+  uint4 raw[kQuantPieces];
+  // pieces is a multiple of the GROUP / 8 lanes of a group, so groups are whole;
+  // lanes past the end only keep the shuffles convergent
+#pragma unroll
+  for (int k = 0; k < kQuantPieces; ++k)
+    raw[k] = first + 256 * k < pieces ? __ldg(w + first + 256 * k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int k = 0; k < kQuantPieces; ++k) {
+    const int64_t v = first + 256 * k;
+    const uint32_t word[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    float quot;
+    uint32_t top = 0u;  // largest magnitude, as bf16 bits: NaN > inf > finite
+    float lo = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, word[i] & 0x7fff7fffu);
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (ZEROS) {
+      float hi = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 p = unpack_bf16x2(word[i]);
+        lo = fminf(lo, fminf(p.x, p.y));
+        hi = fmaxf(hi, fmaxf(p.x, p.y));
+      }
+#pragma unroll
+      for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      quot = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+    } else {
+      quot = __fdiv_rn(__uint_as_float(top << 16), 7.0f);
+    }
+    if (v >= pieces) continue;
+    const bool finite = top < 0x7f80u && isfinite(quot);
+    float s = __bfloat162float(__float2bfloat16_rn(quot));
+    if (s == 0.0f) s = 1.0f;
+    float z = 8.0f;
+    uint32_t code = 0x88888888u;
+    if (finite) {
+      if constexpr (ZEROS) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
+      if (s >= 7.9e-31f) {  // 2^-100: 1 / s is a normal number
+        code = codes_of(raw[k], __frcp_rn(s), z);
+      } else {
+        code = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 p = unpack_bf16x2(word[i / 2]);
+          const float q = fminf(fmaxf(rintf(__fdiv_rn(i & 1 ? p.y : p.x, s)) + z, 0.0f), 15.0f);
+          code |= static_cast<uint32_t>(q) << (4 * i);
+        }
+      }
+    }
+    codes[v] = code;
+    if (v % (GROUP / kVecCols) == 0) {
+      const int64_t g = v / (GROUP / kVecCols);
+      scales[g] = __float2bfloat16_rn(finite ? s : __int_as_float(0x7fc00000));
+      if (ZEROS) zeros[g] = static_cast<uint8_t>(z);
+    }
   }
 }
 
-// One thread per 8 columns: 4 bytes of codes in, 16 bytes of bf16 out, each
-// value rounded once from the exact binary32 product.
+// One thread per two pieces: 8 bytes of codes in, 32 bytes of bf16 out, each value
+// rounded once from the exact binary32 product.
 template <int GROUP, bool ZEROS>
-__global__ void w4_dequantize_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
-                                     const uint8_t* __restrict__ zeros, uint4* __restrict__ w, int64_t vecs) {
+__global__ void __launch_bounds__(256)
+    w4_dequantize_kernel(const uint2* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
+                         const uint8_t* __restrict__ zeros, uint4* __restrict__ w, int64_t pairs) {
   griddep_wait();
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (v >= vecs) return;
-  const int64_t g = v / (GROUP / kVecCols);
-  const uint32_t code = __ldg(codes + v);
-  const float s = __bfloat162float(scales[g]);
-  const float z = ZEROS ? static_cast<float>(zeros[g] & 15) : 8.0f;
-  uint32_t out[4];
+  griddep_launch_dependents();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kQuantPieces) + threadIdx.x;
+  uint2 raw[kQuantPieces];
+  float s[kQuantPieces], z[kQuantPieces];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = static_cast<float>((code >> (8 * i)) & 15u) - z;
-    const float b = static_cast<float>((code >> (8 * i + 4)) & 15u) - z;
-    out[i] = pack_bf16x2(a * s, b * s);
+  for (int k = 0; k < kQuantPieces; ++k) {
+    const int64_t v = first + 256 * k;
+    if (v >= pairs) continue;
+    const int64_t g = v / (GROUP / (2 * kVecCols));
+    raw[k] = __ldg(codes + v);
+    s[k] = __bfloat162float(scales[g]);
+    z[k] = ZEROS ? static_cast<float>(zeros[g] & 15) : 8.0f;
   }
-  w[v] = make_uint4(out[0], out[1], out[2], out[3]);
+#pragma unroll
+  for (int k = 0; k < kQuantPieces; ++k) {
+    const int64_t v = first + 256 * k;
+    if (v >= pairs) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t code = h ? raw[k].y : raw[k].x;
+      uint32_t out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // an integer in a binary32 significand, less 2^23 and the zero point: exact
+        const float a = __uint_as_float(0x4b000000u | ((code >> (8 * i)) & 15u)) - (8388608.0f + z[k]);
+        const float b = __uint_as_float(0x4b000000u | ((code >> (8 * i + 4)) & 15u)) - (8388608.0f + z[k]);
+        out[i] = pack_bf16x2(a * s[k], b * s[k]);
+      }
+      w[2 * v + h] = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
 }
 
 // Activation rows staged once for all CTAs of the product, a CTA a row.
@@ -217,21 +296,22 @@ cudaError_t launch_linear_g(const void* x, const W4Weight& w, const void* bias, 
 }
 
 template <int GROUP>
-cudaError_t launch_quant_g(const void* w, void* codes, void* scales, void* zeros, int64_t vecs, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((vecs + 255) / 256)), block(256);
+cudaError_t launch_quant_g(const void* w, void* codes, void* scales, void* zeros, int64_t pieces, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((pieces + 256 * kQuantPieces - 1) / (256 * kQuantPieces)));
   auto kern = zeros ? w4_quantize_kernel<GROUP, true> : w4_quantize_kernel<GROUP, false>;
-  return launch_pdl(kern, grid, block, 0, s, static_cast<const uint4*>(w), static_cast<uint32_t*>(codes),
-                    static_cast<__nv_bfloat16*>(scales), static_cast<uint8_t*>(zeros), vecs);
+  return launch_pdl(kern, grid, dim3(256), 0, s, static_cast<const uint4*>(w), static_cast<uint32_t*>(codes),
+                    static_cast<__nv_bfloat16*>(scales), static_cast<uint8_t*>(zeros), pieces);
 }
 
 template <int GROUP>
-cudaError_t launch_dequant_g(const void* codes, const void* scales, const void* zeros, void* w, int64_t vecs,
+cudaError_t launch_dequant_g(const void* codes, const void* scales, const void* zeros, void* w, int64_t pieces,
                              cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((vecs + 255) / 256)), block(256);
+  const int64_t pairs = pieces / 2;  // a group has an even number of pieces
+  const dim3 grid(static_cast<unsigned>((pairs + 256 * kQuantPieces - 1) / (256 * kQuantPieces)));
   auto kern = zeros ? w4_dequantize_kernel<GROUP, true> : w4_dequantize_kernel<GROUP, false>;
-  return launch_pdl(kern, grid, block, 0, s, static_cast<const uint32_t*>(codes),
+  return launch_pdl(kern, grid, dim3(256), 0, s, static_cast<const uint2*>(codes),
                     static_cast<const __nv_bfloat16*>(scales), static_cast<const uint8_t*>(zeros),
-                    static_cast<uint4*>(w), vecs);
+                    static_cast<uint4*>(w), pairs);
 }
 
 }  // namespace
