@@ -22,19 +22,29 @@ __all__ = ["w4_quantize", "w4_dequantize", "w4_linear", "moe_route", "moe_swiglu
 # slow, exact check runs only to say what is wrong) and the stream as a number.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 BF16, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
 
-def _check(t, name: str, dtype, shape, like: torch.Tensor) -> None:
-    """_need(t, name, dtype, shape, like.device), fast where nothing is wrong."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == like.get_device() and t.is_cuda and t.is_contiguous()):
-        _need(t, name, dtype, shape, like.device)
+def _device(x, name: str, dtype) -> int:
+    """The index of the device that the call runs on: that of its first tensor."""
+    index = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if index < 0:
+        _need(x, name, dtype)
+    return index
+
+
+def _check(t, name: str, dtype, shape, index: int) -> None:
+    """_need(t, name, dtype, shape, device `index`), fast where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, torch.device("cuda", index))
 
 
 def _launch(fn, index: int, *args) -> None:
     """fn(*args, current stream) with device `index` current."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -57,30 +67,30 @@ def _scratch(index: int, nbytes: int) -> torch.Tensor:
     captured on one stream do not share it."""
     key = (index, _raw_stream(index))
     ws = _scratch_cache.get(key)
-    if ws is None or ws.numel() < nbytes or torch.cuda.is_current_stream_capturing():
+    if ws is None or ws.numel() < nbytes or _capturing():
         ws = alloc_workspace(max(nbytes, DG_ERROR_BLOCK_BYTES), torch.device("cuda", index))
-        if not torch.cuda.is_current_stream_capturing():
+        if not _capturing():
             _scratch_cache[key] = ws
     return ws
 
 
-def _need_workspace(ws: torch.Tensor, nbytes: int, like: torch.Tensor) -> None:
-    _check(ws, "workspace", U8, ws.shape if isinstance(ws, torch.Tensor) else None, like)
+def _need_workspace(ws: torch.Tensor, nbytes: int, index: int) -> None:
+    _check(ws, "workspace", U8, ws.shape if isinstance(ws, torch.Tensor) else None, index)
     if ws.numel() < nbytes:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")
 
 
 # ------------------------------------------------------------------ 4-bit weights
 
-def _need_w4(codes, scales, zeros, lead: tuple, K: int, like, what: str) -> int:
+def _need_w4(codes, scales, zeros, lead: tuple, K: int, index: int, what: str) -> int:
     """Checks one 4-bit weight [*lead, K]; returns its group size."""
-    _check(codes, what + "codes", U8, (*lead, K // 2), like)
+    _check(codes, what + "codes", U8, (*lead, K // 2), index)
     groups = scales.shape[-1] if isinstance(scales, torch.Tensor) and scales.dim() == codes.dim() else 0
     if groups < 1 or K % groups:
         raise ValueError(f"{what}scales must be [..., K/group] beside codes [..., K/2]")
-    _check(scales, what + "scales", BF16, (*lead, groups), like)
+    _check(scales, what + "scales", BF16, (*lead, groups), index)
     if zeros is not None:
-        _check(zeros, what + "zeros", U8, scales.shape, like)
+        _check(zeros, what + "zeros", U8, scales.shape, index)
     return K // groups
 
 
@@ -90,32 +100,31 @@ def w4_quantize(weight: torch.Tensor, group: int = 128, zero_points: bool = Fals
     Returns (codes, scales, zeros): value = (code - zero) * scale.  zeros is
     None unless zero_points (then codes span each group's own range instead of
     a symmetric one)."""
-    lib = load()
-    _need(weight, "weight", torch.bfloat16)
-    K = weight.shape[-1]
+    index = _device(weight, "weight", BF16)
+    _check(weight, "weight", BF16, weight.shape, index)
+    lead, K = weight.shape[:-1], weight.shape[-1]
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide {K}, got {group}")
-    lead, dev = weight.shape[:-1], weight.device
-    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty((*lead, K // group), dtype=torch.bfloat16, device=dev)
-    zeros = torch.empty((*lead, K // group), dtype=torch.uint8, device=dev) if zero_points else None
-    rows = weight.numel() // K if K else 0
-    _launch(lib.dg_w4_quantize, weight.get_device(), rows, K, group, _p(weight), _p(codes), _p(scales), _p(zeros))
+    codes = torch.empty((*lead, K // 2), dtype=U8, device=weight.device)
+    scales = torch.empty((*lead, K // group), dtype=BF16, device=weight.device)
+    zeros = torch.empty((*lead, K // group), dtype=U8, device=weight.device) if zero_points else None
+    _launch(load().dg_w4_quantize, index, weight.numel() // K if K else 0, K, group, weight.data_ptr(),
+            codes.data_ptr(), scales.data_ptr(), _p(zeros))
     return codes, scales, zeros
 
 
 def w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """The bf16 weight [..., K] that 4-bit codes stand for."""
-    lib = load()
-    _need(codes, "codes", torch.uint8)
-    K, lead, dev = 2 * codes.shape[-1], codes.shape[:-1], codes.device
-    group = _need_w4(codes, scales, zeros, tuple(lead), K, codes, "")
+    index = _device(codes, "codes", U8)
+    lead, K = codes.shape[:-1], 2 * codes.shape[-1]
+    group = _need_w4(codes, scales, zeros, lead, K, index, "")
     if out is None:
-        out = torch.empty((*lead, K), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((*lead, K), dtype=BF16, device=scales.device)
     else:
-        _need(out, "out", torch.bfloat16, (*lead, K), dev)
-    _launch(lib.dg_w4_dequantize, codes.get_device(), out.numel() // K if K else 0, K, group, _p(codes), _p(scales), _p(zeros), _p(out))
+        _check(out, "out", BF16, (*lead, K), index)
+    _launch(load().dg_w4_dequantize, index, out.numel() // K if K else 0, K, group, codes.data_ptr(),
+            scales.data_ptr(), _p(zeros), out.data_ptr())
     return out
 
 
@@ -128,17 +137,17 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     and use tp_linear.  `ws` holds the call's error block (default: this
     stream's own), and scratch where there are more than few short rows
     (dg_w4_linear_workspace_bytes)."""
-    lib = load()
+    lib, index = load(), _device(x, "x", BF16)
     lead, in_f, out_f = x.shape[:-1], x.shape[-1], codes.shape[0]
-    _check(x, "x", BF16, x.shape, x)
-    group = _need_w4(codes, scales, zeros, (out_f,), in_f, x, "")
+    _check(x, "x", BF16, x.shape, index)
+    group = _need_w4(codes, scales, zeros, (out_f,), in_f, index, "")
     if bias is not None:
-        _check(bias, "bias", BF16, (out_f,), x)
+        _check(bias, "bias", BF16, (out_f,), index)
     if out is None:
         out = torch.empty((*lead, out_f), dtype=BF16, device=x.device)
     else:
-        _check(out, "out", BF16, (*lead, out_f), x)
-    rows, index = x.numel() // in_f if in_f else 0, x.get_device()
+        _check(out, "out", BF16, (*lead, out_f), index)
+    rows = x.numel() // in_f if in_f else 0
     if ws is None:
         ws = _scratch(index, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f))
     _launch(lib.dg_w4_linear, index, rows, in_f, out_f, group, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
@@ -158,43 +167,43 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     experts (softmax otherwise: over all experts); scale multiplies them.
     Returns idx [T, top_k] int32 (largest logit first) and gates [T, top_k]
     binary32."""
-    lib = load()
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    lib, index = load(), _device(x, "x", BF16)
     T, d = x.shape
-    E, dev, index = w_router.shape[0], x.device, x.get_device()
-    _check(x, "x", BF16, (T, d), x)
-    _check(w_router, "w_router", BF16, (E, d), x)
+    E = w_router.shape[0]
+    _check(x, "x", BF16, (T, d), index)
+    _check(w_router, "w_router", BF16, (E, d), index)
     flags = (DG_MOE_SIGMOID if score == "sigmoid" else 0) | (DG_MOE_RENORM if renormalize else 0)
-    idx = torch.empty((T, top_k), dtype=I32, device=dev)
-    gates = torch.empty((T, top_k), dtype=F32, device=dev)
+    idx = torch.empty((T, top_k), dtype=I32, device=x.device)
+    gates = torch.empty((T, top_k), dtype=F32, device=x.device)
     nbytes = lib.dg_moe_route_workspace_bytes(T, d, E, top_k)
     if workspace is None:
         workspace = _scratch(index, nbytes)
     else:
-        _need_workspace(workspace, nbytes, x)
+        _need_workspace(workspace, nbytes, index)
     _launch(lib.dg_moe_route, index, T, d, E, top_k, flags, scale, x.data_ptr(), w_router.data_ptr(), idx.data_ptr(),
             gates.data_ptr(), workspace.data_ptr(), workspace.numel())
     return idx, gates
 
 
-def _moe_args(x, idx, gates, workspace, out, F: int, E: int, group: int):
+def _moe_args(index, x, idx, gates, workspace, out, F: int, E: int, group: int):
     """Checks the tensors both weight formats share; returns (shape, workspace, out)."""
     T, d = x.shape
     k = idx.shape[-1]
-    _check(x, "x", BF16, (T, d), x)
-    _check(idx, "idx", I32, (T, k), x)
-    _check(gates, "gates", F32, (T, k), x)
+    _check(x, "x", BF16, (T, d), index)
+    _check(idx, "idx", I32, (T, k), index)
+    _check(gates, "gates", F32, (T, k), index)
     sh = MoEShape(T, d, F, E, k)
     nbytes = load().dg_moe_swiglu_workspace_bytes(sh, group)
     if workspace is None:
-        workspace = _scratch(x.get_device(), nbytes)
+        workspace = _scratch(index, nbytes)
     elif nbytes:
-        _need_workspace(workspace, nbytes, x)
+        _need_workspace(workspace, nbytes, index)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _check(out, "out", BF16, (T, d), x)
+        _check(out, "out", BF16, (T, d), index)
     return sh, workspace, out
 
 
@@ -207,13 +216,12 @@ def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: tor
     [0, E) is no expert and adds nothing).  T * k <= 8192.  `workspace`
     (dg_moe_swiglu_workspace_bytes, its error block zeroed; default: this
     stream's own) is not shared by calls that run at the same time."""
-    lib = load()
-    d = x.shape[-1]
+    index, d = _device(x, "x", BF16), x.shape[-1]
     E, F = w13.shape[0], w13.shape[1] // 2
-    _check(w13, "w13", BF16, (E, 2 * F, d), x)
-    _check(w2, "w2", BF16, (E, d, F), x)
-    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, 0)
-    _launch(lib.dg_moe_swiglu, x.get_device(), sh, x.data_ptr(), idx.data_ptr(), gates.data_ptr(), w13.data_ptr(),
+    _check(w13, "w13", BF16, (E, 2 * F, d), index)
+    _check(w2, "w2", BF16, (E, d, F), index)
+    sh, workspace, out = _moe_args(index, x, idx, gates, workspace, out, F, E, 0)
+    _launch(load().dg_moe_swiglu, index, sh, x.data_ptr(), idx.data_ptr(), gates.data_ptr(), w13.data_ptr(),
             w2.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
@@ -222,15 +230,14 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_swiglu with 4-bit experts: w13 and w2 are (codes, scales, zeros) of [E, 2F, d] and [E, d, F]
     (w4_quantize of the bf16 tensors), of one group size, both with zero points or both without."""
-    lib = load()
-    d = x.shape[-1]
+    index, d = _device(x, "x", BF16), x.shape[-1]
     (c13, s13, z13), (c2, s2, z2) = w13, w2
     E, F = c13.shape[0], c13.shape[1] // 2
-    group = _need_w4(c13, s13, z13, (E, 2 * F), d, x, "w13 ")
-    if _need_w4(c2, s2, z2, (E, d), F, x, "w2 ") != group:
+    group = _need_w4(c13, s13, z13, (E, 2 * F), d, index, "w13 ")
+    if _need_w4(c2, s2, z2, (E, d), F, index, "w2 ") != group:
         raise ValueError("w13 and w2 must have the same group size")
-    sh, workspace, out = _moe_args(x, idx, gates, workspace, out, F, E, group)
-    _launch(lib.dg_moe_swiglu_w4, x.get_device(), sh, group, x.data_ptr(), idx.data_ptr(), gates.data_ptr(),
+    sh, workspace, out = _moe_args(index, x, idx, gates, workspace, out, F, E, group)
+    _launch(load().dg_moe_swiglu_w4, index, sh, group, x.data_ptr(), idx.data_ptr(), gates.data_ptr(),
             c13.data_ptr(), s13.data_ptr(), _p(z13), c2.data_ptr(), s2.data_ptr(), _p(z2), out.data_ptr(),
             workspace.data_ptr(), workspace.numel())
     return out
