@@ -520,7 +520,7 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
                       smem + kRowWarps * w4_warp_bytes<FMT, NT>() + wk * w4_xring_bytes<FMT, NT>(), rg * 32 + lane,
                       32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
     } else if (active) {
-      stream.template run<LOCAL>(w4_cols<FMT, NT>(in, K, count, column), acc);
+      stream.template run<LOCAL, false>(w4_cols<FMT, NT>(in, K, count, column), acc);
     }
     if (active) w4_unscale<NT>(acc, LOCAL ? nullptr : in.factor, count, column);
     if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);

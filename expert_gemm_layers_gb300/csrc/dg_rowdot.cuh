@@ -75,6 +75,39 @@ static __device__ __forceinline__ void join_slices(RowSums<NT>& acc, uint8_t* jo
   }
 }
 
+// Joins the sums of a cluster's CTAs, which took slices of K of the same rows, in the
+// order of their ranks, into those of rank 0.  place: the warp's join_bytes, the same
+// in every CTA; holds: the warp has sums.  All threads of the cluster.
+template <int NT>
+static __device__ __forceinline__ void join_cluster(RowSums<NT>& acc, uint8_t* place, bool holds, int ctas) {
+  const uint32_t at = smem_u32(place) + (threadIdx.x & 31) * 16, rank = cluster_ctarank();
+  if (holds && rank != 0) {
+#pragma unroll
+    for (int m = 0; m < kRowTiles; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float4*>(place + (threadIdx.x & 31) * 16 + (m * NT + n) * 512) =
+            make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+  }
+  cluster_sync_all();
+  if (holds && rank == 0) {
+    for (int r = 1; r < ctas; ++r) {
+      const uint32_t from = mapa_shared(at, r);
+#pragma unroll
+      for (int m = 0; m < kRowTiles; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 v = ld_cluster_f32x4(from + (m * NT + n) * 512);
+          acc[m][n][0] += v.x;
+          acc[m][n][1] += v.y;
+          acc[m][n][2] += v.z;
+          acc[m][n][3] += v.w;
+        }
+    }
+  }
+  cluster_sync_all();  // a CTA's shared memory outlives the reads
+}
+
 template <int NT>
 static __device__ __forceinline__ void clear(RowSums<NT>& acc) {
 #pragma unroll
@@ -85,21 +118,23 @@ static __device__ __forceinline__ void clear(RowSums<NT>& acc) {
       for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 }
 
-// How many ways to split K over a CTA's warps: the split with the least time.  It
-// counts the units that fall to an SM times the steps of a unit's slice (and one
+// How many ways to split K over a CTA's warps (up to `most`), and further over the
+// CTAs of a cluster (up to `clusters` of them, whose join costs as much as
+// `join_steps` steps): the split with the least time.  It counts the units that fall to an SM times the steps of a unit's slice (and one
 // for ending the unit), over the rate of an SM with that many CTAs at a time.
 // The CTAs of an SM share its pipes, so it is SMs that have to come out even.
 static inline int rowdot_split(int64_t blocks_per_entry, int64_t entries, int steps, int ctas, int most,
-                               int num_sms) {
+                               int num_sms, int clusters = 1, int join_steps = 0) {
   // measured on the 4-bit products: of the rate with 24 warps, 8 warps reach about half, 16 about 85%
   constexpr int kRate[4] = {0, 50, 85, 100};
   int best = 1;
   double least = 0.0;
-  for (int WK = 1; WK <= most && (WK == 1 || steps >= 2 * WK); WK *= 2) {
+  for (int WK = 1; WK <= most * clusters && (WK == 1 || steps >= 2 * WK); WK *= 2) {
     const int64_t units = entries * ((blocks_per_entry * WK + kRowWarps - 1) / kRowWarps);
     const int64_t rounds = (units + num_sms - 1) / num_sms;
     const int at_a_time = static_cast<int>(rounds < ctas ? rounds : ctas);
-    const double cost = static_cast<double>(rounds) * ((steps + WK - 1) / WK + 1) / kRate[at_a_time];
+    const double cost = static_cast<double>(rounds) * ((steps + WK - 1) / WK + 1 + (WK > most ? join_steps : 0)) /
+                        kRate[at_a_time];
     if (WK == 1 || cost < least) {
       least = cost;
       best = WK;

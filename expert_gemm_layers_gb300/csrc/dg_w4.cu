@@ -174,44 +174,55 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Activation rows staged once for all CTAs of the product, a CTA a row.
-template <int GROUP>
+// Activation rows staged once for all CTAs of the product: a CTA a row, or (STEPS: up
+// to 8 rows) 16 steps a CTA, each with a scale of its own.
+template <int GROUP, bool STEPS>
 __global__ void __launch_bounds__(256)
     w4_stage_kernel(const __nv_bfloat16* __restrict__ x, Staged out, int rows, int K, const uint32_t* err) {
   __shared__ uint32_t top;
-  if (threadIdx.x == 0) top = 0u;
+  if (!STEPS && threadIdx.x == 0) top = 0u;
   griddep_wait();
   griddep_launch_dependents();
   if (err_set(err)) return;
-  __syncthreads();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    w4_stage_row<GROUP>(reinterpret_cast<const uint8_t*>(x + r * K), K, out.frag + r * w4_row_bytes(K),
-                        out.sums + r * w4_row_sums(K, GROUP), out.factor + r, &top);
+  if constexpr (STEPS) {
+    w4_stage_steps<GROUP>(out, rows, K, blockIdx.x, gridDim.x, [&](int i) {
+      return reinterpret_cast<const uint8_t*>(x + static_cast<int64_t>(i) * K);
+    });
+  } else {
+    __syncthreads();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+      w4_stage_row<GROUP>(reinterpret_cast<const uint8_t*>(x + r * K), K, out.frag + r * w4_row_bytes(K),
+                          out.sums + r * w4_row_sums(K, GROUP), out.factor + r, &top);
+  }
 }
 
 // y = x W^T (+ bias): a CTA takes 8 / WK blocks of 32 weight rows and up to 8*NT
-// activation rows.  LOCAL: it stages those itself, in shared memory; else `in` has
+// activation rows, or (gridDim.z > 1) its cluster does.  LOCAL: it stages those itself, in shared memory; else `in` has
 // them.
 template <int GROUP, int NT, bool LOCAL>
-__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kRowWarps * 32, LOCAL ? 3 : 2)
     w4_linear_kernel(const __nv_bfloat16* __restrict__ x, Staged in, const uint8_t* __restrict__ codes,
                      const __nv_bfloat16* __restrict__ scales, const uint8_t* __restrict__ zeros,
                      const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N,
                      int WK, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
-  griddep_wait();
-  const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
+  // Not LOCAL: w4_stage_kernel let this one start after its own wait, so whatever
+  // wrote the weight is done, and codes may be on their way while x is staged.
+  if (LOCAL) griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wk = warp % WK, rg = warp / WK;
   const int r0 = (static_cast<int>(blockIdx.x) * (kRowWarps / WK) + rg) * 16 * kRowTiles;
   const int n0 = static_cast<int>(blockIdx.y) * 8 * NT, count = min(rows - n0, 8 * NT);
   const int steps = w4_steps(K);
+  const int slice = static_cast<int>(blockIdx.z) * WK + wk, slices = static_cast<int>(gridDim.z) * WK;
   uint8_t* joins = smem + w4_ring_bytes<GROUP, NT>(WK);
   // rows past the last one read the last one and store nothing
   W4Stream<GROUP, NT> stream{w4_rows<GROUP>(codes, scales, zeros, K, [&](int i) { return min(r0 + i, N - 1); }),
-                             r0 < N, smem + warp * w4_warp_bytes<GROUP, NT>(), K, steps * wk / WK,
-                             steps * (wk + 1) / WK};
+                             r0 < N, smem + warp * w4_warp_bytes<GROUP, NT>(), K,
+                             steps * slice / slices, steps * (slice + 1) / slices};
   if (r0 < N) stream.start();
+  if (!LOCAL) griddep_wait();
+  const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
   if constexpr (LOCAL) {
     in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
     w4_stage_local<GROUP>(in, count, K,
@@ -227,14 +238,16 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 3 : 2)
   if constexpr (NT > 1) {
     stream.run_wide(in, count, act,
                     smem + kRowWarps * w4_warp_bytes<GROUP, NT>() + wk * w4_xring_bytes<GROUP, NT>(), rg * 32 + lane,
-                    32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
+                    32 * (kRowWarps / WK), (steps + slices - 1) / slices, acc);
   } else if (r0 < N) {
-    stream.template run<LOCAL>(w4_cols<GROUP, NT>(in, K, count, act), acc);
+    stream.template run<true, !LOCAL>(w4_cols<GROUP, NT>(in, K, count, act), acc);
   }
   griddep_launch_dependents();
   if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
-  if (wk != 0 || r0 >= N || failed != 0u) return;
-  w4_unscale<NT>(acc, LOCAL ? nullptr : in.factor, count, act);
+  if (!LOCAL && gridDim.z > 1)
+    join_cluster<NT>(acc, joins + joins_bytes<NT>(WK) + rg * join_bytes<NT>(), wk == 0 && r0 < N, gridDim.z);
+  if (wk != 0 || r0 >= N || failed != 0u || blockIdx.z != 0) return;
+  w4_unscale<NT>(acc, NT == 1 ? nullptr : in.factor, count, act);
 #pragma unroll
   for (int m = 0; m < kRowTiles; ++m)
 #pragma unroll
@@ -256,23 +269,35 @@ struct W4Weight {
   const uint8_t* zeros;
 };
 
+// Narrow weights on long rows: the CTAs of a cluster take slices of K too.  16 rows,
+// K = 14336, N = 4096: 22.9 us with up to 8 CTAs, 24.6 with up to 4, 65 with none.  With a
+// join counted as less than 4 steps, 64 rows of K = 4096, N = 14336 would be split further
+// and take 58 us, not 54; as 8 steps, 16 rows of it less far: 23.2 us, not 21.0.
+constexpr int kClusterMost = 8, kJoinSteps = 4;
+
 template <int GROUP, int NT, bool LOCAL>
 cudaError_t launch_linear(const void* x, const Staged& in, const W4Weight& w, const void* bias, void* y, int rows,
                           int K, int N, const DeviceInfo& dev, cudaStream_t s) {
   constexpr int kRows = 16 * kRowTiles;
   const int x_blocks = (rows + 8 * NT - 1) / (8 * NT);
-  const int WK = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), NT == 1 ? 3 : 2,
-                              w4_most_split<NT>(), dev.num_sms);
+  const int split = rowdot_split((static_cast<int64_t>(N) + kRows - 1) / kRows, x_blocks, w4_steps(K), LOCAL ? 3 : 2,
+                                 w4_most_split<NT>(), dev.num_sms, LOCAL ? 1 : kClusterMost, kJoinSteps);
+  const int WK = split < w4_most_split<NT>() ? split : w4_most_split<NT>(), CK = split / WK;
   const int smem = w4_ring_bytes<GROUP, NT>(WK) + joins_bytes<NT>(WK) +
+                   (CK > 1 ? kRowWarps / WK * join_bytes<NT>() : 0) +
                    (LOCAL ? static_cast<int>(w4_staged_bytes(rows, K, GROUP, true)) : 0);
   auto kern = w4_linear_kernel<GROUP, NT, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
   if (e != cudaSuccess) return e;
   const int a_cta = kRowWarps / WK * kRows;
-  return launch_pdl(kern, dim3((N + a_cta - 1) / a_cta, x_blocks), dim3(kRowWarps * 32), smem, s,
-                    static_cast<const __nv_bfloat16*>(x), in, w.codes, w.scales, w.zeros,
-                    static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), rows, K, N, WK,
-                    static_cast<const uint32_t*>(dev.err));
+  const dim3 grid((N + a_cta - 1) / a_cta, x_blocks, CK), block(kRowWarps * 32);
+  auto launch = [&](auto how) {
+    return how(kern, grid, block, smem, s, static_cast<const __nv_bfloat16*>(x), in, w.codes, w.scales, w.zeros,
+               static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), rows, K, N, WK,
+               static_cast<const uint32_t*>(dev.err));
+  };
+  if (CK > 1) return launch([](auto... a) { return launch_pdl_clusters_z(a...); });
+  return launch([](auto... a) { return launch_pdl(a...); });
 }
 
 template <int GROUP>
@@ -281,8 +306,10 @@ cudaError_t launch_linear_g(const void* x, const W4Weight& w, const void* bias, 
   if (w4_linear_local(rows, K, GROUP))
     return launch_linear<GROUP, 1, true>(x, Staged{}, w, bias, y, rows, K, N, dev, s);
   const Staged in = w4_staged_at(static_cast<uint8_t*>(scratch), rows, K, GROUP);
-  const int grid = rows < 8 * dev.num_sms ? rows : 8 * dev.num_sms;
-  cudaError_t e = launch_pdl(w4_stage_kernel<GROUP>, dim3(grid), dim3(256), 0, s,
+  const int ctas = rows <= 8 ? (rows * w4_steps(K) + 15) / 16 : rows;
+  const int grid = ctas < 8 * dev.num_sms ? ctas : 8 * dev.num_sms;
+  auto stage = rows <= 8 ? w4_stage_kernel<GROUP, true> : w4_stage_kernel<GROUP, false>;
+  cudaError_t e = launch_pdl(stage, dim3(grid), dim3(256), 0, s,
                              static_cast<const __nv_bfloat16*>(x), in, rows, K, static_cast<const uint32_t*>(dev.err));
   if (e != cudaSuccess) return e;
   // blocks of up to four column tiles, as even as it goes
@@ -340,7 +367,7 @@ bool w4_linear_local(int64_t rows, int64_t K, int group) {
 
 size_t w4_linear_scratch_bytes(int64_t rows, int64_t K) {
   // of the finest group; the group is not known to the query
-  return static_cast<size_t>(w4_staged_bytes(rows, static_cast<int>(K), 32));
+  return static_cast<size_t>(w4_staged_bytes(rows, static_cast<int>(K), 32, rows <= 8));
 }
 
 cudaError_t launch_w4_linear(const void* x, const void* codes, const void* scales, const void* zeros,

@@ -133,26 +133,33 @@ static __device__ __forceinline__ void w4_stage_row(const uint8_t* x, int K, uin
   __syncthreads();
 }
 
-// Stages up to 8 rows in shared memory by the 256 threads of a CTA.  row(i): row i.
-// Here every step has a scale of its own (factors[row * steps + step]): the row's
-// largest would take another pass and a barrier.  Synchronises the CTA.
+// Stages up to 8 rows, every step with a scale of its own (factors[row * steps +
+// step]): a row's largest would take another pass and a barrier.  row(i): row i.  The
+// 256 threads of a CTA take 16 steps at a time, from the 16th of number `block` on,
+// every `blocks`.
 template <int GROUP, typename Row>
-static __device__ __forceinline__ void w4_stage_local(const Staged& out, int count, int K, Row row) {
+static __device__ __forceinline__ void w4_stage_steps(const Staged& out, int count, int K, int block, int blocks,
+                                                      Row row) {
   const int p = threadIdx.x & 15, hw = threadIdx.x >> 4, steps = w4_steps(K), total = count * steps;
   const int64_t rb = w4_row_bytes(K);
   const int fs = w4_row_sums(K, GROUP);
-  for (int i0 = 0; i0 < total; i0 += 16) {
+  for (int i0 = 16 * block; i0 < total; i0 += 16 * blocks) {
     const int i = i0 + hw, r = count == 1 ? 0 : i / steps, st = i - r * steps, k = st * kW4Step + 8 * p;
     const bool exists = i < total;
     const uint4 v =
-        exists && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * k) : make_uint4(0u, 0u, 0u, 0u);
+        exists && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * static_cast<int64_t>(k)) : make_uint4(0u, 0u, 0u, 0u);
     uint32_t top = w4_top(v);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int E = w4_exponent(top);
-    w4_stage_piece<GROUP>(v, E, p, st, exists, out.frag + r * rb, out.sums + r * fs);
+    w4_stage_piece<GROUP>(v, E, p, st, exists, out.frag + r * rb, out.sums + static_cast<int64_t>(r) * fs);
     if (exists && p == 0) out.factor[i] = __int_as_float((127 - 14 + E) << 23);
   }
+}
+// The same in shared memory, by one CTA, which it synchronises.
+template <int GROUP, typename Row>
+static __device__ __forceinline__ void w4_stage_local(const Staged& out, int count, int K, Row row) {
+  w4_stage_steps<GROUP>(out, count, K, 0, 1, row);
   __syncthreads();
 }
 
@@ -229,11 +236,39 @@ constexpr int w4_most_split() {
   return NT == 1 ? kRowWarps : 2;
 }
 
+// What a lane takes of a step's activations in memory (NT = 1), asked for a step ahead.
+template <int GROUP>
+struct W4Ahead {
+  uint4 b[4];
+  float sum[2][kW4Step / GROUP], f[2];
+};
+
+// The sums of a row's groups of one step.
+template <int G>
+static __device__ __forceinline__ void w4_load_sums(float (&to)[G], const float* p) {
+  if constexpr (G == 4) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(p);
+  else if constexpr (G == 2) *reinterpret_cast<float2*>(to) = *reinterpret_cast<const float2*>(p);
+  else to[0] = *p;
+}
+
+template <int GROUP, bool STEP_FACTORS>
+static __device__ __forceinline__ void w4_ahead(W4Ahead<GROUP>& a, const W4Cols<1>& x, int c) {
+  constexpr int G = kW4Step / GROUP;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    a.b[i] = *reinterpret_cast<const uint4*>(x.xs + (static_cast<uint64_t>(x.frag[0]) + 16 * c) * 16 + i * 64);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w4_load_sums<G>(a.sum[i], x.xsums + static_cast<uint64_t>(x.sums[0][i]) + c * G);
+    a.f[i] = STEP_FACTORS ? x.factors[x.frow[i] + c] : 1.0f;
+  }
+}
+
 // One step's product.  slot: its codes; zs: {-zero point, scale} of the warp's rows;
-// xstep (NT > 1): the step's activations in shared memory.
+// the step's activations are in shared memory at xstep (NT > 1), or in registers.
 // STEP_FACTORS (NT = 1): the activations' factor of the step is applied too.
 template <int GROUP, int NT, bool STEP_FACTORS>
-static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Cols<NT>& x,
+static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t* zs, const W4Ahead<GROUP>* x,
                                               const uint8_t* xstep, int c, int groups, RowSums<NT>& acc) {
   constexpr int G = kW4Step / GROUP;  // groups a step
   constexpr int W = GROUP / 32;       // code words of a row and group a lane takes
@@ -245,17 +280,14 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* p = NT > 1 ? reinterpret_cast<const float*>(xstep + NT * 2048) + (8 * n + 2 * t + i) * G
-                              : x.xsums + static_cast<uint64_t>(x.sums[n][i]) + c * G;
-      if constexpr (G == 4) *reinterpret_cast<float4*>(xsum[n][i]) = *reinterpret_cast<const float4*>(p);
-      else if constexpr (G == 2) *reinterpret_cast<float2*>(xsum[n][i]) = *reinterpret_cast<const float2*>(p);
-      else xsum[n][i][0] = *p;
+      if constexpr (NT > 1) {
+        w4_load_sums<G>(xsum[n][i], reinterpret_cast<const float*>(xstep + NT * 2048) + (8 * n + 2 * t + i) * G);
+      } else {
+#pragma unroll
+        for (int q = 0; q < G; ++q) xsum[n][i][q] = x->sum[i][q];
+      }
     }
-  float f0 = 1.0f, f1 = 1.0f;
-  if constexpr (STEP_FACTORS) {
-    f0 = x.factors[x.frow[0] + c];
-    f1 = x.factors[x.frow[1] + c];
-  }
+  const float f0 = STEP_FACTORS ? x->f[0] : 1.0f, f1 = STEP_FACTORS ? x->f[1] : 1.0f;
 #pragma unroll
   for (int q = 0; q < G; ++q) {
     if (G == 1 || c * G + q < groups) {  // a group is whole or absent
@@ -281,9 +313,8 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
           uint4 b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = *reinterpret_cast<const uint4*>(
-                NT > 1 ? xstep + ((q * W + j) * NT + n) * 512 + lane * 16
-                       : x.xs + (static_cast<uint64_t>(x.frag[n]) + 16 * c) * 16 + (q * W + j) * 64);
+            b[n] = NT > 1 ? *reinterpret_cast<const uint4*>(xstep + ((q * W + j) * NT + n) * 512 + lane * 16)
+                          : x->b[q * W + j];
 #pragma unroll
           for (int m = 0; m < kTogether; ++m) {
             const uint32_t l = code[2 * m][j], h = code[2 * m + 1][j];
@@ -320,8 +351,8 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
 }
 
 // The codes and scales of steps [c0, c1) of a warp's rows, for up to 8*NT columns.
-// start() is apart from run(), so that a kernel with NT = 1 can ask for them before
-// it has its activations.
+// start() is apart from run() and run_wide(), so that a kernel can ask for them
+// before it has its activations.
 template <int GROUP, int NT>
 struct W4Stream {
   static constexpr int G = kW4Step / GROUP;
@@ -342,7 +373,6 @@ struct W4Stream {
     cp_async16(dst + 512, w.codes + w.next0 + at, in);
     cp_async16(dst + 1024, w.codes1 + at, in);
     cp_async16(dst + 1536, w.codes1 + w.next1 + at, in);
-    if (NT == 1) cp_async_commit();
   }
   __device__ __forceinline__ void load_scales(int c) {
     if (!active || c >= c1) return;
@@ -385,19 +415,22 @@ struct W4Stream {
   }
   __device__ __forceinline__ void start() {
     load_scales(c0);
-    if constexpr (NT == 1) {
 #pragma unroll
-      for (int u = 0; u < R - 1; ++u) fill(c0 + u, u);
-    }
+    for (int u = 0; u < R - 1; ++u) fill(c0 + u, u);
   }
   // acc += the product with staged activation rows, in units of 2^-24 / factor.
   // Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t, 8n + 2t + 1;
-  // row g + 8, the same).  NT = 1: an active warp by itself, the lanes read `x`.
-  template <bool STEP_FACTORS>
+  // row g + 8, the same).  NT = 1: an active warp by itself, the lanes read `x`, AHEAD:
+  // a step before they use it.  STEP_FACTORS: every step of a row has its factor.
+  template <bool STEP_FACTORS, bool AHEAD>
   __device__ __forceinline__ void run(const W4Cols<NT>& x, RowSums<NT>& acc) {
     const int groups = K / GROUP;
+#pragma unroll
+    for (int u = 0; u < R - 1; ++u) cp_async_commit();  // the first holds all of start()'s
     decode(0);
     load_scales(c0 + 1);
+    W4Ahead<GROUP> next;
+    if (AHEAD && c0 < c1) w4_ahead<GROUP, STEP_FACTORS>(next, x, c0);
     int parity = 0;
 #pragma unroll 1
     for (int c = c0; c < c1; c += R) {
@@ -408,11 +441,19 @@ struct W4Stream {
         // the other lanes' copies and scales are in place, and what the step before has read is free
         __syncwarp();
         fill(c + u + R - 1, (u + R - 1) % R);
+        cp_async_commit();
         const uint8_t* zs = decoded(parity);
         parity ^= 1;
         decode(parity);
         load_scales(c + u + 2);
-        w4_use<GROUP, NT, STEP_FACTORS>(ring + u * kW4StepBytes, zs, x, nullptr, c + u, groups, acc);
+        W4Ahead<GROUP> now;
+        if constexpr (AHEAD) {
+          now = next;
+          if (c + u + 1 < c1) w4_ahead<GROUP, STEP_FACTORS>(next, x, c + u + 1);
+        } else {
+          w4_ahead<GROUP, STEP_FACTORS>(now, x, c + u);
+        }
+        w4_use<GROUP, NT, STEP_FACTORS>(ring + u * kW4StepBytes, zs, &now, nullptr, c + u, groups, acc);
       }
     }
     cp_async_wait<0>();
@@ -429,8 +470,7 @@ struct W4Stream {
     const int groups = K / GROUP, tiles = (count + 7) / 8;
     const int64_t rb = w4_row_bytes(K);
     const int fs = w4_row_sums(K, GROUP);
-    auto fill_all = [&](int c, int u) {
-      fill(c, u);
+    auto fill_x = [&](int c, int u) {
       if (c < c1) {
         const uint32_t to = smem_u32(xring) + u * kX;
         for (int i = ix; i < tiles * 128; i += nx) {  // 16 pieces a row, as they lie in the staged row
@@ -448,7 +488,7 @@ struct W4Stream {
       cp_async_commit();
     };
 #pragma unroll
-    for (int u = 0; u < R - 1; ++u) fill_all(c0 + u, u);
+    for (int u = 0; u < R - 1; ++u) fill_x(c0 + u, u);
     decode(0);
     load_scales(c0 + 1);
     int parity = 0;
@@ -460,13 +500,14 @@ struct W4Stream {
         const int c = c0 + s0 + u;
         cp_async_wait<R - 2>();
         __syncthreads();  // the step is in place, and what the step before has read is free
-        fill_all(c + R - 1, (u + R - 1) % R);
+        fill(c + R - 1, (u + R - 1) % R);
+        fill_x(c + R - 1, (u + R - 1) % R);
         const uint8_t* zs = decoded(parity);
         parity ^= 1;
         decode(parity);
         load_scales(c + 2);
         if (active && c < c1)
-          w4_use<GROUP, NT, false>(ring + u * kW4StepBytes, zs, W4Cols<NT>{}, xring + u * kX, c, groups, acc);
+          w4_use<GROUP, NT, false>(ring + u * kW4StepBytes, zs, nullptr, xring + u * kX, c, groups, acc);
       }
     }
     cp_async_wait<0>();
