@@ -274,19 +274,6 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
   constexpr int W = GROUP / 32;       // code words of a row and group a lane takes
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int swz = (g >> 1) & 3;
-  // sums of the columns 8n + 2t and 8n + 2t + 1, all groups of the step
-  float xsum[NT][2][G];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if constexpr (NT > 1) {
-        w4_load_sums<G>(xsum[n][i], reinterpret_cast<const float*>(xstep + NT * 2048) + (8 * n + 2 * t + i) * G);
-      } else {
-#pragma unroll
-        for (int q = 0; q < G; ++q) xsum[n][i][q] = x->sum[i][q];
-      }
-    }
   const float f0 = STEP_FACTORS ? x->f[0] : 1.0f, f1 = STEP_FACTORS ? x->f[1] : 1.0f;
 #pragma unroll
   for (int q = 0; q < G; ++q) {
@@ -313,8 +300,17 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
           uint4 b[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            b[n] = NT > 1 ? *reinterpret_cast<const uint4*>(xstep + ((q * W + j) * NT + n) * 512 + lane * 16)
-                          : x->b[q * W + j];
+            if constexpr (NT > 2 && W == 4) {
+              // in order: the compiler would bring four words' fragments forward and
+              // spill (64 rows, K = 4096, N = 14336: 48 us this way, 59 us that)
+              asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(b[n].x), "=r"(b[n].y), "=r"(b[n].z), "=r"(b[n].w)
+                           : "r"(smem_u32(xstep) + ((q * W + j) * NT + n) * 512 + lane * 16));
+            } else if constexpr (NT > 1) {
+              b[n] = *reinterpret_cast<const uint4*>(xstep + ((q * W + j) * NT + n) * 512 + lane * 16);
+            } else {
+              b[n] = x->b[q * W + j];
+            }
 #pragma unroll
           for (int m = 0; m < kTogether; ++m) {
             const uint32_t l = code[2 * m][j], h = code[2 * m + 1][j];
@@ -339,10 +335,13 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float(&to)[4] = acc[m0 + m][n];
-            to[0] = fmaf(STEP_FACTORS ? l.y * f0 : l.y, fmaf(l.x, xsum[n][0][q], part[m][n][0]), to[0]);
-            to[1] = fmaf(STEP_FACTORS ? l.y * f1 : l.y, fmaf(l.x, xsum[n][1][q], part[m][n][1]), to[1]);
-            to[2] = fmaf(STEP_FACTORS ? h.y * f0 : h.y, fmaf(h.x, xsum[n][0][q], part[m][n][2]), to[2]);
-            to[3] = fmaf(STEP_FACTORS ? h.y * f1 : h.y, fmaf(h.x, xsum[n][1][q], part[m][n][3]), to[3]);
+            // sums of the columns 8n + 2t and 8n + 2t + 1 over the group
+            const float* sums = reinterpret_cast<const float*>(xstep + NT * 2048) + (8 * n + 2 * t) * G + q;
+            const float x0 = NT > 1 ? sums[0] : x->sum[0][q], x1 = NT > 1 ? sums[G] : x->sum[1][q];
+            to[0] = fmaf(STEP_FACTORS ? l.y * f0 : l.y, fmaf(l.x, x0, part[m][n][0]), to[0]);
+            to[1] = fmaf(STEP_FACTORS ? l.y * f1 : l.y, fmaf(l.x, x1, part[m][n][1]), to[1]);
+            to[2] = fmaf(STEP_FACTORS ? h.y * f0 : h.y, fmaf(h.x, x0, part[m][n][2]), to[2]);
+            to[3] = fmaf(STEP_FACTORS ? h.y * f1 : h.y, fmaf(h.x, x1, part[m][n][3]), to[3]);
           }
         }
       }
@@ -473,11 +472,13 @@ struct W4Stream {
     auto fill_x = [&](int c, int u) {
       if (c < c1) {
         const uint32_t to = smem_u32(xring) + u * kX;
+#pragma unroll 1
         for (int i = ix; i < tiles * 128; i += nx) {  // 16 pieces a row, as they lie in the staged row
           const int row = i / 16, p = i % 16;         // p = 4 * (piece of a lane) + t
           cp_async16(to + ((p / 4) * NT + row / 8) * 512 + ((row % 8) * 4 + p % 4) * 16,
                      in.frag + act(min(row, count - 1)) * rb + static_cast<int64_t>(c) * 256 + p * 16, true);
         }
+#pragma unroll 1
         for (int row = ix; row < tiles * 8; row += nx) {
           const float* from = in.sums + act(min(row, count - 1)) * static_cast<int64_t>(fs) + c * G;
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + NT * 2048 + row * 4 * G), "l"(from),
