@@ -145,7 +145,7 @@ dg_status dg_w4_dequantize(int64_t rows, int64_t K, int32_t group, const void* c
 
 size_t dg_w4_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
   (void)out_features;
-  if (rows < 0 || in_features < 1 || rows > kMaxW4LinearRows || in_features > kMaxDim) return 0;
+  if (rows < 0 || in_features < 1 || rows > kMaxW4LinearRows || in_features > kMaxDim / 4) return 0;
   // the finest group takes the most room, staged in the workspace or by the kernel itself
   if (w4_linear_local(rows, in_features, 32)) return DG_ERROR_BLOCK_BYTES;
   return DG_ERROR_BLOCK_BYTES + w4_linear_scratch_bytes(rows, in_features);

@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, LOCAL ? 3 : 2)
                      const __nv_bfloat16* __restrict__ bias, __nv_bfloat16* __restrict__ y, int rows, int K, int N,
                      int WK, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
-  // Not LOCAL: w4_stage_kernel let this one start after its own wait, so whatever
-  // wrote the weight is done, and codes may be on their way while x is staged.
-  if (LOCAL) griddep_wait();
+  griddep_wait();
+  const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int wk = warp % WK, rg = warp / WK;
   const int r0 = (static_cast<int>(blockIdx.x) * (kRowWarps / WK) + rg) * 16 * kRowTiles;
@@ -221,8 +220,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, LOCAL ? 3 : 2)
                              r0 < N, smem + warp * w4_warp_bytes<GROUP, NT>(), K,
                              steps * slice / slices, steps * (slice + 1) / slices};
   if (r0 < N) stream.start();
-  if (!LOCAL) griddep_wait();
-  const uint32_t failed = ld_volatile_u32(err);  // looked at before anything is written
   if constexpr (LOCAL) {
     in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
     w4_stage_local<GROUP>(in, count, K,

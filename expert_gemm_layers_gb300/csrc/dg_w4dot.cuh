@@ -362,6 +362,7 @@ struct W4Stream {
   int K, c0, c1;
   // scales and zero points of row `lane`, of the step after the last one decoded, as they lie in memory
   uint32_t s[2], z;
+  uint32_t ones;  // bit q: group q of row `lane` in the step last decoded has scale 1
 
   __device__ __forceinline__ void fill(int c, int u) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -402,15 +403,38 @@ struct W4Stream {
   __device__ __forceinline__ uint8_t* decoded(int parity) const {
     return ring + R * kW4StepBytes + parity * 256 * G;
   }
-  __device__ __forceinline__ void decode(int parity) const {
+  __device__ __forceinline__ void decode(int parity) {
+    ones = 0u;
 #pragma unroll
     for (int q = 0; q < G; ++q) {
       // -z by way of a binary32 significand
       const float nz = w.zeros ? 8388608.0f - __uint_as_float(0x4b000000u | ((z >> (8 * q)) & 15u)) : -8.0f;
       const uint32_t two = s[q / 2];
+      if ((q % 2 ? two >> 16 : two & 0xffffu) == 0x3f80u) ones |= 1u << q;
       *reinterpret_cast<float2*>(decoded(parity) + q * 256 + (threadIdx.x & 31) * 8) =
           make_float2(nz, __uint_as_float(q % 2 ? two & 0xffff0000u : two << 16));
     }
+  }
+  // A group of zeros is quantised to its zero point with scale 1.  What rounding leaves
+  // of sum q x - z * sum x would show there, beside weights that are mostly far below 1:
+  // such groups get scale 0, and add exactly nothing.  which: `ones` of the step in
+  // `slot`, whose decoded scales are zs.
+  __device__ __forceinline__ void drop_zeros(const uint8_t* slot, uint8_t* zs, uint32_t which) const {
+    if (!active || !__any_sync(0xffffffffu, which != 0u)) return;
+    const int lane = threadIdx.x & 31, g = lane & 7;
+    for (int q = 0; q < G; ++q) {
+      if (!(which >> q & 1u)) continue;
+      float2* p = reinterpret_cast<float2*>(zs + q * 256 + lane * 8);
+      const uint32_t zero = static_cast<uint32_t>(static_cast<int>(-p->x)) * 0x11111111u;
+      bool all = true;
+      for (int i = 0; i < GROUP / 32; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot + (lane >> 3) * 512 + g * 64 +
+                                                        ((q * (GROUP / 32) + i) ^ ((g >> 1) & 3)) * 16);
+        all = all && v.x == zero && v.y == zero && v.z == zero && v.w == zero;
+      }
+      if (all) p->y = 0.0f;
+    }
+    __syncwarp();
   }
   __device__ __forceinline__ void start() {
     load_scales(c0);
@@ -441,7 +465,8 @@ struct W4Stream {
         __syncwarp();
         fill(c + u + R - 1, (u + R - 1) % R);
         cp_async_commit();
-        const uint8_t* zs = decoded(parity);
+        uint8_t* zs = decoded(parity);
+        drop_zeros(ring + u * kW4StepBytes, zs, ones);
         parity ^= 1;
         decode(parity);
         load_scales(c + u + 2);
@@ -503,7 +528,8 @@ struct W4Stream {
         __syncthreads();  // the step is in place, and what the step before has read is free
         fill(c + R - 1, (u + R - 1) % R);
         fill_x(c + R - 1, (u + R - 1) % R);
-        const uint8_t* zs = decoded(parity);
+        uint8_t* zs = decoded(parity);
+        drop_zeros(ring + u * kW4StepBytes, zs, ones);
         parity ^= 1;
         decode(parity);
         load_scales(c + 2);

@@ -23,7 +23,7 @@ __all__ = ["w4_quantize", "w4_dequantize", "w4_linear", "moe_route", "moe_swiglu
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 BF16, U8, I32, F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 
 
@@ -53,6 +53,19 @@ def _launch(fn, index: int, *args) -> None:
         check(status)
 
 
+def _capturing(index: int) -> bool:
+    """Whether device `index`'s current stream is being captured."""
+    if _current_device() == index:
+        return _is_capturing()
+    with torch.cuda.device(index):
+        return _is_capturing()
+
+
+def _size(t, dim: int) -> int:
+    """Size of a dimension; 0 for what has no such dimension, which the check of its shape then refuses."""
+    return t.shape[dim] if isinstance(t, torch.Tensor) and -t.dim() <= dim < t.dim() else 0
+
+
 def _p(t):
     return None if t is None else t.data_ptr()
 
@@ -67,9 +80,9 @@ def _scratch(index: int, nbytes: int) -> torch.Tensor:
     captured on one stream do not share it."""
     key = (index, _raw_stream(index))
     ws = _scratch_cache.get(key)
-    if ws is None or ws.numel() < nbytes or _capturing():
+    if ws is None or ws.numel() < nbytes or _capturing(index):
         ws = alloc_workspace(max(nbytes, DG_ERROR_BLOCK_BYTES), torch.device("cuda", index))
-        if not _capturing():
+        if not _capturing(index):
             _scratch_cache[key] = ws
     return ws
 
@@ -85,7 +98,7 @@ def _need_workspace(ws: torch.Tensor, nbytes: int, index: int) -> None:
 def _need_w4(codes, scales, zeros, lead: tuple, K: int, index: int, what: str) -> int:
     """Checks one 4-bit weight [*lead, K]; returns its group size."""
     _check(codes, what + "codes", U8, (*lead, K // 2), index)
-    groups = scales.shape[-1] if isinstance(scales, torch.Tensor) and scales.dim() == codes.dim() else 0
+    groups = _size(scales, -1)
     if groups < 1 or K % groups:
         raise ValueError(f"{what}scales must be [..., K/group] beside codes [..., K/2]")
     _check(scales, what + "scales", BF16, (*lead, groups), index)
@@ -102,7 +115,7 @@ def w4_quantize(weight: torch.Tensor, group: int = 128, zero_points: bool = Fals
     a symmetric one)."""
     index = _device(weight, "weight", BF16)
     _check(weight, "weight", BF16, weight.shape, index)
-    lead, K = weight.shape[:-1], weight.shape[-1]
+    lead, K = weight.shape[:-1], _size(weight, -1)
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide {K}, got {group}")
     codes = torch.empty((*lead, K // 2), dtype=U8, device=weight.device)
@@ -117,7 +130,7 @@ def w4_dequantize(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """The bf16 weight [..., K] that 4-bit codes stand for."""
     index = _device(codes, "codes", U8)
-    lead, K = codes.shape[:-1], 2 * codes.shape[-1]
+    lead, K = codes.shape[:-1], 2 * _size(codes, -1)
     group = _need_w4(codes, scales, zeros, lead, K, index, "")
     if out is None:
         out = torch.empty((*lead, K), dtype=BF16, device=scales.device)
@@ -138,7 +151,7 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     stream's own), and scratch where there are more than few short rows
     (dg_w4_linear_workspace_bytes)."""
     lib, index = load(), _device(x, "x", BF16)
-    lead, in_f, out_f = x.shape[:-1], x.shape[-1], codes.shape[0]
+    lead, in_f, out_f = x.shape[:-1], _size(x, -1), _size(codes, 0)
     _check(x, "x", BF16, x.shape, index)
     group = _need_w4(codes, scales, zeros, (out_f,), in_f, index, "")
     if bias is not None:
@@ -170,8 +183,7 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     if score not in ("softmax", "sigmoid"):
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
     lib, index = load(), _device(x, "x", BF16)
-    T, d = x.shape
-    E = w_router.shape[0]
+    T, d, E = _size(x, 0), _size(x, -1), _size(w_router, 0)
     _check(x, "x", BF16, (T, d), index)
     _check(w_router, "w_router", BF16, (E, d), index)
     flags = (DG_MOE_SIGMOID if score == "sigmoid" else 0) | (DG_MOE_RENORM if renormalize else 0)
@@ -189,8 +201,7 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
 
 def _moe_args(index, x, idx, gates, workspace, out, F: int, E: int, group: int):
     """Checks the tensors both weight formats share; returns (shape, workspace, out)."""
-    T, d = x.shape
-    k = idx.shape[-1]
+    T, d, k = _size(x, 0), _size(x, -1), _size(idx, -1)
     _check(x, "x", BF16, (T, d), index)
     _check(idx, "idx", I32, (T, k), index)
     _check(gates, "gates", F32, (T, k), index)
@@ -216,8 +227,8 @@ def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: tor
     [0, E) is no expert and adds nothing).  T * k <= 8192.  `workspace`
     (dg_moe_swiglu_workspace_bytes, its error block zeroed; default: this
     stream's own) is not shared by calls that run at the same time."""
-    index, d = _device(x, "x", BF16), x.shape[-1]
-    E, F = w13.shape[0], w13.shape[1] // 2
+    index, d = _device(x, "x", BF16), _size(x, -1)
+    E, F = _size(w13, 0), _size(w13, 1) // 2
     _check(w13, "w13", BF16, (E, 2 * F, d), index)
     _check(w2, "w2", BF16, (E, d, F), index)
     sh, workspace, out = _moe_args(index, x, idx, gates, workspace, out, F, E, 0)
@@ -230,9 +241,9 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_swiglu with 4-bit experts: w13 and w2 are (codes, scales, zeros) of [E, 2F, d] and [E, d, F]
     (w4_quantize of the bf16 tensors), of one group size, both with zero points or both without."""
-    index, d = _device(x, "x", BF16), x.shape[-1]
+    index, d = _device(x, "x", BF16), _size(x, -1)
     (c13, s13, z13), (c2, s2, z2) = w13, w2
-    E, F = c13.shape[0], c13.shape[1] // 2
+    E, F = _size(c13, 0), _size(c13, 1) // 2
     group = _need_w4(c13, s13, z13, (E, 2 * F), d, index, "w13 ")
     if _need_w4(c2, s2, z2, (E, d), F, index, "w2 ") != group:
         raise ValueError("w13 and w2 must have the same group size")

@@ -403,7 +403,10 @@ dg_status dg_tp_linear_bwd(int64_t rows, int64_t in_features, int64_t out_featur
  * ws (dg_w4_linear_workspace_bytes): the error block, then, for all but few
  * short rows, scratch for x in the form the kernel reads; nothing in it outlives
  * the call.
- * An activation that is not finite makes its row of y not finite.
+ * An activation that is not finite makes its row of y not finite.  The kernel
+ * sums q x and z x apart: a sum is off by at most about in_features * 2^-23 of
+ * sum scale (q + z) |x|.  A group of zeros as w4_quantize writes it (all codes at
+ * the zero point, scale 1) adds exactly nothing.
  * These calls have no backward: the codes are not trained.
  * ------------------------------------------------------------------------ */
 dg_status dg_w4_quantize(int64_t rows, int64_t K, int32_t group, const void* weight, void* codes, void* scales,
@@ -450,6 +453,8 @@ dg_status dg_w4_linear(int64_t rows, int64_t in_features, int64_t out_features, 
  *
  * dg_moe_swiglu_w4: the same with both weights in 4 bits (layout above, E*2F
  * and E*d rows; both with or both without zeros); d % group == 0, F % group == 0.
+ * Sums as in dg_w4_linear.  A token with an activation that is not finite gets a
+ * row that is not finite, if it has an expert.
  * No backward: training uses the bf16 layers above.
  * ------------------------------------------------------------------------ */
 #define DG_MOE_SIGMOID 1u

@@ -128,6 +128,49 @@ def test_w4_linear_larger(rows, K, N, group):
     check_linear(rows, K, N, group, True, True, seed=3)
 
 
+@pytest.mark.parametrize("rows,K,N,group", [(3, 40960, 40, 32), (8, 4224, 333, 128), (11, 14336, 70, 64),
+                                            (24, 5120, 200, 32), (33, 8192, 96, 128), (64, 2176, 33, 64)])
+def test_w4_linear_long_rows_of_a_narrow_weight(rows, K, N, group):
+    """K split over several CTAs."""
+    check_linear(rows, K, N, group, True, False, seed=5)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("rows", [1, 8, 20, 30])
+def test_zeros_of_a_weight_stay_zeros(rows, zero_points, group):
+    """Rows, and groups of a row, that are zero add exactly nothing."""
+    K, N = 5 * group, 70
+    w = randn((N, K), 11, K**-0.5)
+    w[::3] = 0.0
+    w[1, group:] = 0.0
+    codes, scales, zeros = dg.w4_quantize(w.to(DEV), group, zero_points)
+    x = randn((rows, K), 12) * 100.0
+    y = dg.w4_linear(x.to(DEV), codes, scales, zeros)
+    assert (y[:, ::3] == 0).all() and (y[:, 1] != 0).all()
+    first = slice(0, group)
+    alone = dg.w4_linear(x[:, first].contiguous().to(DEV), codes[:, : group // 2].contiguous(),
+                         scales[:, :1].contiguous(), None if zeros is None else zeros[:, :1].contiguous())
+    ref = few.w4_linear(f64(x), few.w4_values(codes.cpu().numpy(), f64(scales),
+                                              None if zeros is None else zeros.cpu().numpy()))
+    for got in (y, alone):
+        within(got[:, 1], ref[:, 1], 2.0**-8 * np.abs(ref[:, 1]) + 2 * group * 2.0**-23 *
+               (15 * f64(scales)[1, 0] * np.abs(f64(x))[:, first].sum(1)), "one group")
+
+
+def test_wrappers_name_what_is_no_weight():
+    x = randn((2, 64), 3).to(DEV)
+    w, _ = w4_weight((), 24, 64, 32, False, 4)
+    idx, gates = torch.zeros((2, 1), dtype=torch.int32, device=DEV), torch.ones((2, 1), device=DEV)
+    for call, name in ((lambda: dg.w4_linear(x, None, None), "codes"), (lambda: dg.w4_linear(x, w[0], None), "scales"),
+                       (lambda: dg.moe_route(x, [1], 1), "w_router"), (lambda: dg.moe_route(x[0], x, 1), "x"),
+                       (lambda: dg.moe_swiglu(x, idx, gates, None, x), "w13"),
+                       (lambda: dg.moe_swiglu(x, idx, gates, torch.zeros((1, 16, 64), dtype=BF16, device=DEV), 1), "w2"),
+                       (lambda: dg.moe_swiglu_w4(x, idx, gates, (None,) * 3, w), "codes")):
+        with pytest.raises((TypeError, ValueError), match=name):
+            call()
+
+
 def test_w4_linear_keeps_nonfinite_values_in_their_row_and_column():
     x = randn((11, 256), 1)
     w, _ = w4_weight((), 40, 256, 64, True, 2)
