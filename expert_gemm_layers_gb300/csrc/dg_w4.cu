@@ -18,6 +18,7 @@ __device__ __forceinline__ bool err_set(const uint32_t* err) { return ld_volatil
 
 constexpr int kVecCols = 8;  // columns of a piece: 16 bytes of bf16, 4 bytes of codes
 constexpr int kQuantPieces = 4;  // pieces a thread has in flight
+constexpr int kDequantPieces = 8;
 
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
   uint64_t r;
@@ -76,101 +77,112 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int k = 0; k < kQuantPieces; ++k)
     raw[k] = first + 256 * k < pieces ? __ldg(w + first + 256 * k) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t top = 0u;  // largest magnitude, as bf16 bits: NaN > inf > finite
+  float lo = 0.0f, hi = 0.0f;
+  // The groups of the pieces 0..3 have their scales made by the lanes 0..3 of every
+  // four: a division and a reciprocal a thread, not four.
+  static_assert(kQuantPieces == 4, "lanes of a group");
+  const int mine = threadIdx.x & 3;
 #pragma unroll
   for (int k = 0; k < kQuantPieces; ++k) {
-    const int64_t v = first + 256 * k;
     const uint32_t word[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-    float quot;
-    uint32_t top = 0u;  // largest magnitude, as bf16 bits: NaN > inf > finite
-    float lo = 0.0f;
+    uint32_t t = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, word[i] & 0x7fff7fffu);
-    top = max(top & 0xffffu, top >> 16);
+    for (int i = 0; i < 4; ++i) t = __vmaxu2(t, word[i] & 0x7fff7fffu);
+    t = max(t & 0xffffu, t >> 16);
 #pragma unroll
-    for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+    if (mine == k) top = t;
     if constexpr (ZEROS) {
-      float hi = 0.0f;
+      float l = 0.0f, h = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 p = unpack_bf16x2(word[i]);
-        lo = fminf(lo, fminf(p.x, p.y));
-        hi = fmaxf(hi, fmaxf(p.x, p.y));
+        l = fminf(l, fminf(p.x, p.y));
+        h = fmaxf(h, fmaxf(p.x, p.y));
       }
 #pragma unroll
       for (int o = GROUP / kVecCols / 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        l = fminf(l, __shfl_xor_sync(0xffffffffu, l, o));
+        h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, o));
       }
-      quot = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
-    } else {
-      quot = __fdiv_rn(__uint_as_float(top << 16), 7.0f);
+      if (mine == k) {
+        lo = l;
+        hi = h;
+      }
     }
-    if (v >= pieces) continue;
-    const bool finite = top < 0x7f80u && isfinite(quot);
-    float s = __bfloat162float(__float2bfloat16_rn(quot));
-    if (s == 0.0f) s = 1.0f;
-    float z = 8.0f;
-    uint32_t code = 0x88888888u;
-    if (finite) {
-      if constexpr (ZEROS) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
-      if (s >= 7.9e-31f) {  // 2^-100: 1 / s is a normal number
-        code = codes_of(raw[k], __frcp_rn(s), z);
-      } else {
-        code = 0u;
+  }
+  const float quot = ZEROS ? __fdiv_rn(__fsub_rn(hi, lo), 15.0f) : __fdiv_rn(__uint_as_float(top << 16), 7.0f);
+  float scale = __bfloat162float(__float2bfloat16_rn(quot)), zero = 8.0f;
+  if (scale == 0.0f) scale = 1.0f;
+  if (top < 0x7f80u && isfinite(quot)) {
+    if constexpr (ZEROS) zero = fminf(fmaxf(rintf(__fdiv_rn(-lo, scale)), 0.0f), 15.0f);
+  } else {
+    scale = __int_as_float(0x7fc00000);
+  }
+  const float inverse = __frcp_rn(scale);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 p = unpack_bf16x2(word[i / 2]);
-          const float q = fminf(fmaxf(rintf(__fdiv_rn(i & 1 ? p.y : p.x, s)) + z, 0.0f), 15.0f);
-          code |= static_cast<uint32_t>(q) << (4 * i);
-        }
+  for (int k = 0; k < kQuantPieces; ++k) {
+    const int64_t v = first + 256 * k;
+    const int from = (threadIdx.x & 28) | k;
+    const float s = __shfl_sync(0xffffffffu, scale, from), inv = __shfl_sync(0xffffffffu, inverse, from);
+    const float z = ZEROS ? __shfl_sync(0xffffffffu, zero, from) : 8.0f;
+    if (v >= pieces) continue;
+    uint32_t code = 0x88888888u;
+    if (s >= 7.9e-31f) {  // 2^-100: 1 / s is a normal number
+      code = codes_of(raw[k], inv, z);
+    } else if (!isnan(s)) {
+      const uint32_t word[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      code = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 p = unpack_bf16x2(word[i / 2]);
+        const float q = fminf(fmaxf(rintf(__fdiv_rn(i & 1 ? p.y : p.x, s)) + z, 0.0f), 15.0f);
+        code |= static_cast<uint32_t>(q) << (4 * i);
       }
     }
     codes[v] = code;
     if (v % (GROUP / kVecCols) == 0) {
       const int64_t g = v / (GROUP / kVecCols);
-      scales[g] = __float2bfloat16_rn(finite ? s : __int_as_float(0x7fc00000));
+      scales[g] = __float2bfloat16_rn(s);
       if (ZEROS) zeros[g] = static_cast<uint8_t>(z);
     }
   }
 }
 
-// One thread per two pieces: 8 bytes of codes in, 32 bytes of bf16 out, each value
+// A piece a thread at a time: 4 bytes of codes in, 16 bytes of bf16 out, each value
 // rounded once from the exact binary32 product.
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256)
-    w4_dequantize_kernel(const uint2* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
-                         const uint8_t* __restrict__ zeros, uint4* __restrict__ w, int64_t pairs) {
+    w4_dequantize_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
+                         const uint8_t* __restrict__ zeros, uint4* __restrict__ w, int64_t pieces) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kQuantPieces) + threadIdx.x;
-  uint2 raw[kQuantPieces];
-  float s[kQuantPieces], z[kQuantPieces];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kDequantPieces) + threadIdx.x;
+  uint32_t raw[kDequantPieces];
+  float s[kDequantPieces], z[kDequantPieces];
 #pragma unroll
-  for (int k = 0; k < kQuantPieces; ++k) {
+  for (int k = 0; k < kDequantPieces; ++k) {
     const int64_t v = first + 256 * k;
-    if (v >= pairs) continue;
-    const int64_t g = v / (GROUP / (2 * kVecCols));
+    if (v >= pieces) continue;
+    const int64_t g = v / (GROUP / kVecCols);
     raw[k] = __ldg(codes + v);
     s[k] = __bfloat162float(scales[g]);
     z[k] = ZEROS ? static_cast<float>(zeros[g] & 15) : 8.0f;
   }
 #pragma unroll
-  for (int k = 0; k < kQuantPieces; ++k) {
+  for (int k = 0; k < kDequantPieces; ++k) {
     const int64_t v = first + 256 * k;
-    if (v >= pairs) continue;
+    if (v >= pieces) continue;
+    uint32_t out[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t code = h ? raw[k].y : raw[k].x;
-      uint32_t out[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // an integer in a binary32 significand, less 2^23 and the zero point: exact
-        const float a = __uint_as_float(0x4b000000u | ((code >> (8 * i)) & 15u)) - (8388608.0f + z[k]);
-        const float b = __uint_as_float(0x4b000000u | ((code >> (8 * i + 4)) & 15u)) - (8388608.0f + z[k]);
-        out[i] = pack_bf16x2(a * s[k], b * s[k]);
-      }
-      w[2 * v + h] = make_uint4(out[0], out[1], out[2], out[3]);
+    for (int i = 0; i < 4; ++i) {
+      // an integer in a binary32 significand, less 2^23 and the zero point: exact
+      const float a = __uint_as_float(0x4b000000u | ((raw[k] >> (8 * i)) & 15u)) - (8388608.0f + z[k]);
+      const float b = __uint_as_float(0x4b000000u | ((raw[k] >> (8 * i + 4)) & 15u)) - (8388608.0f + z[k]);
+      out[i] = pack_bf16x2(a * s[k], b * s[k]);
     }
+    w[v] = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
@@ -330,12 +342,11 @@ cudaError_t launch_quant_g(const void* w, void* codes, void* scales, void* zeros
 template <int GROUP>
 cudaError_t launch_dequant_g(const void* codes, const void* scales, const void* zeros, void* w, int64_t pieces,
                              cudaStream_t s) {
-  const int64_t pairs = pieces / 2;  // a group has an even number of pieces
-  const dim3 grid(static_cast<unsigned>((pairs + 256 * kQuantPieces - 1) / (256 * kQuantPieces)));
+  const dim3 grid(static_cast<unsigned>((pieces + 256 * kDequantPieces - 1) / (256 * kDequantPieces)));
   auto kern = zeros ? w4_dequantize_kernel<GROUP, true> : w4_dequantize_kernel<GROUP, false>;
-  return launch_pdl(kern, grid, dim3(256), 0, s, static_cast<const uint2*>(codes),
+  return launch_pdl(kern, grid, dim3(256), 0, s, static_cast<const uint32_t*>(codes),
                     static_cast<const __nv_bfloat16*>(scales), static_cast<const uint8_t*>(zeros),
-                    static_cast<uint4*>(w), pairs);
+                    static_cast<uint4*>(w), pieces);
 }
 
 }  // namespace
