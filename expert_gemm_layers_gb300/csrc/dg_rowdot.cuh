@@ -120,8 +120,9 @@ static __device__ __forceinline__ void clear(RowSums<NT>& acc) {
 
 // How many ways to split K over a CTA's warps (up to `most`), and further over the
 // CTAs of a cluster (up to `clusters` of them, whose join costs as much as
-// `join_steps` steps): the split with the least time.  It counts the units that fall to an SM times the steps of a unit's slice (and one
-// for ending the unit), over the rate of an SM with that many CTAs at a time.
+// `join_steps` steps): the split with the least time.  It counts the units that fall
+// to an SM times the steps of a unit's slice (and one for ending the unit), over the
+// rate of an SM with that many CTAs at a time.
 // The CTAs of an SM share its pipes, so it is SMs that have to come out even.
 static inline int rowdot_split(int64_t blocks_per_entry, int64_t entries, int steps, int ctas, int most,
                                int num_sms, int clusters = 1, int join_steps = 0) {
@@ -152,6 +153,11 @@ static inline int rowdot_split(int64_t blocks_per_entry, int64_t entries, int st
 // 8 (NT = 1), the lanes read them from global memory, where they stay in L1, and
 // each warp runs by itself.  More of them are staged in shared memory beside the
 // weights, once for all warps of the CTA that work on the same slice of K.
+//
+// Bound by the weights' bytes, which it moves at 0.62 to 0.89 of the measured copy rate:
+// the more steps a unit has and the more units an SM, the nearer.  (Weights loaded to
+// registers, without the ring: 77.6 us where this takes 67 to 71, one token and 8 experts
+// of 3 x 4096 x 1792; 700 where this takes 468 to 504, 128 tokens and 64 experts.)
 
 constexpr int kBfRing = 4;
 constexpr int kBfStep = 32;

@@ -64,6 +64,11 @@ __device__ __forceinline__ uint32_t codes_of(const uint4& v, float inv, float z)
 // A thread takes pieces of 8 columns; the GROUP / 8 lanes of a group agree on its
 // scale by shuffles.  A group with a NaN or an infinity, or whose range overflows
 // binary32, gets a NaN scale.
+// Reading 2 bytes a weight and writing half a byte should bound it; 28672 x 4096,
+// groups of 128: 55 us, 5.4 TB/s, 0.79 of the measured copy rate.  What keeps it from
+// that is arithmetic (76% of the issue slots of the busiest pipe): a division a weight
+// and one piece at a time took 178 us, codes_of and four pieces 60, scales by four
+// lanes 55.
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256)
     w4_quantize_kernel(const uint4* __restrict__ w, uint32_t* __restrict__ codes, __nv_bfloat16* __restrict__ scales,
@@ -151,7 +156,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // A piece a thread at a time: 4 bytes of codes in, 16 bytes of bf16 out, each value
-// rounded once from the exact binary32 product.
+// rounded once from the exact binary32 product.  Bound by its writes: 28672 x 4096,
+// groups of 128: 43 us, 6.9 TB/s.  (16 columns a thread, written as two pieces of a
+// 32-byte stride, took 55 us: every line was written twice by halves.)
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256)
     w4_dequantize_kernel(const uint32_t* __restrict__ codes, const __nv_bfloat16* __restrict__ scales,
@@ -208,6 +215,12 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Bound by the latency of a warp's instructions more than by bytes: a step is some 250
+// of them on 32 rows, and what these shapes allow is 16 to 24 warps an SM.  GPU time,
+// floor by the codes' bytes: 1 x 4096 -> 6144, groups of 128, 9.0 us (1.9; an empty
+// kernel is seen to take 4.7); 1 x 4096 -> 28672, 18 us (8.9); 8 x 14336 -> 4096, 14 us
+// (4.6); 40 x 1280 -> 15360, groups of 32, 18.7 us (1.8); 64 x 4096 -> 14336, 52 us (4.9,
+// and 12 by mma.sync's own rate).
 // y = x W^T (+ bias): a CTA takes 8 / WK blocks of 32 weight rows and up to 8*NT
 // activation rows, or (gridDim.z > 1) its cluster does.  LOCAL: it stages those itself, in shared memory; else `in` has
 // them.
@@ -368,7 +381,9 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const vo
 }
 
 // Up to 8 rows whose staged form takes no more than 32 KB are staged by every CTA
-// itself: reading 1 to 8 short rows costs less than another launch.
+// itself, which leaves three CTAs an SM.  One row of 4096 takes 8.6 us so; another
+// kernel before the product is 2.5 to 5 us by itself, and past 32 KB the third CTA
+// would go (1 x 4096 -> 28672: 18 us with three, 21 with two).
 bool w4_linear_local(int64_t rows, int64_t K, int group) {
   return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group, true) <= 32 * 1024;
 }

@@ -59,6 +59,15 @@ def w4_values(codes: np.ndarray, scales: np.ndarray, zeros: np.ndarray | None) -
     return (q - z) * np.repeat(scales, group, axis=-1)
 
 
+def w4_magnitudes(codes: np.ndarray, scales: np.ndarray, zeros: np.ndarray | None) -> np.ndarray:
+    """(code + zero) * scale: what a weight adds to the rounding error of a sum that is made as
+    scale * (sum code x - zero * sum x)."""
+    q = w4_unpack(codes).astype(np.float64)
+    group = q.shape[-1] // scales.shape[-1]
+    z = 8.0 if zeros is None else np.repeat(zeros.astype(np.float64), group, axis=-1)
+    return (q + z) * np.repeat(np.abs(scales), group, axis=-1)
+
+
 def w4_linear(x: np.ndarray, w: np.ndarray, bias: np.ndarray | None = None) -> np.ndarray:
     y = x @ w.T
     return y if bias is None else y + bias
@@ -112,11 +121,12 @@ def moe_swiglu(x: np.ndarray, idx: np.ndarray, gates: np.ndarray, w13: np.ndarra
     return y
 
 
-def moe_swiglu_bound(x, idx, gates, w13, w2) -> np.ndarray:
+def moe_swiglu_bound(x, idx, gates, w13, w2, m13=None, m2=None) -> np.ndarray:
     """Per element, how far a correct bf16 result may be from moe_swiglu:
 
     * a product summed in binary32 over n terms, each addition off by at most
-      one unit 2^-23 of a partial sum: n * 2^-23 * sum |w| |x|
+      one unit 2^-23 of a partial sum: n * 2^-23 * sum |w| |x|.  m13 and m2 stand
+      for |w| where the sum is made of larger terms (4 bits: w4_magnitudes)
     * silu: |silu'| <= 1.1, and 2^-20 relative for exp, divide and product
     * h and y are rounded to bf16 once each: 2^-8 relative
     """
@@ -133,11 +143,12 @@ def moe_swiglu_bound(x, idx, gates, w13, w2) -> np.ndarray:
             w1, w3 = w13[e, :F], w13[e, F:]
             a, b = w1 @ x[t], w3 @ x[t]
             ax = np.abs(x[t])
-            da, db = d * 2.0**-23 * (np.abs(w1) @ ax), d * 2.0**-23 * (np.abs(w3) @ ax)
+            m = np.abs(w13[e]) if m13 is None else m13[e]
+            da, db = d * 2.0**-23 * (m[:F] @ ax), d * 2.0**-23 * (m[F:] @ ax)
             h = silu(a) * b
             dh = 1.1 * da * (np.abs(b) + db) + np.abs(silu(a)) * db + 2.0**-20 * np.abs(h)
             dh = dh + 2.0**-8 * (np.abs(h) + dh)
             aw2, g = np.abs(w2[e]), abs(gates[t, j])
-            err[t] += g * (aw2 @ dh + (F + 4) * 2.0**-23 * (aw2 @ (np.abs(h) + dh)))
+            err[t] += g * (aw2 @ dh + (F + 4) * 2.0**-23 * ((aw2 if m2 is None else m2[e]) @ (np.abs(h) + dh)))
             err[t] += (k + 2) * 2.0**-23 * g * (aw2 @ np.abs(h))
     return err + 2.0**-8 * (np.abs(ref) + err)

@@ -105,13 +105,20 @@ def w4_weight(lead, N, K, group, zeros, seed):
     return tuple(None if t is None else t.to(DEV) for t in (codes, scales, z)), values
 
 
+def w4_terms(w):
+    """few.w4_magnitudes of a device weight."""
+    return few.w4_magnitudes(w[0].cpu().numpy(), f64(w[1]), None if w[2] is None else w[2].cpu().numpy())
+
+
 def check_linear(rows, K, N, group, zeros, bias, seed=0):
     x = randn((rows, K), seed + rows)
     w, values = w4_weight((), N, K, group, zeros, seed + K + N)
     b = randn((N,), seed + 9) if bias else None
     y = dg.w4_linear(x.to(DEV), *w, bias=None if b is None else b.to(DEV))
     ref = few.w4_linear(f64(x), values, None if b is None else f64(b))
-    acc = (K + 8) * 2.0**-23 * (np.abs(f64(x)) @ np.abs(values).T) + 2.0**-23 * np.abs(ref)
+    # sums of codes * x and of zero points * x, made apart: (K + 8) additions of terms s (q + z) |x| at most, and
+    # the staged x, off by 2^-40 of its row's largest, which 2^-23 of one such term in 2^17 covers
+    acc = (K + 8) * 2.0**-23 * (np.abs(f64(x)) @ w4_terms(w).T) + 2.0**-23 * np.abs(ref)
     within(y, ref, acc + 2.0**-8 * (np.abs(ref) + acc), f"w4_linear {rows, K, N, group, zeros, bias}")
 
 
@@ -303,7 +310,8 @@ def check_moe(T, d, F, E, idx, gates, seed=0, group=0, zeros=False):
         y = dg.moe_swiglu(x.to(DEV), idx.to(DEV), gates.to(DEV), b13.to(DEV), b2.to(DEV))
     i, gt = idx.numpy(), f64(gates)
     ref = few.moe_swiglu(f64(x), i, gt, v13, v2)
-    within(y, ref, few.moe_swiglu_bound(f64(x), i, gt, v13, v2), f"moe {T, d, F, E, group, zeros}")
+    terms = (w4_terms(w13), w4_terms(w2)) if group else ()
+    within(y, ref, few.moe_swiglu_bound(f64(x), i, gt, v13, v2, *terms), f"moe {T, d, F, E, group, zeros}")
     # and in the norm: h and y each rounded to bf16, 2^-8 apiece at most
     assert np.linalg.norm(f64(y) - ref) <= 2 * 2.0**-8 * max(np.linalg.norm(ref), 1e-30)
     return y
@@ -413,7 +421,8 @@ def test_a_routed_decode_step_together():
         v13, v2 = (f64(w) if torch.is_tensor(w) else few.w4_values(w[0].cpu().numpy(), f64(w[1]), None)
                    for w in (w13, w2))
         args = (f64(h), ri, f64(gates), v13, v2)
-        within(y, few.moe_swiglu(*args), few.moe_swiglu_bound(*args), "moe_layer")
+        terms = () if torch.is_tensor(w13) else (w4_terms(w13), w4_terms(w2))
+        within(y, few.moe_swiglu(*args), few.moe_swiglu_bound(*args, *terms), "moe_layer")
     # the dequantised weights through the bf16 layer: the same experts up to the rounding of the values
     y4 = dg.moe_swiglu_w4(h, idx, gates, q13, q2)
     yd = dg.moe_swiglu(h, idx, gates, dg.w4_dequantize(*q13), dg.w4_dequantize(*q2))
