@@ -68,6 +68,7 @@ __device__ __forceinline__ void two_sum(float& s, float& c, float p) {
 constexpr int kLogitWarps = 8;
 constexpr int kLogitTokens = 4;
 constexpr int kLogitExperts = 2;
+constexpr int kLogitSpread = 12;
 
 // logits[t, e]: a warp takes kLogitExperts experts and kLogitTokens tokens, and one
 // of KS slices of d (KS > 1 where there are too few of both to fill the GPU).  The
@@ -84,7 +85,6 @@ __global__ void __launch_bounds__(kLogitWarps * 32)
                       float* __restrict__ logits, int T, int d, int E, const uint32_t* err) {
   __shared__ float2 slices[KS > 1 ? kLogitWarps : 1][kLogitExperts * kLogitTokens];
   griddep_wait();
-  griddep_launch_dependents();
   if (err_set(err)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e0 = (static_cast<int>(blockIdx.x) * (kLogitWarps / KS) + warp / KS) * kLogitExperts;
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kLogitWarps * 32)
     if (tokens == kLogitTokens) products(std::true_type{});
     else products(std::false_type{});
   }
+  griddep_launch_dependents();  // not before: waiting CTAs beside these took up to 10 us more
 #pragma unroll
   for (int j = 0; j < kLogitExperts; ++j)
 #pragma unroll
@@ -809,11 +810,17 @@ int moe_max_topk() { return kMaxTopk; }
 cudaError_t launch_moe_logits(const void* x, const void* wr, float* logits, int T, int d, int E, const DeviceInfo& dev,
                               cudaStream_t s) {
   const int pairs = (E + kLogitExperts - 1) / kLogitExperts, blocks = (T + kLogitTokens - 1) / kLogitTokens;
-  // a warp for every pair of experts and block of tokens; fewer than four warps an SM: eight
-  const bool split = static_cast<int64_t>(pairs) * blocks < 4 * dev.num_sms;
-  const int a_cta = split ? 1 : kLogitWarps;
-  return launch_pdl(split ? moe_logits_kernel<kLogitWarps> : moe_logits_kernel<1>,
-                    dim3((pairs + a_cta - 1) / a_cta, blocks), dim3(kLogitWarps * 32), 0, s,
+  // a warp for every pair of experts and block of tokens; with fewer than kLogitSpread
+  // warps an SM, 2, 4 or 8, to which d is split.  32 x 7168 on 256 experts: 26.7 us, with
+  // one warp 29.9; 200 x 4096 on 64: 23.7, 27.8; 16 x 4096 on 128: 10.3 with 8, 10.0 with 4.
+  const int64_t warps = static_cast<int64_t>(pairs) * blocks, want = static_cast<int64_t>(kLogitSpread) * dev.num_sms;
+  const int KS = warps >= want ? 1 : 2 * warps >= want ? 2 : 4 * warps >= want ? 4 : 8;
+  auto kern = KS == 1   ? moe_logits_kernel<1>
+              : KS == 2 ? moe_logits_kernel<2>
+              : KS == 4 ? moe_logits_kernel<4>
+                        : moe_logits_kernel<8>;
+  const int a_cta = kLogitWarps / KS;
+  return launch_pdl(kern, dim3((pairs + a_cta - 1) / a_cta, blocks), dim3(kLogitWarps * 32), 0, s,
                     static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(wr), logits, T, d, E,
                     static_cast<const uint32_t*>(dev.err));
 }
