@@ -380,12 +380,13 @@ cudaError_t launch_w4_dequantize(const void* codes, const void* scales, const vo
   return launch_dequant_g<128>(codes, scales, zeros, w, vecs, s);
 }
 
-// Up to 8 rows whose staged form takes no more than 32 KB are staged by every CTA
-// itself, which leaves three CTAs an SM.  One row of 4096 takes 8.6 us so; another
-// kernel before the product is 2.5 to 5 us by itself, and past 32 KB the third CTA
-// would go (1 x 4096 -> 28672: 18 us with three, 21 with two).
+// Up to 8 rows whose staged form takes no more than 16 KB are staged by every CTA
+// itself, which saves a launch: 1 x 2048 -> 4096 takes 5.2 us so, and 5.9 behind a
+// staging kernel; 1 x 4096 -> 6144 9.1 and 8.7, with 2 us less for the host.  With more
+// the CTAs' own staging costs more than the kernel: 3 x 5120 -> 5120 12.7 and 9.9 us,
+// 2 x 4096 -> 4096 8.1 and 7.1, 1 x 14336 -> 4096 14.0 and 12.2.
 bool w4_linear_local(int64_t rows, int64_t K, int group) {
-  return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group, true) <= 32 * 1024;
+  return rows <= 8 && K <= 32768 && w4_staged_bytes(rows, static_cast<int>(K), group, true) <= 16 * 1024;
 }
 
 size_t w4_linear_scratch_bytes(int64_t rows, int64_t K) {
