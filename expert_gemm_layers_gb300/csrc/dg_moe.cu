@@ -477,7 +477,7 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const int* pai
 
 // One unit: block `b` (16 rows of F, or 32 of d) of an entry's expert for a warp,
 // its `count` pairs as columns.
-template <int FMT, int NT, bool UP, bool LOCAL>
+template <int FMT, int NT, bool UP, bool LOCAL, bool AHEAD>
 __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int* pairs, int count, int b, int rg,
                                          int wk, uint8_t* smem, bool failed) {
   const int lane = threadIdx.x & 31, g = lane >> 2, warp = threadIdx.x >> 5;
@@ -526,7 +526,7 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
                       smem + kRowWarps * w4_warp_bytes<FMT, NT>() + wk * w4_xring_bytes<FMT, NT>(), rg * 32 + lane,
                       32 * (kRowWarps / WK), (steps + WK - 1) / WK, acc);
     } else if (active) {
-      stream.template run<LOCAL, false>(w4_cols<FMT, NT>(in, K, count, column), acc);
+      stream.template run<LOCAL, AHEAD>(w4_cols<FMT, NT>(in, K, count, column), acc);
     }
     if (active) w4_unscale<NT>(acc, LOCAL ? nullptr : in.factor, count, column);
     if (WK > 1) join_slices<NT>(acc, joins, rg, wk, WK);
@@ -535,9 +535,16 @@ __device__ __forceinline__ void moe_unit(const ProductArgs& a, int e, const int*
 }
 
 // CTAs an SM holds by registers.
-template <int FMT, int NTMAX>
+// 4 bits, up to 8 pairs an entry, staged by a kernel in front: two CTAs, whose lanes
+// have the registers to ask for activations a step ahead (128 experts of 3 x 2048 x 768,
+// 48 tokens: 101 us, with three CTAs and no asking 109).
+template <int FMT, int NTMAX, bool LOCAL>
+constexpr bool moe_ahead() {
+  return FMT != kFmtBf16 && NTMAX == 1 && !LOCAL;
+}
+template <int FMT, int NTMAX, bool LOCAL>
 constexpr int moe_ctas() {
-  return NTMAX == 1 ? 3 : 2;
+  return NTMAX == 1 && !moe_ahead<FMT, NTMAX, LOCAL>() ? 3 : 2;
 }
 
 // Both products walk (entry, row block) units; a CTA takes units blockIdx.x,
@@ -548,9 +555,9 @@ constexpr int moe_ctas() {
 // GPU time of a whole call and its floor by the touched experts' bytes, 3 x 4096 x 1792
 // an expert: bf16, 1 token on 8 experts 67 to 71 us (52), 128 tokens on 64 experts 468 to
 // 504 us (416); groups of 128, 1 token 38 us (13).  3 x 1288 x 1400, 77 tokens on 60
-// experts: 143 us (96); 3 x 2048 x 768 in groups of 64, 48 tokens on 128: 109 us (47).
+// experts: 143 us (96); 3 x 2048 x 768 in groups of 64, 48 tokens on 128: 101 us (47).
 template <int FMT, int NTMAX, bool UP, bool LOCAL>
-__global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
+__global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX, LOCAL>())
     moe_product_kernel(const __grid_constant__ ProductArgs a, const uint32_t* err) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int small_map[LOCAL ? 4 + 3 * 64 + 32 : 1];
@@ -574,21 +581,21 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX>())
     const int* pairs = m.pairs + m.start[entry];
     if constexpr (NTMAX >= 4) {
       if (count > 24) {
-        moe_unit<FMT, 4, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 4, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
       if (count > 16) {
-        moe_unit<FMT, 3, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 3, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
     }
     if constexpr (NTMAX >= 2) {
       if (count > 8) {
-        moe_unit<FMT, 2, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+        moe_unit<FMT, 2, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
     }
-    moe_unit<FMT, 1, UP, LOCAL>(a, e, pairs, count, b, rg, wk, smem, failed);
+    moe_unit<FMT, 1, UP, LOCAL, moe_ahead<FMT, NTMAX, LOCAL>()>(a, e, pairs, count, b, rg, wk, smem, failed);
   }
 }
 
@@ -635,7 +642,7 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
   const int entries = a.npairs < a.E ? a.npairs : a.E;  // active experts, at most
   constexpr bool W4 = FMT != kFmtBf16;
   const int steps = W4 ? w4_steps(K) : (K + kBfStep - 1) / kBfStep;
-  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX>(), W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
+  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX, LOCAL>(), W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
   int smem;
   if constexpr (W4)
     smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT, true)) : 0);
@@ -649,15 +656,17 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
                                                                     : (a.d + 32 * RG - 1) / (32 * RG));
   // as many CTAs as the SM's shared memory and registers hold at a time
   int per_sm = 228 * 1024 / (smem + 1024);
-  per_sm = per_sm < 1 ? 1 : per_sm > moe_ctas<FMT, NTMAX>() ? moe_ctas<FMT, NTMAX>() : per_sm;
+  per_sm = per_sm < 1 ? 1 : per_sm > moe_ctas<FMT, NTMAX, LOCAL>() ? moe_ctas<FMT, NTMAX, LOCAL>() : per_sm;
   int64_t grid = static_cast<int64_t>(per_sm) * dev.num_sms;
   if (grid > units) grid = units;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kMoeThreads), smem, s, a,
                     static_cast<const uint32_t*>(dev.err));
 }
 
-// Shared memory of the staged rows of a unit that lets three CTAs share an SM.
-constexpr int64_t kLocalBytes = 24 * 1024;
+// Staged rows of a unit, at most, that every CTA makes for itself.  1 token of 4096
+// (8.6 KB): 38.0 us so, and 37.5 with two staging kernels, which cost the host 4 us; 4
+// tokens of 2048 (16.4 KB), 6 of 64 experts of 768 in groups of 32: 43 and 36 us.
+constexpr int64_t kLocalBytes = 10 * 1024;
 
 template <int FMT, bool UP>
 cudaError_t launch_product_nt(const ProductArgs& a, bool local, int ntmax, const DeviceInfo& dev, cudaStream_t s) {
