@@ -575,22 +575,31 @@ __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX, LOCAL>())
   const int wk = warp % a.WK, rg = warp / a.WK, RG = kMoeWarps / a.WK;
   const int blocks = UP ? (a.F + 16 * RG - 1) / (16 * RG) : (a.d + 32 * RG - 1) / (32 * RG);
   const int units = *m.total * blocks;
+  int last = 0;  // NT of the CTA's last unit
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int entry = u / blocks, b = (u - entry * blocks) * RG + rg;
     const int e = m.expert[entry], count = m.count[entry];
     const int* pairs = m.pairs + m.start[entry];
+    const int nt = NTMAX >= 4 && count > 24 ? 4 : NTMAX >= 4 && count > 16 ? 3 : NTMAX >= 2 && count > 8 ? 2 : 1;
+    if constexpr (NTMAX > 1) {
+      // Rings, staged activations and joins lie elsewhere for another NT.  Warps leave a
+      // unit one by one (NT = 1 has no barrier, and the first of a row block still reads
+      // the joins), so all are through with it before any fills the next one's.
+      if (last != 0 && nt != last) __syncthreads();
+      last = nt;
+    }
     if constexpr (NTMAX >= 4) {
-      if (count > 24) {
+      if (nt == 4) {
         moe_unit<FMT, 4, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
-      if (count > 16) {
+      if (nt == 3) {
         moe_unit<FMT, 3, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
     }
     if constexpr (NTMAX >= 2) {
-      if (count > 8) {
+      if (nt == 2) {
         moe_unit<FMT, 2, UP, LOCAL, false>(a, e, pairs, count, b, rg, wk, smem, failed);
         continue;
       }
