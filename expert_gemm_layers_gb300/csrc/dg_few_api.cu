@@ -68,6 +68,8 @@ dg_status launched(cudaError_t e, const char* what) {
 constexpr int64_t kMaxDim = 0x7fffffff;
 constexpr int64_t kMaxW4Rows = int64_t(1) << 31;
 constexpr int64_t kMaxW4LinearRows = 65535 * 32;
+// the router's column index steps by up to 2 * 8 * 256 past the last column in 32 bits
+constexpr int64_t kMaxRouteDim = kMaxDim + 1 - 8192;
 
 dg_status check_w4(int64_t rows, int64_t K, int32_t group, const char* what) {
   if (group != 32 && group != 64 && group != 128)
@@ -202,8 +204,8 @@ dg_status dg_moe_route(int64_t T, int64_t d, int32_t E, int32_t k, uint32_t flag
   if (E > moe_max_experts() || k > moe_max_topk())
     return fail(DG_ERR_UNSUPPORTED, "moe_route: more than %d experts or %d choices per token", moe_max_experts(),
                 moe_max_topk());
-  if (d > kMaxDim - 256 || T > 65535 * 4)
-    return fail(DG_ERR_UNSUPPORTED, "moe_route: more than %d tokens, or d beyond 2^31 - 256", 65535 * 4);
+  if (d > kMaxRouteDim || T > 65535 * 4)
+    return fail(DG_ERR_UNSUPPORTED, "moe_route: more than %d tokens, or d beyond 2^31 - 8192", 65535 * 4);
   if (T == 0) return DG_OK;
   const size_t need = dg_moe_route_workspace_bytes(T, d, E, k);
   const Arg args[] = {{"x", x, static_cast<size_t>(T) * d * 2, false, false},

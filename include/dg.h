@@ -434,7 +434,7 @@ dg_status dg_w4_linear(int64_t rows, int64_t in_features, int64_t out_features, 
  *   DG_MOE_SIGMOID: 1 / (1 + exp(-l)), with DG_MOE_RENORM / sum over the chosen
  * times `scale`.  A token with a NaN among its logits gets NaN gates.
  *   x [T, d] bf16, w_router [E, d] bf16, idx [T, k] int32, gates [T, k] f32
- *   T >= 0 (0 = nothing to do), at most 65535 * 4; d % 8 == 0;
+ *   T >= 0 (0 = nothing to do), at most 65535 * 4; d % 8 == 0, d <= 2^31 - 8192;
  *   1 <= k <= min(E, 32); E <= 1024
  *
  * dg_moe_swiglu.  For every pair (t, j) with 0 <= idx[t, j] < E,
