@@ -10,11 +10,12 @@
 //    (16 q1, 16 q5) * 2^-24.  With word >> 8 that makes 5 operations for 8 codes
 //    (inserting an exponent and subtracting the zero point would take 11).
 //  - The activations are brought to that form once (w4_stage_row, w4_stage_local): a
-//    row, or 128 columns of it, is scaled by a power of two to magnitudes below 2^15, rounded to fp16, columns 1 3 5 7
-//    of 8 divided by 16, in the order the lanes take them.  A bf16 number has 8
-//    significant bits, so it fits fp16's 11 exactly unless it is 2^28 times smaller
-//    than the row's largest; then it is off by at most 2^-40 of that largest, far
-//    below one unit of the binary32 sum.
+//    row, or 128 columns of it, is scaled by a power of two so that its largest
+//    magnitude lies between 2^14 and 2^15, rounded to fp16, columns 1 3 5 7 of 8
+//    divided by 16, in the order the lanes take them.  A bf16 number has 8 significant
+//    bits and fp16 numbers come in steps of 2^-24, so all down to 2^-27 of the largest
+//    are exact.  Smaller ones are off by at most half a step: 2^-25 of 2^14, that is
+//    2^-39 of the largest, and 16 times that, 2^-35, in the odd columns.
 //  - The zero point is taken out of the group's sum at the end:
 //    sum (q - z) x = sum q x - z * sum x, the second sum made with the scaling.
 //

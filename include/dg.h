@@ -405,7 +405,9 @@ dg_status dg_tp_linear_bwd(int64_t rows, int64_t in_features, int64_t out_featur
  * the call.
  * An activation that is not finite makes its row of y not finite.  The kernel
  * sums q x and z x apart: a sum is off by at most about in_features * 2^-23 of
- * sum scale (q + z) |x|.  A group of zeros as w4_quantize writes it (all codes at
+ * sum scale (q + z) |x|.  In q x it holds an activation exactly down to 2^-27 of
+ * the largest finite one of its row, and below that to 2^-35 of that largest, which adds
+ * at most 2^-35 max|x| sum scale q.  A group of zeros as w4_quantize writes it (all codes at
  * the zero point, scale 1) adds exactly nothing.
  * These calls have no backward: the codes are not trained.
  * ------------------------------------------------------------------------ */

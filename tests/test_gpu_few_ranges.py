@@ -1,0 +1,30 @@
+"""Few-token operators on values far apart: activations that span more than the staged form holds."""
+import numpy as np
+import pytest
+
+import expert_gemm_layers_gb300 as dg
+from oracle import few
+from test_gpu_few import DEV, f64, randn, w4_terms, w4_weight, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [1, 5, 9, 20])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("small", [2.0**-3, 2.0**-9, 2.0**-14, 2.0**-22])
+def test_a_large_activation_on_a_zero_weight(rows, group, small):
+    """Activations 2^23 to 2^42 times smaller than their row's largest, which meets codes and zero points of 0."""
+    K, N = 2 * group if group > 32 else 160, 40
+    x = randn((rows, K), rows) * small
+    x[:, 0] = 2.0**20
+    (codes, scales, zeros), _ = w4_weight((), N, K, group, True, 4)
+    codes[:, 0] &= 0xF0      # column 0, the low nibble: code 0
+    zeros[:, 0] = 0          # of its group
+    y = dg.w4_linear(x.to(DEV), codes, scales, zeros)
+    xs, z, s = f64(x), zeros.cpu().numpy(), f64(scales)
+    ref = few.w4_linear(xs, few.w4_values(codes.cpu().numpy(), s, z))
+    # (K + 8) additions of terms s (q + z) |x| at most; activations held to 2^-35 of the largest in s q x
+    acc = (K + 8) * 2.0**-23 * (np.abs(xs) @ w4_terms((codes, scales, zeros)).T)
+    held = 2.0**-35 * np.abs(xs).max(1, keepdims=True) * few.w4_values(codes.cpu().numpy(), s, 0 * z).sum(1)
+    acc = acc + held + 2.0**-23 * np.abs(ref)
+    within(y, ref, acc + 2.0**-8 * (np.abs(ref) + acc), f"{rows, group, small}")
