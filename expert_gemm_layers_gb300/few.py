@@ -161,8 +161,11 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     else:
         _check(out, "out", BF16, (*lead, out_f), index)
     rows = x.numel() // in_f if in_f else 0
+    nbytes = lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f)
     if ws is None:
-        ws = _scratch(index, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f))
+        ws = _scratch(index, nbytes)
+    else:
+        _need_workspace(ws, nbytes, index)
     _launch(lib.dg_w4_linear, index, rows, in_f, out_f, group, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
             _p(zeros), _p(bias), out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
