@@ -32,15 +32,15 @@ def launches(monkeypatch, lib):  # noqa: F811
 
 def test_w4_linear_checks_the_workspace_it_is_given(launches, lib):  # noqa: F811
     x, codes, scales = on_gpu(20, 256, dtype=BF16), on_gpu(40, 128, dtype=U8), on_gpu(40, 8, dtype=BF16)
-    need = lib.dg_w4_linear_workspace_bytes(20, 256, 40)
+    need, out = lib.dg_w4_linear_workspace_bytes(20, 256, 40), on_gpu(20, 40, dtype=BF16)
     for ws, error, match in ((torch.zeros(need, dtype=U8), ValueError, "CUDA"),          # a host address
                              (on_gpu(need, dtype=torch.int8), TypeError, "uint8"),
                              (on_gpu(2 * need, dtype=U8)[::2], ValueError, "contiguous"),
                              (on_gpu(need - 1, dtype=U8), ValueError, "needs"),
                              (need, TypeError, "tensor")):
         with pytest.raises(error, match=match):
-            few.w4_linear(x, codes, scales, ws=ws)
+            few.w4_linear(x, codes, scales, out=out, ws=ws)
     assert not launches
     ws = on_gpu(need, dtype=U8)
-    few.w4_linear(x, codes, scales, out=on_gpu(20, 40, dtype=BF16), ws=ws)
+    few.w4_linear(x, codes, scales, out=out, ws=ws)
     assert len(launches) == 1 and launches[0][1][-2:] == (ws.data_ptr(), need)
