@@ -9,6 +9,8 @@ require gradients are taken as constants.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from ._lib import DG_ERROR_BLOCK_BYTES, DG_MOE_RENORM, DG_MOE_SIGMOID, MoEShape, check, load
@@ -93,6 +95,22 @@ def _need_workspace(ws: torch.Tensor, nbytes: int, index: int) -> None:
         raise ValueError(f"workspace has {ws.numel()} bytes, needs {nbytes}")
 
 
+# Threads can have the same current stream, and a call is several kernels: those of two calls
+# on this module's workspace are not to mix.
+_scratch_lock = threading.RLock()
+
+
+def _launch_with(workspace, nbytes: int, fn, index: int, *args) -> None:
+    """_launch with a workspace of at least `nbytes` as the last arguments: the caller's, or (None) this module's."""
+    if workspace is not None:
+        _need_workspace(workspace, nbytes, index)
+        _launch(fn, index, *args, workspace.data_ptr(), workspace.numel())
+    else:
+        with _scratch_lock:
+            workspace = _scratch(index, nbytes)
+            _launch(fn, index, *args, workspace.data_ptr(), workspace.numel())
+
+
 # ------------------------------------------------------------------ 4-bit weights
 
 def _need_w4(codes, scales, zeros, lead: tuple, K: int, index: int, what: str) -> int:
@@ -161,13 +179,8 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, zeros:
     else:
         _check(out, "out", BF16, (*lead, out_f), index)
     rows = x.numel() // in_f if in_f else 0
-    nbytes = lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f)
-    if ws is None:
-        ws = _scratch(index, nbytes)
-    else:
-        _need_workspace(ws, nbytes, index)
-    _launch(lib.dg_w4_linear, index, rows, in_f, out_f, group, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-            _p(zeros), _p(bias), out.data_ptr(), ws.data_ptr(), ws.numel())
+    _launch_with(ws, lib.dg_w4_linear_workspace_bytes(rows, in_f, out_f), lib.dg_w4_linear, index, rows, in_f, out_f,
+                 group, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _p(zeros), _p(bias), out.data_ptr())
     return out
 
 
@@ -192,33 +205,23 @@ def moe_route(x: torch.Tensor, w_router: torch.Tensor, top_k: int, score: str = 
     flags = (DG_MOE_SIGMOID if score == "sigmoid" else 0) | (DG_MOE_RENORM if renormalize else 0)
     idx = torch.empty((T, top_k), dtype=I32, device=x.device)
     gates = torch.empty((T, top_k), dtype=F32, device=x.device)
-    nbytes = lib.dg_moe_route_workspace_bytes(T, d, E, top_k)
-    if workspace is None:
-        workspace = _scratch(index, nbytes)
-    else:
-        _need_workspace(workspace, nbytes, index)
-    _launch(lib.dg_moe_route, index, T, d, E, top_k, flags, scale, x.data_ptr(), w_router.data_ptr(), idx.data_ptr(),
-            gates.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _launch_with(workspace, lib.dg_moe_route_workspace_bytes(T, d, E, top_k), lib.dg_moe_route, index, T, d, E, top_k,
+                 flags, scale, x.data_ptr(), w_router.data_ptr(), idx.data_ptr(), gates.data_ptr())
     return idx, gates
 
 
-def _moe_args(index, x, idx, gates, workspace, out, F: int, E: int, group: int):
-    """Checks the tensors both weight formats share; returns (shape, workspace, out)."""
+def _moe_args(index, x, idx, gates, out, F: int, E: int, group: int):
+    """Checks the tensors both weight formats share; returns (shape, workspace bytes, out)."""
     T, d, k = _size(x, 0), _size(x, -1), _size(idx, -1)
     _check(x, "x", BF16, (T, d), index)
     _check(idx, "idx", I32, (T, k), index)
     _check(gates, "gates", F32, (T, k), index)
     sh = MoEShape(T, d, F, E, k)
-    nbytes = load().dg_moe_swiglu_workspace_bytes(sh, group)
-    if workspace is None:
-        workspace = _scratch(index, nbytes)
-    elif nbytes:
-        _need_workspace(workspace, nbytes, index)
     if out is None:
         out = torch.empty_like(x)
     else:
         _check(out, "out", BF16, (T, d), index)
-    return sh, workspace, out
+    return sh, load().dg_moe_swiglu_workspace_bytes(sh, group), out
 
 
 def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
@@ -234,9 +237,9 @@ def moe_swiglu(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13: tor
     E, F = _size(w13, 0), _size(w13, 1) // 2
     _check(w13, "w13", BF16, (E, 2 * F, d), index)
     _check(w2, "w2", BF16, (E, d, F), index)
-    sh, workspace, out = _moe_args(index, x, idx, gates, workspace, out, F, E, 0)
-    _launch(load().dg_moe_swiglu, index, sh, x.data_ptr(), idx.data_ptr(), gates.data_ptr(), w13.data_ptr(),
-            w2.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    sh, nbytes, out = _moe_args(index, x, idx, gates, out, F, E, 0)
+    _launch_with(workspace, nbytes, load().dg_moe_swiglu, index, sh, x.data_ptr(), idx.data_ptr(), gates.data_ptr(),
+                 w13.data_ptr(), w2.data_ptr(), out.data_ptr())
     return out
 
 
@@ -250,10 +253,10 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
     group = _need_w4(c13, s13, z13, (E, 2 * F), d, index, "w13 ")
     if _need_w4(c2, s2, z2, (E, d), F, index, "w2 ") != group:
         raise ValueError("w13 and w2 must have the same group size")
-    sh, workspace, out = _moe_args(index, x, idx, gates, workspace, out, F, E, group)
-    _launch(load().dg_moe_swiglu_w4, index, sh, group, x.data_ptr(), idx.data_ptr(), gates.data_ptr(),
-            c13.data_ptr(), s13.data_ptr(), _p(z13), c2.data_ptr(), s2.data_ptr(), _p(z2), out.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+    sh, nbytes, out = _moe_args(index, x, idx, gates, out, F, E, group)
+    _launch_with(workspace, nbytes, load().dg_moe_swiglu_w4, index, sh, group, x.data_ptr(), idx.data_ptr(),
+                 gates.data_ptr(), c13.data_ptr(), s13.data_ptr(), _p(z13), c2.data_ptr(), s2.data_ptr(), _p(z2),
+                 out.data_ptr())
     return out
 
 

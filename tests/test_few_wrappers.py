@@ -1,4 +1,7 @@
 """The few-token wrappers' host side, without a GPU: tensors that pass for a GPU's, launches that are recorded."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -44,3 +47,56 @@ def test_w4_linear_checks_the_workspace_it_is_given(launches, lib):  # noqa: F81
     ws = on_gpu(need, dtype=U8)
     few.w4_linear(x, codes, scales, out=out, ws=ws)
     assert len(launches) == 1 and launches[0][1][-2:] == (ws.data_ptr(), need)
+
+
+class SlowLibrary:
+    """Sizes from the library; a launch takes a while, and notes whether another is under way on its workspace."""
+
+    def __init__(self, lib):
+        self.lib, self.busy, self.calls, self.shared = lib, set(), 0, 0
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.lib, name)
+
+        def launch(*args):
+            ws = args[-3]
+            self.calls += 1
+            self.shared += ws in self.busy
+            self.busy.add(ws)
+            time.sleep(0.002)    # ctypes lets other threads run during a call
+            self.busy.discard(ws)
+            return 0
+        return launch
+
+
+@pytest.fixture
+def one_stream(monkeypatch, lib):  # noqa: F811
+    """All threads on one stream of one device, workspaces in host memory."""
+    slow = SlowLibrary(lib)
+    monkeypatch.setattr(few, "load", lambda: slow)
+    monkeypatch.setattr(few, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(few, "_current_device", lambda: 0)
+    monkeypatch.setattr(few, "_capturing", lambda index: False)
+    monkeypatch.setattr(few, "alloc_workspace", lambda n, device: torch.zeros(n, dtype=U8))
+    monkeypatch.setattr(few, "_scratch_cache", {})
+    return slow
+
+
+def test_calls_of_two_threads_do_not_mix_on_one_workspace(one_stream):
+    x, out = on_gpu(20, 256, dtype=BF16), on_gpu(20, 40, dtype=BF16)
+    codes, scales = on_gpu(40, 128, dtype=U8), on_gpu(40, 8, dtype=BF16)
+    idx, gates = on_gpu(20, 2, dtype=I32), on_gpu(20, 2, dtype=F32)
+    w13, w2, y = on_gpu(3, 16, 256, dtype=BF16), on_gpu(3, 256, 8, dtype=BF16), on_gpu(20, 256, dtype=BF16)
+
+    def work():
+        for _ in range(10):
+            few.w4_linear(x, codes, scales, out=out)
+            few.moe_swiglu(x, idx, gates, w13, w2, out=y)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert one_stream.calls == 80 and one_stream.shared == 0
