@@ -73,19 +73,22 @@ def _p(t):
 
 
 _scratch_cache: dict = {}
+_KEEP_BYTES = 64 << 20
 
 
 def _scratch(index: int, nbytes: int) -> torch.Tensor:
     """The workspace this module gives calls that bring none: one per (device,
     current stream), grown as needed, its error block zeroed when it is made.
     A captured call gets one of its own, in the graph's memory, so that graphs
-    captured on one stream do not share it."""
+    captured on one stream do not share it; a call that needs more than
+    _KEEP_BYTES gets one that goes back to torch after it (calls of that size take
+    far longer than to zero an error block)."""
+    if nbytes > _KEEP_BYTES or _capturing(index):
+        return alloc_workspace(nbytes, torch.device("cuda", index))
     key = (index, _raw_stream(index))
     ws = _scratch_cache.get(key)
-    if ws is None or ws.numel() < nbytes or _capturing(index):
-        ws = alloc_workspace(max(nbytes, DG_ERROR_BLOCK_BYTES), torch.device("cuda", index))
-        if not _capturing(index):
-            _scratch_cache[key] = ws
+    if ws is None or ws.numel() < nbytes:
+        ws = _scratch_cache[key] = alloc_workspace(nbytes, torch.device("cuda", index))
     return ws
 
 

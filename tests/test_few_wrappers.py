@@ -100,3 +100,13 @@ def test_calls_of_two_threads_do_not_mix_on_one_workspace(one_stream):
     for t in threads:
         t.join()
     assert one_stream.calls == 80 and one_stream.shared == 0
+
+
+def test_a_large_workspace_is_not_kept(one_stream):
+    codes, scales = on_gpu(8, 16, dtype=U8), on_gpu(8, 1, dtype=BF16)
+    sizes = []
+    for rows in (1, 30000, 20, 400000, 1):    # scratch of 0, 10, 0.1 and 133 MB
+        few.w4_linear(on_gpu(rows, 32, dtype=BF16), codes, scales, out=on_gpu(rows, 8, dtype=BF16))
+        sizes.append(sum(ws.numel() for ws in few._scratch_cache.values()))
+    assert sizes[0] < 1 << 20 < 8 << 20 < sizes[1] == sizes[-1] <= few._KEEP_BYTES
+    assert one_stream.calls == 5
