@@ -5,7 +5,7 @@ scratch with torch and passes pointers and the current stream to the C ABI.
 Weights in 4 bits are (codes, scales, zeros) as w4_quantize returns them:
 codes [..., K/2] uint8, scales [..., K/group] bf16, zeros [..., K/group] uint8
 or None (zero point 8).  None of these operators has a backward: inputs that
-require gradients are taken as constants.
+require gradients are taken as constants, and refused by moe_layer.
 """
 from __future__ import annotations
 
@@ -266,7 +266,14 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
 def moe_layer(x: torch.Tensor, w_router: torch.Tensor, w13, w2, top_k: int, score: str = "softmax",
               renormalize: bool = True, scale: float = 1.0, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """A whole routed layer for few tokens: moe_route, then moe_swiglu (bf16 w13, w2) or moe_swiglu_w4
-    (w13, w2 as (codes, scales, zeros))."""
+    (w13, w2 as (codes, scales, zeros)).  `workspace` is the experts' (the router takes this stream's own).
+
+    Unlike the other *_layer functions it is not differentiable: tensors that require gradients are
+    refused where autograd records (run it under torch.no_grad())."""
+    if torch.is_grad_enabled():
+        weights = (w13, w2) if isinstance(w13, torch.Tensor) else (*w13, *w2)
+        if any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, w_router, *weights)):
+            raise RuntimeError("moe_layer has no backward: run it under torch.no_grad(), or detach its inputs")
     idx, gates = moe_route(x, w_router, top_k, score, renormalize, scale)
     call = moe_swiglu if isinstance(w13, torch.Tensor) else moe_swiglu_w4
     return call(x, idx, gates, w13, w2, workspace=workspace)

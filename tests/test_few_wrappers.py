@@ -110,3 +110,25 @@ def test_a_large_workspace_is_not_kept(one_stream):
         sizes.append(sum(ws.numel() for ws in few._scratch_cache.values()))
     assert sizes[0] < 1 << 20 < 8 << 20 < sizes[1] == sizes[-1] <= few._KEEP_BYTES
     assert one_stream.calls == 5
+
+
+def test_moe_layer_refuses_to_drop_gradients(launches, monkeypatch):
+    monkeypatch.setattr(few, "moe_route", lambda *args: ("idx", "gates"))
+    monkeypatch.setattr(few, "moe_swiglu", lambda *args, workspace: "bf16")
+    monkeypatch.setattr(few, "moe_swiglu_w4", lambda *args, workspace: "4 bits")
+    plain = [on_gpu(*s, dtype=BF16) for s in ((2, 64), (3, 64), (3, 16, 64), (3, 64, 8))]
+    q13, q2 = ((on_gpu(3, n, K // 2, dtype=U8), on_gpu(3, n, 1, dtype=BF16), None) for n, K in ((16, 64), (64, 8)))
+    assert few.moe_layer(*plain, 1) == "bf16" and few.moe_layer(*plain[:2], q13, q2, 1) == "4 bits"
+    for i in range(4):
+        args = list(plain)
+        args[i] = torch.zeros(plain[i].shape, dtype=BF16, requires_grad=True)
+        with pytest.raises(RuntimeError, match="no_grad"):
+            few.moe_layer(*args, 1)
+        if i < 2:
+            with pytest.raises(RuntimeError, match="no_grad"):
+                few.moe_layer(*args[:2], q13, q2, 1)
+        with torch.no_grad():
+            assert few.moe_layer(*args, 1) == "bf16"
+    scales = torch.zeros(q2[1].shape, dtype=BF16, requires_grad=True)
+    with pytest.raises(RuntimeError, match="no_grad"):
+        few.moe_layer(*plain[:2], q13, (q2[0], scales, None), 1)
