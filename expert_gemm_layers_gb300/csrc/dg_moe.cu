@@ -229,7 +229,12 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
     if (!sigmoid && !renorm) all += expf(v - top);
   }
   float p = 0.0f;
-  if (lane < k) p = sigmoid ? 1.0f / (1.0f + expf(-mine)) : expf(mine - top);
+  if (lane < k) {
+    // A sigmoid is e^l / (1 + e^l), renormalised times e^-top where all are below 0: gates that
+    // are in proportion to each other do not all vanish where 1 / (1 + e^-l) would.
+    const float shift = renorm ? fminf(top, 0.0f) : 0.0f;
+    p = !sigmoid ? expf(mine - top) : mine > 0.0f ? 1.0f / (1.0f + expf(-mine)) : expf(mine - shift) / (1.0f + expf(mine));
+  }
   float sum = renorm ? p : all;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {

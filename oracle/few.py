@@ -93,7 +93,11 @@ def moe_choose(logits: np.ndarray, k: int, score: str = "softmax", renormalize: 
             if np.isnan(l).any():
                 gates[t] = np.nan
                 continue
-            p = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - l.max())
+            if score == "sigmoid":
+                log_p = -np.logaddexp(0.0, -l)    # renormalised: only in proportion, so that not all vanish
+                p = np.exp(log_p - (log_p.max() if renormalize else 0.0))
+            else:
+                p = np.exp(l - l.max())
             if renormalize:
                 total = p[pick].sum()
             else:

@@ -1,10 +1,12 @@
-"""Few-token operators on values far apart: activations that span more than the staged form holds."""
+"""Few-token operators on values far apart: activations that span more than the staged form holds,
+logits whose sigmoids are below the smallest numbers."""
 import numpy as np
 import pytest
+import torch
 
 import expert_gemm_layers_gb300 as dg
 from oracle import few
-from test_gpu_few import DEV, f64, randn, w4_terms, w4_weight, within
+from test_gpu_few import BF16, DEV, check_route, f64, randn, w4_terms, w4_weight, within
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,19 @@ def test_a_large_activation_on_a_zero_weight(rows, group, small):
     held = 2.0**-35 * np.abs(xs).max(1, keepdims=True) * few.w4_values(codes.cpu().numpy(), s, 0 * z).sum(1)
     acc = acc + held + 2.0**-23 * np.abs(ref)
     within(y, ref, acc + 2.0**-8 * (np.abs(ref) + acc), f"{rows, group, small}")
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("near,far", [(-60.0, -60.0), (-95.0, -95.0), (-150.0, -150.0), (-1000.0, -1000.0),
+                                      (-20.0, -110.0), (30.0, -100.0), (200.0, 100.0)])
+def test_route_sigmoids_of_large_logits(near, far, renorm):
+    """Logits around `near` for every other expert and around `far` for the rest."""
+    d, E = 64, 24
+    w = randn((E, d), 5, 0.25).float()
+    w[::2] += near / d
+    w[1::2] += far / d
+    x = torch.ones((3, d)) + 0.125 * torch.arange(3)[:, None]
+    check_route(x.to(BF16), w.to(BF16), 16, "sigmoid", renorm, 2.5)
+    _, gates = dg.moe_route(x.to(BF16).to(DEV), w.to(BF16).to(DEV), 16, score="sigmoid", renormalize=renorm)
+    if renorm:   # 16 gates that add up to 1, each off by a few units, and so the sum
+        assert torch.isfinite(gates).all() and (gates.sum(1) - 1).abs().max() <= 16 * 2.0**-22
