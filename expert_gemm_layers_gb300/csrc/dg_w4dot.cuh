@@ -38,8 +38,8 @@ constexpr int kW4Step = 128;
 
 // Staged activations: of every row and step 256 bytes of fp16 (pieces of 8
 // columns, [piece of a lane][lane t]); of every row and group the sum of its scaled
-// columns; of every row (or, staged by the product's own CTA, every step of a row)
-// the inverse of its scale.  Rows are padded by 64 bytes against bank conflicts in
+// columns; of every row (or, of up to 8 rows, every step of a row) its factor, a
+// power of two.  Rows are padded by 64 bytes against bank conflicts in
 // shared memory.
 struct Staged {
   uint8_t* frag;
@@ -73,9 +73,16 @@ static __device__ __forceinline__ uint32_t w4_top(const uint4& v) {
   }
   return top;
 }
-// Exponent E of a row's scale 2^(14 - E); the scale is at most 2^114, so that it and
-// its inverse are normal numbers.
+// Exponent E of a row's scale 2^(14 - E); at least -100, so that the scale and the factor
+// are normal numbers.
 static __device__ __forceinline__ int w4_exponent(uint32_t top) { return max(static_cast<int>(top >> 7) - 127, -100); }
+// A row's factor: what its products, in units of 2^-24 for the codes and 2^(E - 14) for
+// the activations, are multiplied by beside kW4Unit.  It goes to the weights' scales
+// before their product with a sum.  The unit is so small that results down to the
+// smallest bf16 numbers are held on the way (with 2^24, results below 2^-117 were not),
+// and no smaller, so that a scale below 32 times the factor of the largest bf16 number is finite.
+constexpr float kW4Unit = 16384.0f;
+static __device__ __forceinline__ float w4_factor(int E) { return __int_as_float((127 - 4 + E) << 23); }
 
 // Stages pieces p of steps `st` of a row: the 16 lanes of half a warp hold the 16
 // pieces of one step; all lanes of the warp call together.  Nothing is written
@@ -133,7 +140,7 @@ static __device__ __forceinline__ void w4_stage_row(const uint8_t* x, int K, uin
     const int st = s0 + (threadIdx.x >> 4);
     w4_stage_piece<GROUP>(piece(st), E, p, st, st < steps, frag, sums);
   }
-  if (threadIdx.x == 0) *factor = __int_as_float((127 - 14 + E) << 23);
+  if (threadIdx.x == 0) *factor = w4_factor(E);
   __syncthreads();
   if (threadIdx.x == 0) *shared_top = 0u;
   __syncthreads();
@@ -159,7 +166,7 @@ static __device__ __forceinline__ void w4_stage_steps(const Staged& out, int cou
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int E = w4_exponent(top);
     w4_stage_piece<GROUP>(v, E, p, st, exists, out.frag + r * rb, out.sums + static_cast<int64_t>(r) * fs);
-    if (exists && p == 0) out.factor[i] = __int_as_float((127 - 14 + E) << 23);
+    if (exists && p == 0) out.factor[i] = w4_factor(E);
   }
 }
 // The same in shared memory, by one CTA, which it synchronises.
@@ -447,7 +454,7 @@ struct W4Stream {
 #pragma unroll
     for (int u = 0; u < R - 1; ++u) fill(c0 + u, u);
   }
-  // acc += the product with staged activation rows, in units of 2^-24 / factor.
+  // acc += the product with staged activation rows, in units of w4_unscale.
   // Thread (g, t) ends with acc[m][n] = (row g of tile m, columns 8n + 2t, 8n + 2t + 1;
   // row g + 8, the same).  NT = 1: an active warp by itself, the lanes read `x`, AHEAD:
   // a step before they use it.  STEP_FACTORS: every step of a row has its factor.
@@ -584,8 +591,8 @@ static __device__ __forceinline__ W4Cols<NT> w4_cols(const Staged& in, int K, in
   return x;
 }
 
-// The sums are in units of 2^-24, those of the codes, and of their row's scale
-// (factor NULL: that has been applied).
+// The sums are in units of 1 / kW4Unit and of their row's factor (NULL: that has been
+// applied).  The factor first, as kW4Unit says.
 template <int NT, typename Act>
 static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc, const float* factor, int count, Act act) {
   const int t = threadIdx.x & 3;
@@ -596,8 +603,8 @@ static __device__ __forceinline__ void w4_unscale(RowSums<NT>& acc, const float*
       const float f = factor ? factor[act(min(8 * n + 2 * t + i, count - 1))] : 1.0f;
 #pragma unroll
       for (int m = 0; m < kRowTiles; ++m) {
-        acc[m][n][i] = acc[m][n][i] * 16777216.0f * f;
-        acc[m][n][2 + i] = acc[m][n][2 + i] * 16777216.0f * f;
+        acc[m][n][i] = acc[m][n][i] * f * kW4Unit;
+        acc[m][n][2 + i] = acc[m][n][2 + i] * f * kW4Unit;
       }
     }
 }

@@ -1,5 +1,5 @@
 """Few-token operators on values far apart: activations that span more than the staged form holds,
-logits whose sigmoids are below the smallest numbers."""
+weights near the smallest numbers, logits whose sigmoids are below them."""
 import numpy as np
 import pytest
 import torch
@@ -30,6 +30,33 @@ def test_a_large_activation_on_a_zero_weight(rows, group, small):
     held = 2.0**-35 * np.abs(xs).max(1, keepdims=True) * few.w4_values(codes.cpu().numpy(), s, 0 * z).sum(1)
     acc = acc + held + 2.0**-23 * np.abs(ref)
     within(y, ref, acc + 2.0**-8 * (np.abs(ref) + acc), f"{rows, group, small}")
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 33])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("weight,activation", [(-131, 0), (-126, 0), (-100, -24), (-40, -90), (-133, 12), (-10, -110),
+                                               (120, -122), (100, -130), (1, 120)])
+def test_w4_linear_of_tiny_and_huge_values(rows, group, weight, activation):
+    """Scales around 2^weight on activations around 2^activation, products down to bf16's subnormal numbers."""
+    K, N = 2 * group, 40
+    x = (randn((rows, K), rows).float() * 2.0**activation).to(BF16)
+    (codes, scales, zeros), _ = w4_weight((), N, K, group, True, 4)
+    scales = torch.ldexp(scales.double() * (4 * K**0.5), torch.tensor(weight, device=DEV)).to(BF16)    # 0.5 to 1.5 before
+    y = dg.w4_linear(x.to(DEV), codes, scales, zeros)
+    w = (codes, scales, zeros)
+    ref = few.w4_linear(f64(x), few.w4_values(codes.cpu().numpy(), f64(scales), zeros.cpu().numpy()))
+    # as elsewhere; then what 32-bit numbers below 2^-126 lose: half of 2^-149 for each of at most 8 group sums
+    # (K / group and the slices' joins) and for the factor's product, in units of 2^-14 of the row's largest
+    # and of 1; and half a step of bf16's, 2^-133
+    xs = f64(x)
+    acc = (K + 8) * 2.0**-23 * (np.abs(xs) @ w4_terms(w).T) + 2.0**-23 * np.abs(ref)
+    acc = acc + 2.0**-150 * 2.0**14 * (8 * np.maximum(np.abs(xs).max(1, keepdims=True), 1.0) + 1)
+    bound = acc + 2.0**-8 * (np.abs(ref) + acc) + 2.0**-134
+    # the largest: 64 to 256 terms of 2^1 * 2^120 * (q - z) can add up to more than binary32 holds
+    holds = np.abs(ref) + bound < 2.0**127
+    assert holds.mean() > 0.25
+    within(torch.where(torch.from_numpy(holds).to(DEV), y, 0.0), np.where(holds, ref, 0.0), bound,
+           f"{rows, group, weight, activation}")
 
 
 @pytest.mark.parametrize("renorm", [True, False])
