@@ -426,8 +426,11 @@ dg_status dg_w4_linear(int64_t rows, int64_t in_features, int64_t out_features, 
 /* ------------------------------------------------------------------------
  * Routed experts for few tokens: the router, and the SwiGLU experts' products.
  *
- * dg_moe_route.  logits[t, e] = sum_c x[t, c] * w_router[e, c], summed without
- * rounding and rounded once to binary32.  Each token takes its k experts with
+ * dg_moe_route.  logits[t, e] = sum_c x[t, c] * w_router[e, c], summed in two
+ * binary32 words (about 48 bits) and rounded once to binary32.  That is the number
+ * nearest to the sum, unless the sum lies within (d / 64 + 8)^2 * 2^-48 of
+ * sum |x w| of the middle between two.  (Products below 2^-134 lose bits; a partial
+ * sum beyond binary32's range makes the logit infinite or NaN.)  Each token takes its k experts with
  * the largest logits, in falling order; among equal logits the lower index
  * comes first, and a NaN ranks behind every number, so idx always holds k
  * distinct experts.  Gates (binary32):

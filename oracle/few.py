@@ -74,7 +74,7 @@ def w4_linear(x: np.ndarray, w: np.ndarray, bias: np.ndarray | None = None) -> n
 
 
 def moe_logits(x: np.ndarray, w_router: np.ndarray) -> np.ndarray:
-    """Router logits: the exact sums rounded once to binary32 (held in binary64)."""
+    """Router logits: binary64 sums rounded once to binary32 (held in binary64)."""
     return (x @ w_router.T).astype(np.float32).astype(np.float64)
 
 
