@@ -55,14 +55,6 @@ def _launch(fn, index: int, *args) -> None:
         check(status)
 
 
-def _capturing(index: int) -> bool:
-    """Whether device `index`'s current stream is being captured."""
-    if _current_device() == index:
-        return _is_capturing()
-    with torch.cuda.device(index):
-        return _is_capturing()
-
-
 def _size(t, dim: int) -> int:
     """Size of a dimension; 0 for what has no such dimension, which the check of its shape then refuses."""
     return t.shape[dim] if isinstance(t, torch.Tensor) and -t.dim() <= dim < t.dim() else 0
@@ -76,16 +68,16 @@ _scratch_cache: dict = {}
 _KEEP_BYTES = 64 << 20
 
 
-def _scratch(index: int, nbytes: int) -> torch.Tensor:
+def _scratch(index: int, stream: int, nbytes: int) -> torch.Tensor:
     """The workspace this module gives calls that bring none: one per (device,
     current stream), grown as needed, its error block zeroed when it is made.
     A captured call gets one of its own, in the graph's memory, so that graphs
     captured on one stream do not share it; a call that needs more than
     _KEEP_BYTES gets one that goes back to torch after it (calls of that size take
-    far longer than to zero an error block)."""
-    if nbytes > _KEEP_BYTES or _capturing(index):
+    far longer than to zero an error block).  Device `index` is current."""
+    if nbytes > _KEEP_BYTES or _is_capturing():
         return alloc_workspace(nbytes, torch.device("cuda", index))
-    key = (index, _raw_stream(index))
+    key = (index, stream)
     ws = _scratch_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _scratch_cache[key] = alloc_workspace(nbytes, torch.device("cuda", index))
@@ -108,10 +100,17 @@ def _launch_with(workspace, nbytes: int, fn, index: int, *args) -> None:
     if workspace is not None:
         _need_workspace(workspace, nbytes, index)
         _launch(fn, index, *args, workspace.data_ptr(), workspace.numel())
-    else:
-        with _scratch_lock:
-            workspace = _scratch(index, nbytes)
-            _launch(fn, index, *args, workspace.data_ptr(), workspace.numel())
+        return
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            _launch_with(None, nbytes, fn, index, *args)
+        return
+    stream = _raw_stream(index)
+    with _scratch_lock:
+        workspace = _scratch(index, stream, nbytes)
+        status = fn(*args, workspace.data_ptr(), workspace.numel(), stream)
+    if status:
+        check(status)
 
 
 # ------------------------------------------------------------------ 4-bit weights

@@ -77,7 +77,7 @@ def one_stream(monkeypatch, lib):  # noqa: F811
     monkeypatch.setattr(few, "load", lambda: slow)
     monkeypatch.setattr(few, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(few, "_current_device", lambda: 0)
-    monkeypatch.setattr(few, "_capturing", lambda index: False)
+    monkeypatch.setattr(few, "_is_capturing", lambda: False)
     monkeypatch.setattr(few, "alloc_workspace", lambda n, device: torch.zeros(n, dtype=U8))
     monkeypatch.setattr(few, "_scratch_cache", {})
     return slow
