@@ -200,7 +200,8 @@ dg_status dg_moe_route(int64_t T, int64_t d, int32_t E, int32_t k, uint32_t flag
   if (T < 0 || d < 1 || E < 1) return fail(DG_ERR_INVALID_ARGUMENT, "moe_route: T must be >= 0, d and E >= 1");
   if (d % 8) return fail(DG_ERR_INVALID_ARGUMENT, "moe_route: d must be a multiple of 8");
   if (k < 1 || k > E) return fail(DG_ERR_INVALID_ARGUMENT, "moe_route: k must be between 1 and E");
-  if (flags & ~(DG_MOE_SIGMOID | DG_MOE_RENORM)) return fail(DG_ERR_INVALID_ARGUMENT, "moe_route: unknown flags %u", flags);
+  if (flags & ~(DG_MOE_SIGMOID | DG_MOE_RENORM))
+    return fail(DG_ERR_INVALID_ARGUMENT, "moe_route: unknown flags %u", flags);
   if (E > moe_max_experts() || k > moe_max_topk())
     return fail(DG_ERR_UNSUPPORTED, "moe_route: more than %d experts or %d choices per token", moe_max_experts(),
                 moe_max_topk());

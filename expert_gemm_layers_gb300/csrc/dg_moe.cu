@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kTopkWarps * 32)
     // A sigmoid is e^l / (1 + e^l), renormalised times e^-top where all are below 0: gates that
     // are in proportion to each other do not all vanish where 1 / (1 + e^-l) would.
     const float shift = renorm ? fminf(top, 0.0f) : 0.0f;
-    p = !sigmoid ? expf(mine - top) : mine > 0.0f ? 1.0f / (1.0f + expf(-mine)) : expf(mine - shift) / (1.0f + expf(mine));
+    if (!sigmoid) p = expf(mine - top);
+    else if (mine > 0.0f) p = 1.0f / (1.0f + expf(-mine));
+    else p = expf(mine - shift) / (1.0f + expf(mine));
   }
   float sum = renorm ? p : all;
 #pragma unroll
@@ -467,9 +469,8 @@ __device__ __forceinline__ void store_block(const ProductArgs& a, const int* pai
       const int64_t p = pairs[c];
       if (UP) {
         const int f = b * 16 + r;
-        const float u = acc[0][n][i], v = acc[1][n][i];
-        if (f < a.F)
-          reinterpret_cast<__nv_bfloat16*>(a.out + p * a.out_stride)[f] = __float2bfloat16_rn(u / (1.0f + expf(-u)) * v);
+        const float u = acc[0][n][i], v = acc[1][n][i], h = u / (1.0f + expf(-u)) * v;
+        if (f < a.F) reinterpret_cast<__nv_bfloat16*>(a.out + p * a.out_stride)[f] = __float2bfloat16_rn(h);
       } else {
         const float gate = a.gates[p];
 #pragma unroll
@@ -657,10 +658,12 @@ cudaError_t launch_product(ProductArgs a, const DeviceInfo& dev, cudaStream_t s)
   const int entries = a.npairs < a.E ? a.npairs : a.E;  // active experts, at most
   constexpr bool W4 = FMT != kFmtBf16;
   const int steps = W4 ? w4_steps(K) : (K + kBfStep - 1) / kBfStep;
-  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX, LOCAL>(), W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
+  a.WK = rowdot_split(blocks, entries, steps, moe_ctas<FMT, NTMAX, LOCAL>(),
+                      W4 ? w4_most_split<NTMAX>() : kMoeWarps / NTMAX, dev.num_sms);
   int smem;
   if constexpr (W4)
-    smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) + (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT, true)) : 0);
+    smem = moe_w4_ring<FMT, NTMAX>(a.WK) + joins_bytes<NTMAX>(a.WK) +
+           (LOCAL ? static_cast<int>(w4_staged_bytes(a.cap, K, FMT, true)) : 0);
   else smem = bf_smem<NTMAX>(a.WK);
   auto kern = moe_product_kernel<FMT, NTMAX, UP, LOCAL>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), 160 * 1024, dev.device);
@@ -751,7 +754,8 @@ cudaError_t moe_launches(const MoeCall& c, const DeviceInfo& dev, cudaStream_t s
   Staged staged_x{}, staged_h{};
   if constexpr (W4) {
     staged_x = w4_staged_at(base + sc.x, c.T, c.d, FMT);
-    staged_h = Staged{base + sc.h, reinterpret_cast<float*>(base + sc.hsums), reinterpret_cast<float*>(base + sc.hfactor)};
+    staged_h = Staged{base + sc.h, reinterpret_cast<float*>(base + sc.hsums),
+                      reinterpret_cast<float*>(base + sc.hfactor)};
   }
   cudaError_t e;
   if (!local) {

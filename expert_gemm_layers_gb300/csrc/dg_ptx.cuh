@@ -290,7 +290,7 @@ static __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// All threads of both CTAs of the cluster.
+// 16 bytes of a cluster CTA's shared memory, by their shared::cluster address.
 static __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -299,6 +299,7 @@ static __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t cluster_addr)
                : "memory");
   return v;
 }
+// All threads of all CTAs of the cluster.
 static __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }

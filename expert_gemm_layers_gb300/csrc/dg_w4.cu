@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(256)
 // (4.6); 40 x 1280 -> 15360, groups of 32, 18.7 us (1.8); 64 x 4096 -> 14336, 52 us (4.9,
 // and 12 by mma.sync's own rate).
 // y = x W^T (+ bias): a CTA takes 8 / WK blocks of 32 weight rows and up to 8*NT
-// activation rows, or (gridDim.z > 1) its cluster does.  LOCAL: it stages those itself, in shared memory; else `in` has
-// them.
+// activation rows, or (gridDim.z > 1) its cluster does.  LOCAL: it stages those itself,
+// in shared memory; else `in` has them.
 template <int GROUP, int NT, bool LOCAL>
 __global__ void __launch_bounds__(kRowWarps * 32, LOCAL ? 3 : 2)
     w4_linear_kernel(const __nv_bfloat16* __restrict__ x, Staged in, const uint8_t* __restrict__ codes,
@@ -247,8 +247,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, LOCAL ? 3 : 2)
   if (r0 < N) stream.start();
   if constexpr (LOCAL) {
     in = w4_staged_at(joins + joins_bytes<NT>(WK), count, K, GROUP);
-    w4_stage_local<GROUP>(in, count, K,
-                          [&](int i) { return reinterpret_cast<const uint8_t*>(x + static_cast<int64_t>(n0 + i) * K); });
+    w4_stage_local<GROUP>(in, count, K, [&](int i) {
+      return reinterpret_cast<const uint8_t*>(x + static_cast<int64_t>(n0 + i) * K);
+    });
   } else {
     in.frag += n0 * w4_row_bytes(K);
     in.sums += static_cast<int64_t>(n0) * w4_row_sums(K, GROUP);

@@ -159,8 +159,8 @@ static __device__ __forceinline__ void w4_stage_steps(const Staged& out, int cou
   for (int i0 = 16 * block; i0 < total; i0 += 16 * blocks) {
     const int i = i0 + hw, r = count == 1 ? 0 : i / steps, st = i - r * steps, k = st * kW4Step + 8 * p;
     const bool exists = i < total;
-    const uint4 v =
-        exists && k < K ? *reinterpret_cast<const uint4*>(row(r) + 2 * static_cast<int64_t>(k)) : make_uint4(0u, 0u, 0u, 0u);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (exists && k < K) v = *reinterpret_cast<const uint4*>(row(r) + 2 * static_cast<int64_t>(k));
     uint32_t top = w4_top(v);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
