@@ -454,7 +454,9 @@ struct ProductArgs {
 // A warp's sums to memory.
 //   UP    its two row tiles are 16 rows of w1 and the same 16 of w3, so a and b of one
 //         (pair, f) meet in one thread: h[pair, f] = bf16(silu(a) * b).  h is rounded
-//         to bf16 once: it is the next product's matrix operand.
+//         to bf16 once: it is the next product's matrix operand.  (In 4 bits, where the
+//         operand is scaled fp16, too: the scratch stays 2 bytes a value and the hidden
+//         rows are those of the bf16 form, off by 2^-8 of each at most, beside weights of 4 bits.)
 //   else  32 rows of w2: part[pair, r] = gate * (w2[e, r] . h[pair])
 template <int NT, bool UP>
 __device__ __forceinline__ void store_block(const ProductArgs& a, const int* pairs, int count, int b,
@@ -561,8 +563,11 @@ constexpr int moe_ctas() {
 // an SM take the room of this one's (1 to 2% more time).
 // GPU time of a whole call and its floor by the touched experts' bytes, 3 x 4096 x 1792
 // an expert: bf16, 1 token on 8 experts 67 to 71 us (52), 128 tokens on 64 experts 468 to
-// 504 us (416); groups of 128, 1 token 38 us (13).  3 x 1288 x 1400, 77 tokens on 60
-// experts: 143 us (96); 3 x 2048 x 768 in groups of 64, 48 tokens on 128: 101 us (47).
+// 505 us (416); groups of 128, 1 token 38 us (13), 128 tokens 332 us (107).  bf16,
+// 3 x 1288 x 1400, 77 tokens on 60 experts: 143 to 147 us (96).  4 bits, 3 x 2048 x 768 in
+// groups of 64, 48 tokens on 128: 101 us (47); 3 x 2048 x 2048, 128 tokens, 4 of 32 experts:
+// groups of 128 135 us (31), of 32 182 us (35).  From 9 tokens an expert the 4-bit form is
+// bound by its instructions, at 16 warps an SM.
 template <int FMT, int NTMAX, bool UP, bool LOCAL>
 __global__ void __launch_bounds__(kMoeThreads, moe_ctas<FMT, NTMAX, LOCAL>())
     moe_product_kernel(const __grid_constant__ ProductArgs a, const uint32_t* err) {

@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t codes_of(const uint4& v, float inv, float z)
 // groups of 128: 55 us, 5.4 TB/s, 0.79 of the measured copy rate.  What keeps it from
 // that is arithmetic (76% of the issue slots of the busiest pipe): a division a weight
 // and one piece at a time took 178 us, codes_of and four pieces 60, scales by four
-// lanes 55.
+// lanes 55.  With zero points 76 us, 3.9 TB/s: the smallest and the largest of a group are
+// two reductions more, 32-bit ones where a magnitude's is two 16-bit values at a time.
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256)
     w4_quantize_kernel(const uint4* __restrict__ w, uint32_t* __restrict__ codes, __nv_bfloat16* __restrict__ scales,
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(256)
 
 // A piece a thread at a time: 4 bytes of codes in, 16 bytes of bf16 out, each value
 // rounded once from the exact binary32 product.  Bound by its writes: 28672 x 4096,
-// groups of 128: 43 us, 6.9 TB/s.  (16 columns a thread, written as two pieces of a
+// groups of 128: 43 to 46 us, 6.9 to 6.4 TB/s.  (16 columns a thread, written as two pieces of a
 // 32-byte stride, took 55 us: every line was written twice by halves.)
 template <int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(256)
@@ -218,9 +219,10 @@ __global__ void __launch_bounds__(256)
 // Bound by the latency of a warp's instructions more than by bytes: a step is some 250
 // of them on 32 rows, and what these shapes allow is 16 to 24 warps an SM.  GPU time,
 // floor by the codes' bytes: 1 x 4096 -> 6144, groups of 128, 9.0 us (1.9; an empty
-// kernel is seen to take 4.7); 1 x 4096 -> 28672, 18 us (8.9); 8 x 14336 -> 4096, 14 us
-// (4.6); 40 x 1280 -> 15360, groups of 32, 18.7 us (1.8); 64 x 4096 -> 14336, 52 us (4.9,
-// and 12 by mma.sync's own rate).
+// kernel is seen to take 4.7); 1 x 4096 -> 28672, 18.4 us (8.9); 8 x 14336 -> 4096, 14.2 us
+// (4.6); 40 x 1280 -> 15360, groups of 32, 18.6 us (1.8); 64 x 4096 -> 14336, 51 us (4.9,
+// and 12 by mma.sync's own rate).  Those are with codes in the L2; from HBM 10.2, 18.9,
+// 15.6, 19.2 and 51 us.
 // y = x W^T (+ bias): a CTA takes 8 / WK blocks of 32 weight rows and up to 8*NT
 // activation rows, or (gridDim.z > 1) its cluster does.  LOCAL: it stages those itself,
 // in shared memory; else `in` has them.
@@ -293,9 +295,9 @@ struct W4Weight {
 };
 
 // Narrow weights on long rows: the CTAs of a cluster take slices of K too.  16 rows,
-// K = 14336, N = 4096: 22.9 us with up to 8 CTAs, 24.6 with up to 4, 65 with none.  With a
-// join counted as less than 4 steps, 64 rows of K = 4096, N = 14336 would be split further
-// and take 58 us, not 54; as 8 steps, 16 rows of it less far: 23.2 us, not 21.0.
+// K = 14336, N = 4096: 23.1 us with up to 8 CTAs, 25.2 with up to 4, 67 with none.  With a
+// join counted as 2 steps, 64 rows of K = 4096, N = 14336 would be split further and take
+// 60 us, not 51; as 8 steps, 16 rows of it less far: 23.6 us, not 21.7.
 constexpr int kClusterMost = 8, kJoinSteps = 4;
 
 template <int GROUP, int NT, bool LOCAL>

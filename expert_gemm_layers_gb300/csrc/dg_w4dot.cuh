@@ -219,7 +219,7 @@ struct W4Cols {
 // word a lane all spread over the banks.
 template <int NT>
 constexpr int w4_ring() {
-  return NT > 2 ? 2 : 3;  // two CTAs an SM (40 x 1280 -> 15360 with 3 for NT = 3: 20.6 us, not 18.1)
+  return NT > 2 ? 2 : 3;  // two CTAs an SM (40 x 1280 -> 15360 with 3 for NT = 3: 21.9 us, not 18.6)
 }
 constexpr int kW4StepBytes = kLaneRows * 512;
 // Behind the codes: {-zero point, scale} of the warp's 32 rows, [G][32], two steps.
@@ -315,7 +315,7 @@ static __device__ __forceinline__ void w4_use(const uint8_t* slot, const uint8_t
           for (int n = 0; n < NT; ++n)
             if constexpr (NT > 2 && W == 4) {
               // in order: the compiler would bring four words' fragments forward and
-              // spill (64 rows, K = 4096, N = 14336: 48 us this way, 59 us that)
+              // spill (64 rows, K = 4096, N = 14336: 51 us this way, 66 us that)
               asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(b[n].x), "=r"(b[n].y), "=r"(b[n].z), "=r"(b[n].w)
                            : "r"(smem_u32(xstep) + ((q * W + j) * NT + n) * 512 + lane * 16));
