@@ -80,7 +80,7 @@ static __device__ __forceinline__ int w4_exponent(uint32_t top) { return max(sta
 // the activations, are multiplied by beside kW4Unit.  It goes to the weights' scales
 // before their product with a sum.  The unit is so small that results down to the
 // smallest bf16 numbers are held on the way (with 2^24, results below 2^-117 were not),
-// and no smaller, so that a scale below 32 times the factor of the largest bf16 number is finite.
+// and no smaller, so that a scale below 32 is finite beside the largest factor, 2^123.
 constexpr float kW4Unit = 16384.0f;
 static __device__ __forceinline__ float w4_factor(int E) { return __int_as_float((127 - 4 + E) << 23); }
 

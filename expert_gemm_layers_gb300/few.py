@@ -265,12 +265,13 @@ def moe_swiglu_w4(x: torch.Tensor, idx: torch.Tensor, gates: torch.Tensor, w13, 
 def moe_layer(x: torch.Tensor, w_router: torch.Tensor, w13, w2, top_k: int, score: str = "softmax",
               renormalize: bool = True, scale: float = 1.0, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """A whole routed layer for few tokens: moe_route, then moe_swiglu (bf16 w13, w2) or moe_swiglu_w4
-    (w13, w2 as (codes, scales, zeros)).  `workspace` is the experts' (the router takes this stream's own).
+    (w13, w2 as (codes, scales, zeros)).  T * top_k <= 8192, as theirs: split a longer prompt by tokens.
+    `workspace` is the experts' (the router takes this stream's own).
 
     Unlike the other *_layer functions it is not differentiable: tensors that require gradients are
     refused where autograd records (run it under torch.no_grad())."""
     if torch.is_grad_enabled():
-        weights = (w13, w2) if isinstance(w13, torch.Tensor) else (*w13, *w2)
+        weights = [t for w in (w13, w2) for t in (w if isinstance(w, (tuple, list)) else (w,))]
         if any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, w_router, *weights)):
             raise RuntimeError("moe_layer has no backward: run it under torch.no_grad(), or detach its inputs")
     idx, gates = moe_route(x, w_router, top_k, score, renormalize, scale)
