@@ -16,6 +16,12 @@ TMA/mbarrier pipelines):
                 moe_swiglu on bf16 or moe_swiglu_w4 on 4-bit weights; forward)
 * w4_linear     a linear on 4-bit weights with group scales for few rows, and
                 the quantiser (w4_quantize, w4_dequantize; forward)
+* fp8_linear    a linear on block-scaled e4m3 (power-of-two scales) from one row
+                to whole prompts, its gradients from 8-bit activations, and the
+                quantiser (fp8_quantize, fp8_dequantize; fp8_linear_layer)
+* rms_norm      the root-mean-square norm with the residual's addition, its
+                result in bf16 or block-scaled e4m3 (forward, backward,
+                autograd; fp8_norm_linear_layer joins it with the linear)
 
 The library is loaded lazily on first use and fails loudly if it is missing.
 """
@@ -26,6 +32,8 @@ from .ops import (A2AFFN, DG_FFN_COMP_ONLY, DG_FFN_FUSED_GATE, DG_FFN_SEPARATE_G
                   ffn_shape, gemm_fp8, tp_swiglu, tp_linear, tp_linear_backward, tp_linear_layer, TPLinear,
                   tp_swiglu_backward, tp_swiglu_layer, trace_begin, trace_end)
 from .few import moe_layer, moe_route, moe_swiglu, moe_swiglu_w4, w4_dequantize, w4_linear, w4_quantize
+from .fp8 import (FP8Linear, FP8NormLinear, RMSNorm, fp8_dequantize, fp8_linear, fp8_linear_backward, fp8_linear_layer,
+                  fp8_norm_linear_layer, fp8_quantize, rms_norm, rms_norm_backward, rms_norm_layer)
 
 __all__ = [
     "A2AFFN", "DG_FFN_COMP_ONLY", "DG_FFN_FUSED_GATE", "DG_FFN_SEPARATE_GATE", "FFN_PARAM_NAMES", "a2a_combine",
@@ -34,5 +42,7 @@ __all__ = [
     "alloc_workspace", "debug_wait_timeout", "device_status", "error_block", "ffn_shape", "gemm_fp8", "tp_swiglu",
     "tp_swiglu_backward", "TPSwiGLU", "tp_swiglu_layer", "tp_linear", "tp_linear_backward", "TPLinear",
     "tp_linear_layer", "trace_begin", "trace_end", "moe_layer", "moe_route", "moe_swiglu", "moe_swiglu_w4",
-    "w4_dequantize", "w4_linear", "w4_quantize",
+    "w4_dequantize", "w4_linear", "w4_quantize", "FP8Linear", "FP8NormLinear", "RMSNorm", "fp8_dequantize", "fp8_linear",
+    "fp8_linear_backward", "fp8_linear_layer", "fp8_norm_linear_layer", "fp8_quantize", "rms_norm", "rms_norm_backward",
+    "rms_norm_layer",
 ]

@@ -91,6 +91,15 @@ SIGNATURES = {
     "dg_moe_swiglu_workspace_bytes": (_sz, [_PMOE, _i32]),
     "dg_moe_swiglu": (ctypes.c_int, [_PMOE] + [_vp] * 7 + [_sz, _vp]),
     "dg_moe_swiglu_w4": (ctypes.c_int, [_PMOE, _i32] + [_vp] * 11 + [_sz, _vp]),
+    "dg_fp8_quantize": (ctypes.c_int, [_i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "dg_fp8_dequantize": (ctypes.c_int, [_i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "dg_fp8_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dg_fp8_linear": (ctypes.c_int, [_i64, _i64, _i64] + [_vp] * 7 + [_sz, _vp]),
+    "dg_fp8_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dg_fp8_linear_bwd": (ctypes.c_int, [_i64, _i64, _i64] + [_vp] * 9 + [_sz, _vp]),
+    "dg_rms_norm": (ctypes.c_int, [_i64, _i64, _f32] + [_vp] * 8),
+    "dg_rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "dg_rms_norm_bwd": (ctypes.c_int, [_i64, _i64, _f32] + [_vp] * 7 + [_sz, _vp]),
     "dg_trace_begin": (ctypes.c_int, []),
     "dg_trace_begin_only": (ctypes.c_int, [ctypes.c_char_p]),
     "dg_trace_end": (ctypes.c_int32, [ctypes.POINTER(TraceEntry), ctypes.c_int32]),

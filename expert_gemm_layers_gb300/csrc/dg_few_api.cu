@@ -36,35 +36,6 @@ cudaError_t smem_limit_once(const void* kern, int bytes, int dev) {
 
 namespace {
 
-// A tensor of a call: its name, address and bytes, whether it may be NULL
-// (then it takes no part) and whether the call writes it.
-struct Arg {
-  const char* name;
-  const void* p;
-  size_t bytes;
-  bool optional;
-  bool written;
-};
-
-// NULL, alignment and overlap rules of all tensors of one call.
-template <int N>
-dg_status check_args(const char* what, const Arg (&a)[N]) {
-  for (const Arg& t : a) {
-    if (!t.p && !t.optional) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is NULL", what, t.name);
-    if (!aligned16(t.p)) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", what, t.name);
-  }
-  for (int i = 0; i < N; ++i)
-    for (int j = 0; j < N; ++j)
-      if (i != j && a[i].written && overlaps(a[i].p, a[i].bytes, a[j].p, a[j].bytes))
-        return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s", what, a[i].name, a[j].name);
-  return DG_OK;
-}
-
-dg_status launched(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return DG_OK;
-  return fail(DG_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
 constexpr int64_t kMaxDim = 0x7fffffff;
 constexpr int64_t kMaxW4Rows = int64_t(1) << 31;
 constexpr int64_t kMaxW4LinearRows = 65535 * 32;

@@ -1,0 +1,547 @@
+// Row kernels of the block-scaled e4m3 format (include/dg.h): the quantiser and its
+// inverse, and the root-mean-square norm (forward, in bf16 or in the format; backward).
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "dg_internal.h"
+
+namespace dg {
+
+namespace {
+
+constexpr uint32_t kScaleNan = 0xffu;
+constexpr uint32_t kCodeNan4 = 0x7f7f7f7fu;  // four e4m3 NaN codes
+constexpr int kMinExp = -124;                // 2^-124 * 2^-9 = 2^-133: every value is a bf16 number
+
+// e8m0 byte of a block whose largest magnitude has the binary32 bits `a`: 127 + e with
+// the least e >= kMinExp for which amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t a) {
+  if (a == 0u) return 127u;
+  if (a >= 0x7f800000u) return kScaleNan;
+  const int e = static_cast<int>(a >> 23) - 127 - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return static_cast<uint32_t>(max(e, kMinExp) + 127);
+}
+// 2^-(byte - 127) for a byte of scale_byte that is no NaN (3..247).
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^(byte - 127) of any byte.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte == kScaleNan ? 0x7fc00000u : byte << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Eight values in binary32 -> eight codes of a block with the given scale byte.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t byte) {
+  if (byte == kScaleNan) return make_uint2(kCodeNan4, kCodeNan4);
+  const float k = scale_inverse(byte);
+  return make_uint2(e4m3x4(v[0] * k, v[1] * k, v[2] * k, v[3] * k), e4m3x4(v[4] * k, v[5] * k, v[6] * k, v[7] * k));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_bf16x2(w[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Largest magnitude of eight bf16 values as 16-bit patterns (sign bits cleared; a NaN is the largest).
+__device__ __forceinline__ uint32_t amax_bits8(const uint4& u) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+  return max(a & 0xffffu, a >> 16);
+}
+
+// Maximum over the 16 lanes that hold a block.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ quantise, blocks of 1 x 128
+
+// Half a warp takes a block of 128 columns, eight columns a lane, kQuantUnits blocks in flight.
+constexpr int kQuantUnits = 4;
+template <bool kWhole>  // whole: K is a multiple of 128, blocks lie one after another
+__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
+                                                              uint8_t* __restrict__ scale, int64_t blocks, int K, int nb) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int sub = threadIdx.x & 15;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kQuantUnits * kThreads + threadIdx.x) >> 4;
+  uint4 v[kQuantUnits];
+  int64_t at[kQuantUnits];
+  bool in[kQuantUnits];
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const int64_t b = first + i * (kThreads / 16);
+    if (kWhole) {
+      at[i] = b * 128 + 8 * sub;
+      in[i] = b < blocks;
+    } else {
+      const int64_t row = b / nb;
+      const int c = static_cast<int>(b - row * nb) * 128 + 8 * sub;
+      at[i] = row * K + c;
+      in[i] = b < blocks && c < K;
+    }
+    v[i] = in[i] ? __ldcs(reinterpret_cast<const uint4*>(x + at[i])) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantUnits; ++i) {
+    const int64_t b = first + i * (kThreads / 16);
+    const uint32_t byte = scale_byte(max16(amax_bits8(v[i])) << 16);
+    float f[8];
+    unpack8(v[i], f);
+    if (in[i]) *reinterpret_cast<uint2*>(q + at[i]) = codes8(f, byte);
+    if (sub == 0 && b < blocks) scale[b] = static_cast<uint8_t>(byte);
+  }
+}
+
+// ------------------------------------------------------------------ quantise, blocks of 128 x 128
+
+// One CTA a block: 16 lanes across its columns, 16 rows at a time, all eight reads before the maximum.
+__global__ void __launch_bounds__(kThreads) quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
+                                                               uint8_t* __restrict__ scale, int64_t rows, int K, int nb) {
+  __shared__ uint32_t part[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t tile = blockIdx.x;
+  const int64_t rb = tile / nb;
+  const int kb = static_cast<int>(tile - rb * nb);
+  const int c = kb * 128 + 8 * (threadIdx.x & 15);
+  const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
+  uint4 v[8];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + 16 * i;
+    v[i] = r < rows && c < K ? __ldcs(reinterpret_cast<const uint4*>(x + r * K + c)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, amax_bits8(v[i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w]);
+  const uint32_t byte = scale_byte(m << 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + 16 * i;
+    float f[8];
+    unpack8(v[i], f);
+    if (r < rows && c < K) *reinterpret_cast<uint2*>(q + r * K + c) = codes8(f, byte);
+  }
+  if (threadIdx.x == 0) scale[tile] = static_cast<uint8_t>(byte);
+}
+
+// ------------------------------------------------------------------ dequantise
+
+// A warp takes 256 columns of a row at a time, eight a lane (whole lines in and out), kDeqUnits of them in flight.
+constexpr int kDeqUnits = 4;
+__global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                                                           __nv_bfloat16* __restrict__ x, int64_t rows, int K, int nb,
+                                                           int row_shift, int spans) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t row = w / spans;
+  if (row >= rows) return;
+  const int c0 = static_cast<int>(w - row * spans) * (256 * kDeqUnits) + 8 * (threadIdx.x & 31);
+  const uint8_t* srow = scale + (row >> row_shift) * nb;
+  uint2 v[kDeqUnits];
+  float s[kDeqUnits];
+#pragma unroll
+  for (int i = 0; i < kDeqUnits; ++i) {
+    const int c = c0 + 256 * i;
+    v[i] = make_uint2(0u, 0u);
+    s[i] = 0.0f;
+    if (c < K) {
+      v[i] = __ldcs(reinterpret_cast<const uint2*>(q + row * K + c));
+      s[i] = scale_value(__ldg(srow + (c >> 7)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kDeqUnits; ++i) {
+    const int c = c0 + 256 * i;
+    if (c >= K) break;
+    const uint32_t u[2] = {v[i].x, v[i].y};
+    uint32_t o[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[h >> 1] >> (16 * (h & 1))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(hr));
+      o[h] = pack_bf16x2(f.x * s[i], f.y * s[i]);
+    }
+    *reinterpret_cast<uint4*>(x + row * K + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ------------------------------------------------------------------ root-mean-square norm
+
+// Sum over the `T` threads of a row (a power of two from 32 to blockDim.x); all of them get it, in one fixed order.
+template <int kSums>
+__device__ __forceinline__ void row_sum(float (&v)[kSums], int T, float (*part)[32]) {
+#pragma unroll
+  for (int k = 0; k < kSums; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (T == 32) return;
+  const int warp = threadIdx.x >> 5;
+  __syncthreads();  // the previous sums have been read
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) part[k][warp] = v[k];
+  __syncthreads();
+  const int w0 = warp & ~((T >> 5) - 1);
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) {
+    float s = 0.0f;
+    for (int w = 0; w < (T >> 5); ++w) s += part[k][w0 + w];
+    v[k] = s;
+  }
+}
+
+// A row whose squares overflow binary32 is summed as (h 2^-64)^2 instead.
+constexpr float kShrink = 5.42101086242752217e-20f;  // 2^-64
+
+struct NormArgs {
+  const __nv_bfloat16 *x, *res, *w;
+  __nv_bfloat16 *h, *y;
+  uint8_t *q, *scale;
+  int64_t rows;
+  int d, nb;
+  float eps;
+};
+
+// T threads a row, C chunks of eight columns a thread (chunk i of a thread is i * T + its number:
+// 16 lanes hold a block of 128 columns).
+template <int T, int C, bool kFp8>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(const NormArgs a) {
+  __shared__ float part[1][32];
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  const int t = threadIdx.x & (T - 1);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  const bool live = row < a.rows;
+  const int chunks = a.d / 8;
+  griddep_wait();
+  griddep_launch_dependents();
+  uint4 xv[C], rv[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    const bool in = live && c < chunks;
+    xv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.x + row * a.d) + c) : make_uint4(0u, 0u, 0u, 0u);
+    rv[i] = in && a.res ? __ldcs(reinterpret_cast<const uint4*>(a.res + row * a.d) + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float sum[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    float v[8];
+    unpack8(xv[i], v);
+    if (a.res) {
+      float r[8];
+      unpack8(rv[i], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += r[e];
+      xv[i] = pack8(v);  // the sum is a bf16 tensor, and its norm that of what is stored
+      if (live && t + i * T < chunks) reinterpret_cast<uint4*>(a.h + row * a.d)[t + i * T] = xv[i];
+      unpack8(xv[i], v);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
+  }
+  row_sum<1>(sum, T, part);
+  const float n = static_cast<float>(a.d);
+  float rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
+  float pre = 1.0f;
+  // (all rows of a CTA take the slow path together: it has barriers)
+  const bool over = !(sum[0] < __int_as_float(0x7f800000));
+  if (T == 32 ? __any_sync(0xffffffffu, over) : __syncthreads_or(over)) {
+    float s2[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float v[8];
+      unpack8(xv[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s2[0] = fmaf(v[e] * kShrink, v[e] * kShrink, s2[0]);
+    }
+    row_sum<1>(s2, T, part);
+    if (over) {
+      rstd = 1.0f / sqrtf(s2[0] / n);  // eps is far below the last bit
+      pre = kShrink;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    const bool in = live && c < chunks;
+    const uint4 wv = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+    float v[8], g[8];
+    unpack8(xv[i], v);
+    unpack8(wv, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * pre * rstd * g[e];
+    if (kFp8) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+      const uint32_t byte = scale_byte(max16(in ? m : 0u));
+      if (in) {
+        *reinterpret_cast<uint2*>(a.q + row * a.d + 8 * static_cast<int64_t>(c)) = codes8(v, byte);
+        if ((c & 15) == 0) a.scale[row * a.nb + (c >> 4)] = static_cast<uint8_t>(byte);
+      }
+    } else if (in) {
+      reinterpret_cast<uint4*>(a.y + row * a.d)[c] = pack8(v);
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const __nv_bfloat16 *h, *w, *dy, *dh;
+  __nv_bfloat16* dx;
+  float* part;  // [gridDim.x][d], or NULL
+  int64_t rows;
+  int d;
+  float eps;
+};
+
+// As rms_norm_kernel, a CTA taking every gridDim.x-th group of rows; the weight's gradient stays in
+// registers over a thread's rows and leaves as one partial sum a CTA.
+template <int T, int C>
+__global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  __shared__ float part[2][32];
+  extern __shared__ float wsum[];  // T < 256: [256 / T - 1][T * C * 8]
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  const int t = threadIdx.x & (T - 1);
+  const int sub = threadIdx.x / T;
+  const int chunks = a.d / 8;
+  const float n = static_cast<float>(a.d);
+  griddep_wait();
+  griddep_launch_dependents();
+  uint4 wv[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    wv[i] = t + i * T < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
+  float dw[C][8] = {};
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    const int64_t row = r0 + sub;
+    const bool live = row < a.rows;
+    uint4 hv[C], yv[C], pv[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = t + i * T;
+      const bool in = live && c < chunks;
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      hv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.h + row * a.d) + c) : z;
+      yv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.dy + row * a.d) + c) : z;
+      pv[i] = in && a.dh ? __ldcs(reinterpret_cast<const uint4*>(a.dh + row * a.d) + c) : z;
+    }
+    float s[2] = {0.0f, 0.0f};  // sum h^2, sum (dy w) h
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float h[8], y[8], g[8];
+      unpack8(hv[i], h);
+      unpack8(yv[i], y);
+      unpack8(wv[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[0] = fmaf(h[e], h[e], s[0]);
+        s[1] = fmaf(y[e] * g[e], h[e], s[1]);
+      }
+    }
+    row_sum<2>(s, T, part);
+    float pre = 1.0f, rstd = 1.0f / sqrtf(s[0] / n + a.eps);
+    const bool over = !(s[0] < __int_as_float(0x7f800000));
+    if (T == 32 ? __any_sync(0xffffffffu, over) : __syncthreads_or(over)) {
+      float q[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        float h[8], y[8], g[8];
+        unpack8(hv[i], h);
+        unpack8(yv[i], y);
+        unpack8(wv[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = h[e] * kShrink;
+          q[0] = fmaf(u, u, q[0]);
+          q[1] = fmaf(y[e] * g[e], u, q[1]);
+        }
+      }
+      row_sum<2>(q, T, part);
+      if (over) {
+        pre = kShrink;
+        rstd = 1.0f / sqrtf(q[0] / n);
+        s[1] = q[1];
+      }
+    }
+    // with n_h = h pre rstd (the normalised row): dx = rstd pre (dy w - n_h mean(dy w n_h)) + dh
+    const float mean = s[1] * rstd / n;
+    const float out = rstd * pre;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float h[8], y[8], g[8], p[8];
+      unpack8(hv[i], h);
+      unpack8(yv[i], y);
+      unpack8(wv[i], g);
+      unpack8(pv[i], p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float nh = h[e] * pre * rstd;
+        dw[i][e] = fmaf(y[e], nh, dw[i][e]);
+        p[e] = fmaf(out, fmaf(-nh, mean, y[e] * g[e]), p[e]);
+      }
+      if (a.dx && live && t + i * T < chunks) reinterpret_cast<uint4*>(a.dx + row * a.d)[t + i * T] = pack8(p);
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
+  if (kRows > 1) {
+    if (sub > 0)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wsum[((sub - 1) * T * C + i * T + t) * 8 + e] = dw[i][e];
+    __syncthreads();
+    if (sub > 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = t + i * T;
+    if (c >= chunks) continue;
+#pragma unroll
+    for (int k = 0; k < kRows - 1; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[i][e] += wsum[(k * T * C + c) * 8 + e];
+    float4* o = reinterpret_cast<float4*>(out + 8 * c);
+    o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+    o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+  }
+}
+
+// d_weight[c] = sum over `parts` partial sums, in order: 32 columns a CTA, 8 warps over the partials.
+__global__ void __launch_bounds__(kThreads) norm_weight_grad_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
+                                                                    int parts, int d) {
+  __shared__ float s[kThreads / 32][32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.0f;
+  if (c < d)
+    for (int k = warp; k < parts; k += kThreads / 32) v += part[static_cast<int64_t>(k) * d + c];
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    float r = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) r += s[k][lane];
+    out[c] = __float2bfloat16_rn(r);
+  }
+}
+
+template <int T, int C, bool kFp8>
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  return launch_pdl(rms_norm_kernel<T, C, kFp8>, dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)),
+                    dim3(T < 256 ? 256 : T), 0, s, a);
+}
+
+template <bool kFp8>
+cudaError_t norm_launch_d(const NormArgs& a, cudaStream_t s) {
+  if (a.d <= 256) return norm_launch<32, 1, kFp8>(a, s);
+  if (a.d <= 1024) return norm_launch<128, 1, kFp8>(a, s);
+  if (a.d <= 2048) return norm_launch<256, 1, kFp8>(a, s);
+  if (a.d <= 4096) return norm_launch<256, 2, kFp8>(a, s);
+  if (a.d <= 8192) return norm_launch<512, 2, kFp8>(a, s);
+  if (a.d <= 16384) return norm_launch<1024, 2, kFp8>(a, s);
+  return norm_launch<1024, 4, kFp8>(a, s);
+}
+
+template <int T, int C>
+cudaError_t norm_bwd_launch(const NormBwdArgs& a, int grid, cudaStream_t s) {
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  return launch_pdl(rms_norm_bwd_kernel<T, C>, dim3(grid), dim3(T < 256 ? 256 : T),
+                    sizeof(float) * (kRows - 1) * T * C * 8, s, a);
+}
+
+int norm_threads(int d) { return d <= 256 ? 32 : d <= 1024 ? 128 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
+                                cudaStream_t s) {
+  const int nb = (K + 127) / 128;
+  auto* xp = static_cast<const __nv_bfloat16*>(x);
+  auto* q = static_cast<uint8_t*>(codes);
+  auto* sc = static_cast<uint8_t*>(scales);
+  if (block_rows == 1) {
+    const int64_t blocks = rows * nb, per = kThreads / 16 * kQuantUnits;
+    const dim3 grid(static_cast<unsigned>((blocks + per - 1) / per));
+    return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb)
+                        : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb);
+  }
+  const int64_t tiles = (rows + 127) / 128 * nb;
+  return launch_pdl(quant_tiles_kernel, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, s, xp, q, sc, rows, K, nb);
+}
+
+cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
+                                  cudaStream_t s) {
+  const int nb = (K + 127) / 128, spans = (K + 256 * kDeqUnits - 1) / (256 * kDeqUnits);
+  const int64_t warps = rows * spans;
+  return launch_pdl(dequant_kernel, dim3(static_cast<unsigned>((warps * 32 + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+                    static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), static_cast<__nv_bfloat16*>(x),
+                    rows, K, nb, block_rows == 1 ? 0 : 7, spans);
+}
+
+cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
+                            int64_t rows, int d, float eps, cudaStream_t s) {
+  const NormArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res),
+                   static_cast<const __nv_bfloat16*>(w), static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(y),
+                   static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, d, (d + 127) / 128, eps};
+  return codes ? norm_launch_d<true>(a, s) : norm_launch_d<false>(a, s);
+}
+
+int rms_norm_bwd_parts(int64_t rows, int d) {
+  const int T = norm_threads(d);
+  const int64_t groups = T < 256 ? (rows + 256 / T - 1) / (256 / T) : rows;
+  const int64_t most = 152 * (T <= 256 ? 3 : T == 512 ? 2 : 1);
+  return static_cast<int>(groups < most ? groups : most);
+}
+
+cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, const void* dh, void* dx, void* d_weight,
+                                float* part, int64_t rows, int d, float eps, cudaStream_t s) {
+  const NormBwdArgs a{static_cast<const __nv_bfloat16*>(h),  static_cast<const __nv_bfloat16*>(w),
+                      static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dh),
+                      static_cast<__nv_bfloat16*>(dx),       d_weight ? part : nullptr, rows, d, eps};
+  const int parts = rms_norm_bwd_parts(rows, d);
+  cudaError_t e = d <= 256    ? norm_bwd_launch<32, 1>(a, parts, s)
+                  : d <= 1024 ? norm_bwd_launch<128, 1>(a, parts, s)
+                  : d <= 2048 ? norm_bwd_launch<256, 1>(a, parts, s)
+                  : d <= 4096 ? norm_bwd_launch<256, 2>(a, parts, s)
+                  : d <= 8192 ? norm_bwd_launch<512, 2>(a, parts, s)
+                  : d <= 16384 ? norm_bwd_launch<1024, 2>(a, parts, s)
+                               : norm_bwd_launch<1024, 4>(a, parts, s);
+  if (e != cudaSuccess || !d_weight) return e;
+  return launch_pdl(norm_weight_grad_kernel, dim3((d + 31) / 32), dim3(kThreads), 0, s, static_cast<const float*>(part),
+                    static_cast<__nv_bfloat16*>(d_weight), parts, d);
+}
+
+}  // namespace dg

@@ -26,6 +26,35 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// A tensor of a call: its name, address and bytes, whether it may be NULL
+// (then it takes no part) and whether the call writes it.
+struct Arg {
+  const char* name;
+  const void* p;
+  size_t bytes;
+  bool optional;
+  bool written;
+};
+
+// NULL, alignment and overlap rules of all tensors of one call.
+template <int N>
+dg_status check_args(const char* what, const Arg (&a)[N]) {
+  for (const Arg& t : a) {
+    if (!t.p && !t.optional) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is NULL", what, t.name);
+    if (!aligned16(t.p)) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", what, t.name);
+  }
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < N; ++j)
+      if (i != j && a[i].written && overlaps(a[i].p, a[i].bytes, a[j].p, a[j].bytes))
+        return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s", what, a[i].name, a[j].name);
+  return DG_OK;
+}
+
+inline dg_status launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return DG_OK;
+  return fail(DG_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
 // Per-device facts, cached on first use of each device.  `err` is the
 // error word the kernels of one call record a failed wait in: each entry point
 // points it at the error block of its caller's workspace (device_info leaves
@@ -369,6 +398,29 @@ cudaError_t launch_debug_wait(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 // Sets a kernel's dynamic shared-memory limit the first time it is launched on
 // a device (`dev` current); later calls only look it up.
 cudaError_t smem_limit_once(const void* kern, int bytes, int dev);
+
+// ---------------------------------------------------------------- block-scaled e4m3 (dg_fp8_rows.cu, dg_mx_gemm.cu)
+
+// x [rows, K] bf16 <-> codes [rows, K] and scales [ceil(rows / block_rows), ceil(K / 128)]; block_rows 1 or 128.
+cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
+                                cudaStream_t s);
+cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
+                                  cudaStream_t s);
+
+// h = x + res (res NULL: h is x and not written); the norm of h into y, or into codes and scales where codes is given.
+cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
+                            int64_t rows, int d, float eps, cudaStream_t s);
+// part [rms_norm_bwd_parts][d] binary32; d_weight, dx and dh may be NULL.
+int rms_norm_bwd_parts(int64_t rows, int d);
+cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, const void* dh, void* dx, void* d_weight,
+                                float* part, int64_t rows, int d, float eps, cudaStream_t s);
+
+// One launch of the block-scaled GEMM (dg_mx.cuh); p.tiles_* and p.n_fastest are filled in.  Box heights of the maps:
+// A 128 rows, a K-major B kMxTileN / 2 rows, an MN-major B 128 columns by 128 rows, D 32 columns by 32 rows.
+struct MxParams;
+constexpr int kMxTileN = 224;
+cudaError_t launch_gemm_mx(bool b_mn_major, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d,
+                           const MxParams& p, const DeviceInfo& dev, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights (dg_w4.cu)
 

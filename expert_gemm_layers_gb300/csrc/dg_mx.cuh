@@ -1,0 +1,440 @@
+// Persistent tcgen05 GEMM on e4m3 operands with power-of-two block scales
+// (sm_103a, CTA pairs): D[m, n] = bias[n] + sum_k a[m, k] b[n, k] with
+//   a = A code * 2^(sa[m, k/128] - 127),  b = B code * 2^(sb[n/128, k/128] - 127).
+//
+// The scales are applied by the tensor core itself: tcgen05.mma with
+// .kind::mxf8f6f4.block_scale reads one e8m0 byte per row and 32 values of K from
+// TMEM, so the accumulator needs no promotion in registers at block borders.  The
+// operands' blocks are 128 long, so the four K steps of a stage read the same byte;
+// a 32-bit TMEM word holds the bytes of four K blocks and the instruction
+// descriptor's scale index picks one.  Scales therefore move once every 512 K.
+//
+// Warp roles (320 threads a CTA):
+//   warp 0      TMA producer: ring of (A, B) K blocks of 128 bytes a row
+//   warp 1      MMA issuer (pair leader, one lane)
+//   warps 2-5   epilogue: TMEM -> + bias -> bf16 -> swizzled staging -> TMA store
+//   warps 6-9   scales: global bytes -> registers -> tcgen05.st into one of four
+//               TMEM buffers (every warp writes its own lane quarter: the layout
+//               wants row r's word in lane r % 32 of all quarters, column r / 32)
+// TMEM: two accumulators of BN columns, then the scale buffers; two of 224 and four
+// buffers of 16 fill the 512 columns.
+//
+// B is K-major ([N][K], the forward) or MN-major ([K][N], the input gradient, whose
+// contraction runs over the weight's rows): the weight's codes are held once.
+#pragma once
+
+#include "dg_gemm.cuh"
+
+namespace dg {
+
+struct MxParams {
+  int32_t M, N, K;
+  int32_t tiles_m, tiles_n, n_fastest;
+  const uint8_t* sa;         // [M][ka]: e8m0 bytes of A's rows
+  int32_t ka;                // K blocks = ceil(K / 128)
+  const uint8_t* sb;         // byte of column block nb and K block kb at sb[nb * sb_n + kb * sb_k]
+  int32_t sb_n, sb_k;
+  const __nv_bfloat16* bias; // [N] or NULL
+  uint32_t* err;
+};
+
+enum MxSite : uint32_t { SITE_SF_EMPTY = 8, SITE_SF_FULL = 9 };
+
+template <bool kBMN, int kBN>
+struct MxCfg {
+  static constexpr int CTAS = 2;
+  static constexpr int BM = 128;
+  static constexpr int UMMA_M = 256;
+  static constexpr int BN = kBN;
+  static constexpr int B_ROWS = BN / CTAS;
+  static constexpr int BK = 128;
+  static constexpr int K_STEPS = 4;
+  static constexpr int STAGES = 6;
+  static constexpr int A_BYTES = BM * 128;
+  // MN-major: 128 K rows of 128 bytes, of which the MMA reads B_ROWS columns
+  static constexpr int B_BYTES = kBMN ? 128 * 128 : B_ROWS * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int CHUNK = 32;                     // output columns per staging buffer
+  static constexpr int EPI_BUF_BYTES = 32 * CHUNK * 2;
+  static constexpr int EPI_BYTES = EPI_WARPS * 2 * EPI_BUF_BYTES;
+  static constexpr int SF_WARPS = 4;
+  static constexpr int SF_BUFS = 4;
+  static constexpr int SF_COLS = 16;                   // A words at +0, B words at +8
+  static constexpr int SF_BASE = 512 - SF_BUFS * SF_COLS;
+  static constexpr int NB_WORDS = BN / 32;
+  static constexpr int NB_BLOCKS = (BN + 127 + 127) / 128;  // 128-column blocks that a tile can touch
+  static constexpr int NUM_THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
+  static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * SF_BUFS + 1;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES;
+  // kind::mxf8f6f4 instruction descriptor: e4m3 x e4m3, majorness, N, e8m0 scales (bit 23),
+  // M; bits 4-5 and 29-30 (scale index of B and A) are filled in per K block
+  static constexpr uint32_t IDESC = (static_cast<uint32_t>(kBMN) << 16) | ((BN >> 3) << 17) | (1u << 23) |
+                                    ((UMMA_M >> 4) << 24);
+  static_assert(NUM_BARS * 8 + 4 <= BAR_BYTES, "barrier area");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(2 * BN <= SF_BASE && BN % 32 == 0 && NB_WORDS <= 8, "tensor memory");
+  static_assert(STAGE_BYTES % 1024 == 0 && A_BYTES % 1024 == 0, "swizzled tiles");
+  static_assert(!kBMN || B_ROWS <= 128, "one 128-byte MN block a CTA");
+};
+
+// D(tmem of both CTAs) (+)= (A x scales) (B x scales), e4m3, one e8m0 scale per 32 K.
+static __device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                      uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+static __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Thread i of the warp writes lane (base + i), columns col..col+N-1.
+static __device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+static __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+static __device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// mbar_wait by a whole warp: all lanes go on or none does.
+static __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, site));
+}
+
+constexpr uint32_t kScaleOnes = 0x7f7f7f7fu;  // four scales of 1
+
+// Bytes kb..kb+3 of a scale row (consecutive K blocks, `step` bytes apart); blocks at or past `kend` read as 1.
+static __device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int kb, int kend, int64_t step) {
+  if (step == 1 && kb + 4 <= kend && (reinterpret_cast<uintptr_t>(p + kb) & 3u) == 0)
+    return __ldg(reinterpret_cast<const uint32_t*>(p + kb));
+  uint32_t w = kScaleOnes;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (kb + i < kend) w = (w & ~(0xffu << (8 * i))) | (static_cast<uint32_t>(__ldg(p + (kb + i) * step)) << (8 * i));
+  return w;
+}
+
+template <bool kBMN, int kBN>
+__global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
+    gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmD, const MxParams p) {
+  using Cfg = MxCfg<kBMN, kBN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t s_abort;
+
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stage_base = smem_raw + pad;
+  uint8_t* epi_base = stage_base + Cfg::STAGES * Cfg::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi_base + Cfg::EPI_BYTES);
+  uint64_t* empty = full + Cfg::STAGES;
+  uint64_t* tfull = empty + Cfg::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* sf_full = tempty + 2;
+  uint64_t* sf_empty = sf_full + Cfg::SF_BUFS;
+  uint64_t* drain = sf_empty + Cfg::SF_BUFS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0u;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], Cfg::EPI_WARPS * Cfg::CTAS);
+    }
+    for (int b = 0; b < Cfg::SF_BUFS; ++b) {
+      mbar_init(&sf_full[b], Cfg::SF_WARPS * Cfg::CTAS);
+      mbar_init(&sf_empty[b], 1);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmD);
+  }
+  cluster_sync_all();
+  griddep_wait();
+
+  // a failure recorded earlier: the leader decides for the pair
+  if (threadIdx.x == 0 && leader) {
+    const uint32_t v = ld_volatile_u32(p.err);
+    st_cluster_u32(mapa_shared(smem_u32(&s_abort), 0), v);
+    st_cluster_u32(mapa_shared(smem_u32(&s_abort), 1), v);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  cluster_sync_all();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_holder;
+  const bool aborted = s_abort != 0u;
+
+  const int total_tiles = p.tiles_m * p.tiles_n;
+  const int num_kb = p.ka;
+  const int unit = static_cast<int>(blockIdx.x) / Cfg::CTAS;
+  const int num_units = static_cast<int>(gridDim.x) / Cfg::CTAS;
+  auto coords = [&](int tile, int& mt, int& nt) {
+    if (p.n_fastest) {
+      mt = tile / p.tiles_n;
+      nt = tile - mt * p.tiles_n;
+    } else {
+      nt = tile / p.tiles_m;
+      mt = tile - nt * p.tiles_m;
+    }
+  };
+
+  if (aborted) {
+    // straight to the teardown
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int tile = unit; tile < total_tiles && ok; tile += num_units) {
+        int mt, nt;
+        coords(tile, mt, nt);
+        const int m0 = mt * Cfg::UMMA_M + static_cast<int>(rank) * Cfg::BM;
+        const int n0 = nt * Cfg::BN + static_cast<int>(rank) * Cfg::B_ROWS;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, SITE_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES * Cfg::CTAS);
+          const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+          uint8_t* sa = stage_base + stage * Cfg::STAGE_BYTES;
+          tma_load_3d_pair(sa, &tmA, bar, kb * Cfg::BK, m0, 0);
+          if (kBMN)
+            tma_load_3d_pair(sa + Cfg::A_BYTES, &tmB, bar, n0, kb * Cfg::BK, 0);
+          else
+            tma_load_3d_pair(sa + Cfg::A_BYTES, &tmB, bar, kb * Cfg::BK, n0, 0);
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every load issued must land before the CTA exits
+      for (int s = 0; s < Cfg::STAGES; ++s)
+        if (leader && (armed & (1u << s)) && !mbar_try_wait(&full[s], (armed_parity >> s) & 1u)) {
+          uint32_t dummy = 0;
+          mbar_wait_slow(&full[s], (armed_parity >> s) & 1u, &dummy, SITE_DRAIN, kWaitLimitNs);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (pair leader)
+    if (lane == 0 && leader) {
+      int stage = 0, sfb = 0;
+      uint32_t phase = 0, tphase = 0, sfphase = 0;
+      bool ok = true;
+      int local = 0;
+      for (int tile = unit; tile < total_tiles && ok; tile += num_units, ++local) {
+        const int acc = local & 1;
+        if (!mbar_wait(&tempty[acc], ((tphase >> acc) & 1u) ^ 1u, p.err, SITE_TEMPTY)) break;
+        tphase ^= 1u << acc;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::BN);
+        for (int kb = 0; kb < num_kb; ++kb) {
+          const uint32_t q = static_cast<uint32_t>(kb) & 3u;
+          if (q == 0 && !mbar_wait(&sf_full[sfb], sfphase, p.err, SITE_SF_FULL)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(&full[stage], phase, p.err, SITE_FULL)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sa = smem_u32(stage_base + stage * Cfg::STAGE_BYTES);
+          const uint32_t sb = sa + Cfg::A_BYTES;
+          const uint32_t idesc = Cfg::IDESC | (q << 4) | (q << 29);
+          const uint32_t sf = tmem_base + static_cast<uint32_t>(Cfg::SF_BASE + sfb * Cfg::SF_COLS);
+#pragma unroll
+          for (int j = 0; j < Cfg::K_STEPS; ++j) {
+            // K-major: 32 bytes on in the swizzle row.  MN-major: 32 K rows of 128 bytes on;
+            // groups of 8 K rows lie 1024 bytes apart.
+            const uint64_t ad = smem_desc_sw128(sa + j * 32, 16, 1024);
+            const uint64_t bd = kBMN ? smem_desc_sw128(sb + j * 4096, 128 * 128, 1024) : smem_desc_sw128(sb + j * 32, 16, 1024);
+            umma_mxf8_pair(d_tmem, ad, bd, idesc, sf, sf + 8, (kb > 0 || j > 0) ? 1u : 0u);
+          }
+          tc_commit_pair_mc(&empty[stage], 0x3);
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (q == 3u || kb + 1 == num_kb) {
+            tc_commit_pair_mc(&sf_empty[sfb], 0x3);
+            if (++sfb == Cfg::SF_BUFS) {
+              sfb = 0;
+              sfphase ^= 1u;
+            }
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&tfull[acc], 0x3);
+      }
+      tc_commit_pair_mc(drain, 0x1);
+      if (!mbar_try_wait(drain, 0)) {
+        uint32_t dummy = 0;
+        mbar_wait_slow(drain, 0, &dummy, SITE_DRAIN, kWaitLimitNs);
+      }
+    }
+  } else if (warp < 2 + Cfg::EPI_WARPS) {
+    // ------------------------------------------------------------ epilogue
+    const int lg = warp & 3;
+    uint8_t* stg = epi_base + (warp - 2) * 2 * Cfg::EPI_BUF_BYTES;
+    uint32_t tphase = 0, ctr = 0;
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * lg) << 16);
+    int local = 0;
+    for (int tile = unit; tile < total_tiles; tile += num_units, ++local) {
+      int mt, nt;
+      coords(tile, mt, nt);
+      const int row0 = mt * Cfg::UMMA_M + static_cast<int>(rank) * Cfg::BM + 32 * lg;
+      const int n0 = nt * Cfg::BN;
+      const int acc = local & 1;
+      int nchunks = (min(p.N - n0, Cfg::BN) + Cfg::CHUNK - 1) / Cfg::CHUNK;
+      if (row0 >= p.M) nchunks = 0;
+      if (!warp_wait(&tfull[acc], (tphase >> acc) & 1u, p.err, SITE_TFULL)) break;
+      tphase ^= 1u << acc;
+      tc_fence_after_sync();
+      auto release_acc = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+      };
+      if (nchunks == 0) release_acc();
+      for (int j = 0; j < nchunks; ++j, ++ctr) {
+        const int c0 = n0 + Cfg::CHUNK * j;
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(acc * Cfg::BN + Cfg::CHUNK * j), r);
+        tmem_ld_wait();
+        tmem_regs_after_wait(r);
+        if (j + 1 == nchunks) release_acc();
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (p.bias) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (c0 + 8 * q < p.N) {
+              const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + c0 + 8 * q));
+              const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 b2 = unpack_bf16x2(bw[e]);
+                v[8 * q + 2 * e] += b2.x;
+                v[8 * q + 2 * e + 1] += b2.y;
+              }
+            }
+          }
+        }
+        uint8_t* sbuf = stg + (ctr & 1u) * Cfg::EPI_BUF_BYTES;
+        // the store that last read this buffer must be done
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(sbuf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tmD, sbuf, c0, row0, 0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ scales
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    int buf = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = unit; tile < total_tiles && ok; tile += num_units) {
+      int mt, nt;
+      coords(tile, mt, nt);
+      const int m0 = mt * Cfg::UMMA_M + static_cast<int>(rank) * Cfg::BM + lane;
+      const int n0 = nt * Cfg::BN;
+      const int nb0 = n0 >> 7;
+      for (int kb = 0; kb < num_kb; kb += 4) {
+        uint32_t a[4], blk[Cfg::NB_BLOCKS], b[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[j] = m0 + 32 * j < p.M ? scale_word(p.sa + static_cast<int64_t>(m0 + 32 * j) * p.ka, kb, num_kb, 1) : kScaleOnes;
+#pragma unroll
+        for (int j = 0; j < Cfg::NB_BLOCKS; ++j)
+          blk[j] = (nb0 + j) * 128 < p.N ? scale_word(p.sb + static_cast<int64_t>(nb0 + j) * p.sb_n, kb, num_kb, p.sb_k) : kScaleOnes;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          b[j] = kScaleOnes;
+          if (j < Cfg::NB_WORDS) {
+            const int at = ((n0 + lane + 32 * j) >> 7) - nb0;
+#pragma unroll
+            for (int i = 0; i < Cfg::NB_BLOCKS; ++i)
+              if (at == i) b[j] = blk[i];
+          }
+        }
+        if (!warp_wait(&sf_empty[buf], phase ^ 1u, p.err, SITE_SF_EMPTY)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t at = lane_addr + static_cast<uint32_t>(Cfg::SF_BASE + buf * Cfg::SF_COLS);
+        tmem_st_32x32b_x4(at, a);
+        tmem_st_32x32b_x8(at + 8, b);
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sf_full[buf]), 0));
+        if (++buf == Cfg::SF_BUFS) {
+          buf = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  griddep_launch_dependents();
+  tc_fence_before_sync();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace dg

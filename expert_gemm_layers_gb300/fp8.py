@@ -1,0 +1,293 @@
+"""Torch-facing wrappers of the block-scaled e4m3 operators: quantiser, linear, root-mean-square norm.
+
+As in ops.py, each function checks its arguments, allocates outputs and
+scratch with torch and passes pointers and the current stream to the C ABI.
+A matrix in this format is a pair (codes, scales): codes float8_e4m3fn
+[..., K], scales float8_e8m0fnu with one power of two for every 128 columns of
+a row (activations: [..., ceil(K/128)]) or every 128 x 128 block (weights
+[N, K]: [ceil(N/128), ceil(K/128)]); value = code * scale.
+
+The *_layer functions are differentiable and keep activations in 8 bits for
+the backward; in the others, inputs that require gradients are taken as
+constants.  A layer's backward can be captured into a graph with
+torch.autograd.grad; no gradient of a gradient.
+"""
+from __future__ import annotations
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from ._lib import load
+from .few import BF16, _check, _device, _launch, _launch_with, _p, _size
+
+__all__ = ["fp8_quantize", "fp8_dequantize", "fp8_linear", "fp8_linear_backward", "FP8Linear", "fp8_linear_layer",
+           "rms_norm", "rms_norm_backward", "RMSNorm", "rms_norm_layer", "FP8NormLinear", "fp8_norm_linear_layer"]
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _pair(pair, what: str):
+    if not (isinstance(pair, (tuple, list)) and len(pair) == 2):
+        raise TypeError(f"{what} must be (codes, scales)")
+    return pair
+
+
+def _need_rows(pair, what: str, index: int) -> tuple:
+    """Checks activations in 8 bits; returns (codes, scales)."""
+    codes, scales = _pair(pair, what)
+    _check(codes, what + " codes", E4M3, codes.shape if isinstance(codes, torch.Tensor) else None, index)
+    _check(scales, what + " scales", E8M0, (*codes.shape[:-1], _blocks(_size(codes, -1))), index)
+    return codes, scales
+
+
+def _need_weight(pair, what: str, in_f: int, index: int) -> tuple:
+    """Checks a weight [out, in_f] in 8 bits; returns (codes, scales)."""
+    codes, scales = _pair(pair, what)
+    out_f = _size(codes, 0)
+    _check(codes, what + " codes", E4M3, (out_f, in_f), index)
+    _check(scales, what + " scales", E8M0, (_blocks(out_f), _blocks(in_f)), index)
+    return codes, scales
+
+
+def _rows(t) -> int:
+    return t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0
+
+
+# ------------------------------------------------------------------ the format
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1):
+    """(codes, scales) of a bf16 tensor: one scale per 128 columns of a row (block_rows 1, x [..., K]) or per
+    128 x 128 block (block_rows 128, x [N, K]).  K % 16 == 0.
+
+    A scale is the least power of two (from 2^-124) for which no code exceeds 448, 1 for a block of zeros; a block
+    with a NaN or an infinity becomes NaN."""
+    index = _device(x, "x", BF16)
+    _check(x, "x", BF16, x.shape, index)
+    if block_rows not in (1, 128) or x.dim() < 1 or (block_rows == 128 and x.dim() != 2):
+        raise ValueError(f"block_rows must be 1, or 128 with x [N, K]; got {block_rows} with shape {tuple(x.shape)}")
+    K, rows = x.shape[-1], _rows(x)
+    lead = x.shape[:-1] if block_rows == 1 else (_blocks(rows),)
+    codes = torch.empty(x.shape, dtype=E4M3, device=x.device)
+    scales = torch.empty((*lead, _blocks(K)), dtype=E8M0, device=x.device)
+    _launch(load().dg_fp8_quantize, index, rows, K, block_rows, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def fp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bf16 tensor that (codes, scales) stand for.  scales [..., ceil(K/128)] is read as activations' and
+    [ceil(N/128), ceil(K/128)] beside codes [N, K] as a weight's (one row is both)."""
+    index = _device(codes, "codes", E4M3)
+    _check(codes, "codes", E4M3, codes.shape, index)
+    K, rows = _size(codes, -1), _rows(codes)
+    as_rows = (*codes.shape[:-1], _blocks(K))
+    block_rows = 1
+    if codes.dim() == 2 and isinstance(scales, torch.Tensor) and scales.shape != as_rows:
+        as_rows, block_rows = (_blocks(rows), _blocks(K)), 128
+    _check(scales, "scales", E8M0, as_rows, index)
+    if out is None:
+        out = torch.empty(codes.shape, dtype=BF16, device=codes.device)
+    else:
+        _check(out, "out", BF16, codes.shape, index)
+    _launch(load().dg_fp8_dequantize, index, rows, K, block_rows, codes.data_ptr(), scales.data_ptr(), out.data_ptr())
+    return out
+
+
+# ------------------------------------------------------------------ linear
+
+def fp8_linear(x, weight, bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x @ W^T (+ bias) in block-scaled e4m3, from one row (a decode step) to whole prompts.
+
+    x: activations in 8 bits (codes, scales), as fp8_quantize and rms_norm(..., fp8=True) return them, or bf16
+    [..., in], which is quantised on the way.  weight: (codes, scales) of fp8_quantize(W [out, in], 128).  Sums in
+    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, its error block zeroed; default:
+    this stream's own) is not shared by calls that run at the same time."""
+    if isinstance(x, torch.Tensor):
+        index = _device(x, "x", BF16)
+        x = fp8_quantize(x)
+    else:
+        index = _device(_pair(x, "x")[0], "x codes", E4M3)
+    lib, (xc, xs) = load(), _need_rows(x, "x", index)
+    in_f = _size(xc, -1)
+    wc, wscale = _need_weight(weight, "weight", in_f, index)
+    out_f, rows = _size(wc, 0), _rows(xc)
+    if bias is not None:
+        _check(bias, "bias", BF16, (out_f,), index)
+    if out is None:
+        out = torch.empty((*xc.shape[:-1], out_f), dtype=BF16, device=xc.device)
+    else:
+        _check(out, "out", BF16, (*xc.shape[:-1], out_f), index)
+    _launch_with(workspace, lib.dg_fp8_linear_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear, index, rows, in_f,
+                 out_f, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), wscale.data_ptr(), _p(bias), out.data_ptr())
+    return out
+
+
+def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_dw: bool = True,
+                        need_db: bool = False, workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of fp8_linear from the 8-bit operands that the forward read, given dy [..., out] bf16.
+
+    "x" = q(dy) W, where q(dy) is dy through fp8_quantize, "weight" = dy^T x (dy as it is), "bias" = column sums of
+    dy; bf16, None where not needed.  x or weight may be None where its product is not needed (then the other gives
+    the sizes)."""
+    lib, index = load(), _device(dy, "dy", BF16)
+    _check(dy, "dy", BF16, dy.shape, index)
+    out_f, lead, rows = _size(dy, -1), dy.shape[:-1], _rows(dy)
+    xc = xs = wc = ws = None
+    if x is None and (need_dw or weight is None) or weight is None and need_dx:
+        raise ValueError("x is needed for the weight's gradient, weight for that of x")
+    if x is not None:
+        xc, xs = _need_rows(x, "x", index)
+        if xc.shape[:-1] != lead:
+            raise ValueError(f"x codes have shape {tuple(xc.shape)} beside dy {tuple(dy.shape)}")
+    in_f = _size(xc if xc is not None else _pair(weight, "weight")[0], -1)
+    if weight is not None:
+        wc, ws = _need_weight(weight, "weight", in_f, index)
+        if wc.shape[0] != out_f:
+            raise ValueError(f"weight codes have shape {tuple(wc.shape)} beside dy {tuple(dy.shape)}")
+    new = lambda shape: torch.empty(shape, dtype=BF16, device=dy.device)
+    g = dict(x=new((*lead, in_f)) if need_dx else None, weight=new((out_f, in_f)) if need_dw else None,
+             bias=new((out_f,)) if need_db else None)
+    _launch_with(workspace, lib.dg_fp8_linear_bwd_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear_bwd, index, rows,
+                 in_f, out_f, _p(xc), _p(xs), _p(wc), _p(ws), dy.data_ptr(), _p(g["x"]), _p(g["weight"]), _p(g["bias"]))
+    return g
+
+
+class FP8Linear(torch.autograd.Function):
+    """Autograd wrapper of fp8_linear on bf16 tensors: quantises both operands and keeps them in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias):
+        x8, w8 = fp8_quantize(x), fp8_quantize(weight, 128)
+        ctx.save_for_backward(*x8, *w8)
+        return fp8_linear(x8, w8, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        xc, xs, wc, ws = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = fp8_linear_backward((xc, xs), (wc, ws), dy.contiguous(), need[0], need[1], need[2])
+        return g["x"], g["weight"], g["bias"]
+
+
+def fp8_linear_layer(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable y = x @ weight^T (+ bias): x [..., in], weight [out, in] and bias bf16, products in block-scaled
+    e4m3.  Of x the backward keeps 8 bits a value; its gradients are fp8_linear_backward's, passed through the
+    quantisers."""
+    return FP8Linear.apply(x, weight, bias)
+
+
+# ------------------------------------------------------------------ root-mean-square norm
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             fp8: bool = False):
+    """y = h / sqrt(mean(h^2) + eps) * weight over the last dimension, h = x + residual (bf16).
+
+    y is bf16, or with fp8 activations in 8 bits (codes, scales) for fp8_linear, from the binary32 values.  Returns y,
+    or (y, h) where a residual is given.  x, residual [..., d], weight [d] bf16; d % 8 == 0 (16 with fp8),
+    d <= 32768, eps >= 1e-30."""
+    index = _device(x, "x", BF16)
+    _check(x, "x", BF16, x.shape, index)
+    d = _size(x, -1)
+    _check(weight, "weight", BF16, (d,), index)
+    h = y = codes = scales = None
+    if residual is not None:
+        _check(residual, "residual", BF16, x.shape, index)
+        h = torch.empty_like(x)
+    if fp8:
+        codes = torch.empty(x.shape, dtype=E4M3, device=x.device)
+        scales = torch.empty((*x.shape[:-1], _blocks(d)), dtype=E8M0, device=x.device)
+    else:
+        y = torch.empty_like(x)
+    _launch(load().dg_rms_norm, index, _rows(x), d, eps, x.data_ptr(), _p(residual), weight.data_ptr(), _p(h), _p(y),
+            _p(codes), _p(scales))
+    y = (codes, scales) if fp8 else y
+    return y if residual is None else (y, h)
+
+
+def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dh: torch.Tensor | None = None,
+                      eps: float = 1e-6, need_dx: bool = True, need_dw: bool = True,
+                      workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of rms_norm from h (x, where there was no residual), dy and, if h had other uses, their gradient dh:
+    "x" (also the residual's) and "weight", bf16."""
+    lib, index = load(), _device(h, "h", BF16)
+    _check(h, "h", BF16, h.shape, index)
+    d, rows = _size(h, -1), _rows(h)
+    _check(weight, "weight", BF16, (d,), index)
+    _check(dy, "dy", BF16, h.shape, index)
+    if dh is not None:
+        _check(dh, "dh", BF16, h.shape, index)
+    g = dict(x=torch.empty_like(h) if need_dx else None, weight=torch.empty_like(weight) if need_dw else None)
+    _launch_with(workspace, lib.dg_rms_norm_bwd_workspace_bytes(rows, d), lib.dg_rms_norm_bwd, index, rows, d, eps,
+                 h.data_ptr(), weight.data_ptr(), dy.data_ptr(), _p(dh), _p(g["x"]), _p(g["weight"]))
+    return g
+
+
+def _norm_grads(h, weight, dy, dh, eps, need):
+    """(dx, d_weight, d_residual) of a norm for needs (x, weight, residual); dy or dh None: no gradient came that way."""
+    dy = torch.zeros_like(h) if dy is None else dy.contiguous()
+    g = rms_norm_backward(h, weight, dy, None if dh is None else dh.contiguous(), eps, need[0] or need[2], need[1])
+    return g["x"] if need[0] else None, g["weight"], g["x"] if need[2] else None
+
+
+class RMSNorm(torch.autograd.Function):
+    """Autograd wrapper of rms_norm with a bf16 result; keeps h and the weight."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        out = rms_norm(x, weight, residual, eps)
+        ctx.save_for_backward(x if residual is None else out[1], weight)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        return (*_norm_grads(*ctx.saved_tensors, dy, dh, ctx.eps, ctx.needs_input_grad), None)
+
+
+def rms_norm_layer(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Differentiable rms_norm (bf16 result): y, or (y, h) with a residual."""
+    return RMSNorm.apply(x, weight, residual, eps)
+
+
+class FP8NormLinear(torch.autograd.Function):
+    """Norm, then linear, the normalised activations in 8 bits between them and for the backward."""
+
+    @staticmethod
+    def forward(ctx, x, norm_weight, weight, bias, residual, eps):
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        normed = rms_norm(x, norm_weight, residual, eps, fp8=True)
+        n8, h = normed if residual is not None else (normed, x)
+        w8 = fp8_quantize(weight, 128)
+        y = fp8_linear(n8, w8, bias)
+        ctx.save_for_backward(h, norm_weight, *n8, *w8)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, norm_weight, nc, ns, wc, ws = ctx.saved_tensors
+        need_x, need_nw, need_w, need_b, need_r, _ = ctx.needs_input_grad
+        if dy is None:
+            dy = torch.zeros((*h.shape[:-1], wc.shape[0]), dtype=BF16, device=h.device)
+        through = need_x or need_nw or need_r
+        g = fp8_linear_backward((nc, ns), (wc, ws), dy.contiguous(), through, need_w, need_b)
+        dx = dnw = dr = None
+        if through:
+            dx, dnw, dr = _norm_grads(h, norm_weight, g["x"], dh, ctx.eps, (need_x, need_nw, need_r))
+        return dx, dnw, g["weight"], g["bias"], dr, None
+
+
+def fp8_norm_linear_layer(x: torch.Tensor, norm_weight: torch.Tensor, weight: torch.Tensor,
+                          bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Differentiable rms_norm(x + residual) @ weight^T (+ bias), the norm's result in block-scaled e4m3: y, or (y, h)
+    with a residual.  Between forward and backward it keeps h (bf16, the residual stream itself) and 8 bits a value of
+    the norm's result and of the weight."""
+    return FP8NormLinear.apply(x, norm_weight, weight, bias, residual, eps)

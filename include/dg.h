@@ -486,6 +486,81 @@ dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void*
                            size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Block-scaled e4m3: quantiser, linear with its gradients, root-mean-square norm.
+ *
+ * The format.  A matrix [rows, K] is held as
+ *   codes  e4m3 [rows, K]
+ *   scales e8m0 [ceil(rows / block_rows), ceil(K / 128)]   (a byte s stands for 2^(s - 127), 255 for NaN)
+ * and stands for value = code * scale.  block_rows is 1 (activations) or 128 (weights); blocks at the end of a row
+ * or column are short.  Scales are powers of two because the tensor core multiplies by such; a value has four
+ * significant bits and is an exact bf16 number (but 2^128, to which magnitudes over 31/32 of it round).
+ *
+ * dg_fp8_quantize, for each block of x [rows, K] bf16: scale = 2^e with the least e >= -124 for which
+ * max |x| <= 448 * 2^e (1 for a block of zeros), code = the e4m3 value nearest to x / scale, ties to even.  A block
+ * that holds a NaN or an infinity gets NaN for its scale and all its codes.
+ * dg_fp8_dequantize writes the values, rounded to bf16 (exact for what the quantiser wrote).
+ * K % 16 == 0; rows >= 0 (0 = nothing to do).
+ * ------------------------------------------------------------------------ */
+dg_status dg_fp8_quantize(int64_t rows, int64_t K, int32_t block_rows, const void* x, void* codes, void* scales,
+                          void* stream);
+
+dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const void* codes, const void* scales,
+                            void* x, void* stream);
+
+/*
+ * dg_fp8_linear: y = x W^T (+ bias), all of it as in dg_tp_linear_fwd but for the operands:
+ *   x_codes, x_scales   [rows, in_features], block_rows 1
+ *   w_codes, w_scales   [out_features, in_features], block_rows 128
+ *   bias [out_features] bf16 or NULL, y [rows, out_features] bf16
+ * Products of codes and scales are exact, sums binary32, one rounding to bf16.  A row of x or W with a NaN in it
+ * gives NaN in its row or column of y.
+ * in_features % 16 == 0, out_features % 16 == 0; rows >= 0 (0 = nothing to do).
+ * ws (dg_fp8_linear_workspace_bytes): the error block, then scratch; nothing in it outlives the call.
+ *
+ * dg_fp8_linear_bwd: the gradients for dy [rows, out_features] bf16, given what the forward read (the activations
+ * need not be kept in any other form):
+ *   dx       [rows, in_features]   = q(dy) W, where q(dy) is dy through dg_fp8_quantize with block_rows 1
+ *   d_weight [out_features, in_features] = dy^T x    (dy in bf16 and the values of x: both exact)
+ *   d_bias   [out_features]        = column sums of dy
+ * all bf16, overwritten; each may be NULL (not computed).  x_* may be NULL without d_weight, w_* without dx.
+ * The quantisers are passed through: dx is the gradient with respect to what x_codes stand for.
+ * rows == 0 writes zeros into d_weight and d_bias.
+ */
+size_t dg_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
+
+dg_status dg_fp8_linear(int64_t rows, int64_t in_features, int64_t out_features, const void* x_codes,
+                        const void* x_scales, const void* w_codes, const void* w_scales, const void* bias, void* y,
+                        void* ws, size_t ws_bytes, void* stream);
+
+size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
+
+dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_features, int64_t out_features, const void* x_codes,
+                            const void* x_scales, const void* w_codes, const void* w_scales, const void* dy, void* dx,
+                            void* d_weight, void* d_bias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dg_rms_norm: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, each row of d columns by itself.
+ *   x, residual, h, y [rows, d], weight [d]: bf16.  residual may be NULL: then h is x, and the argument h is NULL.
+ *   The norm is that of h as it is stored (rounded to bf16); y is rounded once, from binary32,
+ *   to bf16 (codes and scales NULL), or straight to codes and scales as dg_fp8_quantize with block_rows 1 would
+ *   (y NULL; d % 16 == 0).
+ *   d % 8 == 0, d <= 32768; eps >= 1e-30; rows >= 0 (0 = nothing to do).
+ * dg_rms_norm_bwd: with s = 1 / sqrt(mean(h^2) + eps) and dy [rows, d] the gradient of y (of what codes and scales
+ * stand for), dh [rows, d] that of h from elsewhere or NULL:
+ *   dx       [rows, d] = s (dy weight - h s^2 mean(dy weight h)) + dh     (the gradient of x and of residual)
+ *   d_weight [d]       = sum over rows of dy h s                          (in an order that the sizes fix)
+ * bf16, overwritten; either may be NULL.  rows == 0 writes zeros into d_weight.
+ * ws (dg_rms_norm_bwd_workspace_bytes): the error block, then partial sums.
+ */
+dg_status dg_rms_norm(int64_t rows, int64_t d, float eps, const void* x, const void* residual, const void* weight,
+                      void* h, void* y, void* codes, void* scales, void* stream);
+
+size_t dg_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t d);
+
+dg_status dg_rms_norm_bwd(int64_t rows, int64_t d, float eps, const void* h, const void* weight, const void* dy,
+                          const void* dh, void* dx, void* d_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics.
  * dg_debug_wait_timeout launches one small kernel that waits, with the
  * library's bounded wait, on a barrier nothing will ever arrive at; after
