@@ -83,6 +83,21 @@ dg_status run_mx(bool b_mn_major, int64_t M, int64_t N, int64_t K, const void* a
   return launched(launch_gemm_mx(b_mn_major, ma, mb, md, p, dev, s), name);
 }
 
+// The product for few rows.
+dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, const void* x, const void* sx, const void* w, const void* sw,
+                     const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s, const char* name) {
+  CUtensorMap mw, mx;
+  dg_status st;
+  const uint64_t m = M, n = N, k = K;
+  if ((st = make_map_3d(&mw, false, w, k, n, 1, k, n * k, 128, 128, 1, "weight codes")) != DG_OK) return st;
+  if ((st = make_map_3d(&mx, false, x, k, m, 1, k, m * k, 128, plan.nt, 1, "codes")) != DG_OK) return st;
+  const double wn = static_cast<double>(N) * K;
+  TraceScope trace(name, s, 2.0 * M * wn, static_cast<double>(M) * K + wn + 2.0 * M * N);
+  return launched(launch_mx_few(plan, mw, mx, w, sw, sx, bias, y, static_cast<int>(M), static_cast<int>(N),
+                                static_cast<int>(K), dev, s),
+                  name);
+}
+
 struct BwdLayout {
   size_t dy_codes, dy_scales, x, total;
 };
@@ -159,8 +174,11 @@ dg_status dg_fp8_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x
     return fail(DG_ERR_WORKSPACE, "fp8_linear: workspace has %zu bytes, needs %zu", ws_bytes, need);
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "fp8_linear")) != DG_OK) return st;
-  return run_mx(false, rows, out_f, in_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev,
-                static_cast<cudaStream_t>(stream), "fp8_linear");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const MxFewPlan few = mx_few_plan(rows, out_f, in_f, dev);
+  if (few.better)
+    return run_mx_few(few, rows, out_f, in_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev, s, "fp8_linear_few");
+  return run_mx(false, rows, out_f, in_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev, s, "fp8_linear");
 }
 
 size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {

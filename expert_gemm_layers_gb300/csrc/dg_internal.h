@@ -422,6 +422,18 @@ constexpr int kMxTileN = 224;
 cudaError_t launch_gemm_mx(bool b_mn_major, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d,
                            const MxParams& p, const DeviceInfo& dev, cudaStream_t s);
 
+// The same product for few rows (dg_mx_few.cu): rows of x a tile has, the CTAs that share its K, and whether it is
+// the form to take.
+// Box heights of the maps: W 128 rows, x plan.nt rows.
+struct MxFewPlan {
+  int nt, split;
+  bool better;
+};
+MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
+cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* w_codes,
+                          const void* sw, const void* sx, const void* bias, void* y, int M, int N, int K,
+                          const DeviceInfo& dev, cudaStream_t s);
+
 // ---------------------------------------------------------------- 4-bit weights (dg_w4.cu)
 
 // Weights [rows, K] bf16 <-> codes [rows, K/2], scales [rows, K/group] bf16

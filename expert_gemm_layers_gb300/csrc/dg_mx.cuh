@@ -67,7 +67,8 @@ struct MxCfg {
   static constexpr int NUM_THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
   static constexpr int NUM_BARS = 2 * STAGES + 4 + 2 * SF_BUFS + 1;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + BAR_BYTES;
+  static constexpr int FEED_BYTES = (2 * 4 * (BM + 4) * 4 + 15) / 16 * 16;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + FEED_BYTES + BAR_BYTES;
   // kind::mxf8f6f4 instruction descriptor: e4m3 x e4m3, majorness, N, e8m0 scales (bit 23),
   // M; bits 4-5 and 29-30 (scale index of B and A) are filled in per K block
   static constexpr uint32_t IDESC = (static_cast<uint32_t>(kBMN) << 16) | ((BN >> 3) << 17) | (1u << 23) |
@@ -115,23 +116,92 @@ static __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Arrive once on an mbarrier given by its shared::cluster address, with the default release at CTA scope: what it
+// orders here are tcgen05 accesses that have completed (wait::ld, wait::st) and been fenced.  A release at cluster
+// scope waits for the thread's memory accesses to reach that scope, up to a microsecond.
+static __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // mbar_wait by a whole warp: all lanes go on or none does.
 static __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, site));
 }
 
+// One lane of a converged warp, the same one every time.  Under `if (elect_one())` the compiler knows that a single
+// lane issues the copies and MMAs: a stage's four MMAs took 115 cycles to issue and its two copies 290, against 350
+// and 400 under `lane == 0` (clock64).
+static __device__ __forceinline__ bool elect_one() {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(v)
+      :
+      : "memory");
+  return v != 0u;
+}
+
 constexpr uint32_t kScaleOnes = 0x7f7f7f7fu;  // four scales of 1
 
-// Bytes kb..kb+3 of a scale row (consecutive K blocks, `step` bytes apart); blocks at or past `kend` read as 1.
-static __device__ __forceinline__ uint32_t scale_word(const uint8_t* p, int kb, int kend, int64_t step) {
-  if (step == 1 && kb + 4 <= kend && (reinterpret_cast<uintptr_t>(p + kb) & 3u) == 0)
-    return __ldg(reinterpret_cast<const uint32_t*>(p + kb));
-  uint32_t w = kScaleOnes;
+// How 128 threads bring block scales to the words that tcgen05.st writes, 16 K blocks at a time: the bytes of kRows
+// rows (K blocks next to one another) and of up to kBlocks 128-blocks of the other operand go through registers
+// (fetch, a batch ahead) into shared memory (publish), each byte once.  Fetched word by word in every warp and waited
+// for at once they came every 2400 cycles per 512 K, five times slower than the tensor core uses them; rows whose
+// length is no multiple of 16 blocks cost 32 sectors an instruction.
+template <int kRows, int kBlocks>
+struct ScaleFeed {
+  static constexpr int BYTES = 2 * 4 * (kRows + 4) * 4;
+  static constexpr int PER = kRows / 8;  // narrow: two rows an instruction and warp
+  uint32_t* smem;                        // [2][4 groups][kRows + 4]: rows, then blocks
+  const uint8_t *sa, *sb;
+  int64_t sb_n, sb_k;
+  int ka, rows, blocks;                  // bytes of a row; rows and blocks that exist
+  int tid;
+  bool wide;                             // rows can be read in 16 bytes
+  uint32_t v[PER < 4 ? 4 : PER], w;
+
+  __device__ __forceinline__ void fetch(int row0, int block0, int kb, int kend) {
+    const int warp = tid >> 5, lane = tid & 31;
+    if (wide) {
+      uint4 q = make_uint4(kScaleOnes, kScaleOnes, kScaleOnes, kScaleOnes);
+      if (tid < kRows && row0 + tid < rows)
+        q = __ldg(reinterpret_cast<const uint4*>(sa + static_cast<int64_t>(row0 + tid) * ka + kb));
+      v[0] = q.x;
+      v[1] = q.y;
+      v[2] = q.z;
+      v[3] = q.w;
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (kb + i < kend) w = (w & ~(0xffu << (8 * i))) | (static_cast<uint32_t>(__ldg(p + (kb + i) * step)) << (8 * i));
-  return w;
-}
+      for (int i = 0; i < PER; ++i) {
+        const int r = row0 + warp * (kRows / 4) + 2 * i + (lane >> 4), k = kb + (lane & 15);
+        v[i] = r < rows && k < kend ? __ldg(sa + static_cast<int64_t>(r) * ka + k) : 127u;
+      }
+    }
+    const int k = kb + lane;
+    w = warp < kBlocks && lane < 16 && block0 + warp < blocks && k < kend ? __ldg(sb + (block0 + warp) * sb_n + k * sb_k)
+                                                                         : 127u;
+  }
+  __device__ __forceinline__ void publish(int half) {
+    const int warp = tid >> 5, lane = tid & 31;
+    uint32_t* at = smem + half * 4 * (kRows + 4);
+    if (wide) {
+      if (tid < kRows)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) at[g * (kRows + 4) + tid] = v[g];
+    } else {
+      uint8_t* bytes = reinterpret_cast<uint8_t*>(at + ((lane & 15) >> 2) * (kRows + 4)) + (lane & 3);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) bytes[4 * (warp * (kRows / 4) + 2 * i + (lane >> 4))] = static_cast<uint8_t>(v[i]);
+    }
+    if (warp < kBlocks && lane < 16)
+      reinterpret_cast<uint8_t*>(at + (lane >> 2) * (kRows + 4) + kRows + warp)[lane & 3] = static_cast<uint8_t>(w);
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+  }
+  __device__ __forceinline__ uint32_t row(int half, int g, int r) const { return smem[(half * 4 + g) * (kRows + 4) + r]; }
+  __device__ __forceinline__ uint32_t block(int half, int g, int b) const {
+    return smem[(half * 4 + g) * (kRows + 4) + kRows + b];
+  }
+};
 
 template <bool kBMN, int kBN>
 __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
@@ -139,12 +209,11 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
                    const __grid_constant__ CUtensorMap tmD, const MxParams p) {
   using Cfg = MxCfg<kBMN, kBN>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t s_abort;
 
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stage_base = smem_raw + pad;
   uint8_t* epi_base = stage_base + Cfg::STAGES * Cfg::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(epi_base + Cfg::EPI_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi_base + Cfg::EPI_BYTES + Cfg::FEED_BYTES);
   uint64_t* empty = full + Cfg::STAGES;
   uint64_t* tfull = empty + Cfg::STAGES;
   uint64_t* tempty = tfull + 2;
@@ -153,7 +222,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
   uint64_t* drain = sf_empty + Cfg::SF_BUFS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // known to be uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0u;
@@ -177,24 +246,15 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmD);
   }
-  cluster_sync_all();
-  griddep_wait();
-
-  // a failure recorded earlier: the leader decides for the pair
-  if (threadIdx.x == 0 && leader) {
-    const uint32_t v = ld_volatile_u32(p.err);
-    st_cluster_u32(mapa_shared(smem_u32(&s_abort), 0), v);
-    st_cluster_u32(mapa_shared(smem_u32(&s_abort), 1), v);
-  }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, 512);
     tmem_relinquish_pair();
   }
+  griddep_wait();
   tc_fence_before_sync();
   cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
-  const bool aborted = s_abort != 0u;
 
   const int total_tiles = p.tiles_m * p.tiles_n;
   const int num_kb = p.ka;
@@ -210,11 +270,11 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
     }
   };
 
-  if (aborted) {
-    // straight to the teardown
-  } else if (warp == 0) {
+  // After a failure recorded earlier the pipeline still runs (or gives up at its first long wait, which looks
+  // at the error word) but nothing is stored: that way no CTA waits for the word before its first copy.
+  if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_parity = 0;
       bool ok = true;
@@ -228,9 +288,10 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES * Cfg::CTAS);
+          // the pair's copies all complete on the leader's barrier
           const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
           uint8_t* sa = stage_base + stage * Cfg::STAGE_BYTES;
+          if (leader) mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES * Cfg::CTAS);
           tma_load_3d_pair(sa, &tmA, bar, kb * Cfg::BK, m0, 0);
           if (kBMN)
             tma_load_3d_pair(sa + Cfg::A_BYTES, &tmB, bar, n0, kb * Cfg::BK, 0);
@@ -253,56 +314,57 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (pair leader)
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       int stage = 0, sfb = 0;
       uint32_t phase = 0, tphase = 0, sfphase = 0;
       bool ok = true;
       int local = 0;
+      // K-major: 32 bytes on in the swizzle row per K step.  MN-major: 32 K rows of 128 bytes on;
+      // groups of 8 K rows lie 1024 bytes apart.
+      const uint64_t a0 = smem_desc_sw128(smem_u32(stage_base), 16, 1024);
+      const uint64_t b0 = smem_desc_sw128(smem_u32(stage_base) + Cfg::A_BYTES, kBMN ? 128 * 128 : 16, 1024);
       for (int tile = unit; tile < total_tiles && ok; tile += num_units, ++local) {
         const int acc = local & 1;
         if (!mbar_wait(&tempty[acc], ((tphase >> acc) & 1u) ^ 1u, p.err, SITE_TEMPTY)) break;
         tphase ^= 1u << acc;
-        tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * Cfg::BN);
-        for (int kb = 0; kb < num_kb; ++kb) {
-          const uint32_t q = static_cast<uint32_t>(kb) & 3u;
-          if (q == 0 && !mbar_wait(&sf_full[sfb], sfphase, p.err, SITE_SF_FULL)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait(&full[stage], phase, p.err, SITE_FULL)) {
+        // four K blocks a turn, straight through: what lies between one block's MMAs and the next one's leaves the
+        // tensor core without work
+        for (int kb = 0; kb < num_kb && ok; kb += 4) {
+          if (!mbar_wait(&sf_full[sfb], sfphase, p.err, SITE_SF_FULL)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t sa = smem_u32(stage_base + stage * Cfg::STAGE_BYTES);
-          const uint32_t sb = sa + Cfg::A_BYTES;
-          const uint32_t idesc = Cfg::IDESC | (q << 4) | (q << 29);
           const uint32_t sf = tmem_base + static_cast<uint32_t>(Cfg::SF_BASE + sfb * Cfg::SF_COLS);
 #pragma unroll
-          for (int j = 0; j < Cfg::K_STEPS; ++j) {
-            // K-major: 32 bytes on in the swizzle row.  MN-major: 32 K rows of 128 bytes on;
-            // groups of 8 K rows lie 1024 bytes apart.
-            const uint64_t ad = smem_desc_sw128(sa + j * 32, 16, 1024);
-            const uint64_t bd = kBMN ? smem_desc_sw128(sb + j * 4096, 128 * 128, 1024) : smem_desc_sw128(sb + j * 32, 16, 1024);
-            umma_mxf8_pair(d_tmem, ad, bd, idesc, sf, sf + 8, (kb > 0 || j > 0) ? 1u : 0u);
-          }
-          tc_commit_pair_mc(&empty[stage], 0x3);
-          if (++stage == Cfg::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (q == 3u || kb + 1 == num_kb) {
-            tc_commit_pair_mc(&sf_empty[sfb], 0x3);
-            if (++sfb == Cfg::SF_BUFS) {
-              sfb = 0;
-              sfphase ^= 1u;
+          for (uint32_t q = 0; q < 4; ++q) {
+            if (kb + static_cast<int>(q) >= num_kb) break;
+            ok = ok && mbar_wait(&full[stage], phase, p.err, SITE_FULL);
+            if (!ok) break;
+            const uint64_t ad = a0 + static_cast<uint32_t>(stage * (Cfg::STAGE_BYTES / 16));
+            const uint64_t bd = b0 + static_cast<uint32_t>(stage * (Cfg::STAGE_BYTES / 16));
+            constexpr uint32_t kScaleId = (1u << 4) | (1u << 29);
+#pragma unroll
+            for (int j = 0; j < Cfg::K_STEPS; ++j)
+              umma_mxf8_pair(d_tmem, ad + 2 * j, bd + (kBMN ? 256 : 2) * j, Cfg::IDESC + q * kScaleId, sf, sf + 8,
+                             (kb > 0 || q > 0 || j > 0) ? 1u : 0u);
+            tc_commit_pair_mc(&empty[stage], 0x3);
+            if (++stage == Cfg::STAGES) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
+          if (!ok) break;
+          tc_commit_pair_mc(&sf_empty[sfb], 0x3);
+          if (++sfb == Cfg::SF_BUFS) {
+            sfb = 0;
+            sfphase ^= 1u;
+          }
         }
-        if (!ok) break;
-        tc_commit_pair_mc(&tfull[acc], 0x3);
+        if (ok) tc_commit_pair_mc(&tfull[acc], 0x3);
       }
+      // every MMA issued must complete before TMEM is released
       tc_commit_pair_mc(drain, 0x1);
       if (!mbar_try_wait(drain, 0)) {
         uint32_t dummy = 0;
@@ -314,6 +376,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
     const int lg = warp & 3;
     uint8_t* stg = epi_base + (warp - 2) * 2 * Cfg::EPI_BUF_BYTES;
     uint32_t tphase = 0, ctr = 0;
+    const bool aborted = ld_volatile_u32(p.err) != 0u;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * lg) << 16);
     int local = 0;
     for (int tile = unit; tile < total_tiles; tile += num_units, ++local) {
@@ -330,7 +393,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
       auto release_acc = [&]() {
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        if (lane == 0) mbar_arrive_pair(mapa_shared(smem_u32(&tempty[acc]), 0));
       };
       if (nchunks == 0) release_acc();
       for (int j = 0; j < nchunks; ++j, ++ctr) {
@@ -369,7 +432,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && !aborted) {
           tma_store_3d(&tmD, sbuf, c0, row0, 0);
           bulk_commit_group();
         }
@@ -380,48 +443,58 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
   } else {
     // ------------------------------------------------------------ scales
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    int buf = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = unit; tile < total_tiles && ok; tile += num_units) {
+    ScaleFeed<Cfg::BM, Cfg::NB_BLOCKS> feed;
+    feed.smem = reinterpret_cast<uint32_t*>(epi_base + Cfg::EPI_BYTES);
+    feed.sa = p.sa;
+    feed.sb = p.sb;
+    feed.sb_n = p.sb_n;
+    feed.sb_k = p.sb_k;
+    feed.ka = p.ka;
+    feed.rows = p.M;
+    feed.blocks = (p.N + 127) / 128;
+    feed.tid = static_cast<int>(threadIdx.x) - (Cfg::NUM_THREADS - 128);
+    feed.wide = (p.ka & 15) == 0;
+    auto fetch = [&](int tile, int kb) {
       int mt, nt;
       coords(tile, mt, nt);
-      const int m0 = mt * Cfg::UMMA_M + static_cast<int>(rank) * Cfg::BM + lane;
+      feed.fetch(mt * Cfg::UMMA_M + static_cast<int>(rank) * Cfg::BM, (nt * Cfg::BN) >> 7, kb, num_kb);
+    };
+    int buf = 0, half = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    if (unit < total_tiles) fetch(unit, 0);
+    for (int tile = unit; tile < total_tiles; tile += num_units) {
+      int mt, nt;
+      coords(tile, mt, nt);
       const int n0 = nt * Cfg::BN;
-      const int nb0 = n0 >> 7;
-      for (int kb = 0; kb < num_kb; kb += 4) {
-        uint32_t a[4], blk[Cfg::NB_BLOCKS], b[8];
+      for (int kb = 0; kb < num_kb; kb += 16, half ^= 1) {
+        feed.publish(half);
+        if (kb + 16 < num_kb)
+          fetch(tile, kb + 16);
+        else if (tile + num_units < total_tiles)
+          fetch(tile + num_units, 0);
+        for (int g = 0; g < 4 && kb + 4 * g < num_kb; ++g) {
+          uint32_t a[4], b[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[j] = m0 + 32 * j < p.M ? scale_word(p.sa + static_cast<int64_t>(m0 + 32 * j) * p.ka, kb, num_kb, 1) : kScaleOnes;
+          for (int j = 0; j < 4; ++j) a[j] = feed.row(half, g, lane + 32 * j);
 #pragma unroll
-        for (int j = 0; j < Cfg::NB_BLOCKS; ++j)
-          blk[j] = (nb0 + j) * 128 < p.N ? scale_word(p.sb + static_cast<int64_t>(nb0 + j) * p.sb_n, kb, num_kb, p.sb_k) : kScaleOnes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          b[j] = kScaleOnes;
-          if (j < Cfg::NB_WORDS) {
-            const int at = ((n0 + lane + 32 * j) >> 7) - nb0;
-#pragma unroll
-            for (int i = 0; i < Cfg::NB_BLOCKS; ++i)
-              if (at == i) b[j] = blk[i];
+          for (int j = 0; j < 8; ++j)
+            b[j] = j < Cfg::NB_WORDS ? feed.block(half, g, ((n0 + lane + 32 * j) >> 7) - (n0 >> 7)) : kScaleOnes;
+          // after a failed wait the warp only keeps the others company at the feed's barrier
+          ok = ok && warp_wait(&sf_empty[buf], phase ^ 1u, p.err, SITE_SF_EMPTY);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint32_t at = lane_addr + static_cast<uint32_t>(Cfg::SF_BASE + buf * Cfg::SF_COLS);
+          tmem_st_32x32b_x4(at, a);
+          tmem_st_32x32b_x8(at + 8, b);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(mapa_shared(smem_u32(&sf_full[buf]), 0));
+          if (++buf == Cfg::SF_BUFS) {
+            buf = 0;
+            phase ^= 1u;
           }
-        }
-        if (!warp_wait(&sf_empty[buf], phase ^ 1u, p.err, SITE_SF_EMPTY)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t at = lane_addr + static_cast<uint32_t>(Cfg::SF_BASE + buf * Cfg::SF_COLS);
-        tmem_st_32x32b_x4(at, a);
-        tmem_st_32x32b_x8(at + 8, b);
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sf_full[buf]), 0));
-        if (++buf == Cfg::SF_BUFS) {
-          buf = 0;
-          phase ^= 1u;
         }
       }
     }

@@ -106,7 +106,8 @@ def test_dequantize_every_scale():
 
 LINEAR = [(1, 16, 16), (1, 4096, 256), (2, 128, 240), (7, 144, 224), (16, 512, 448), (17, 528, 464), (33, 2064, 128),
           (64, 1024, 1024), (100, 1296, 2064), (128, 640, 272), (129, 256, 512), (256, 896, 224), (257, 384, 688),
-          (511, 2048, 480), (1000, 272, 1296)]
+          (511, 2048, 480), (1000, 272, 1296), (3, 8192, 144), (40, 8208, 272), (65, 4112, 128), (100, 8192, 528),
+          (128, 8208, 400), (300, 12288, 272)]
 
 
 @pytest.mark.parametrize("rows,K,N", LINEAR)
@@ -118,7 +119,7 @@ def test_linear(rows, K, N, bias):
     within(y, fp8.linear(x, w, None if b is None else f64(b)), "y")
 
 
-@pytest.mark.parametrize("rows,K,N", [(3, 2176, 400), (40, 1152, 656), (300, 1664, 528)])
+@pytest.mark.parametrize("rows,K,N", [(3, 2176, 400), (40, 1152, 656), (300, 1664, 528), (7, 8320, 144), (90, 8320, 400)])
 def test_every_block_has_its_own_scale(rows, K, N):
     """Codes of one, scales of all sizes: each sum is that of its own blocks' scales, exactly."""
     rng = np.random.default_rng(rows)
@@ -129,7 +130,7 @@ def test_every_block_has_its_own_scale(rows, K, N):
     x, w = np.full((rows, K), 0x38, np.uint8), np.full((N, K), 0x38, np.uint8)
     y = dg.fp8_linear((one((rows, K)), torch.from_numpy(xs).view(E8M0).to(DEV)),
                       (one((N, K)), torch.from_numpy(ws).view(E8M0).to(DEV)))
-    exact = fp8.values(x, xs) @ fp8.values(w, ws, 128).T   # at most 17 bits between 2^-8 and 2^19 * 17
+    exact = fp8.values(x, xs) @ fp8.values(w, ws, 128).T   # multiples of 2^-8 below 2^16: 24 bits
     assert np.array_equal(f64(y), fp8.bf16_rne(exact.astype(np.float32)))
 
 
