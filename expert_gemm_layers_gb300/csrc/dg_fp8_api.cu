@@ -98,14 +98,23 @@ dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, con
                   name);
 }
 
+dg_status run_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x, const void* sx, const void* w,
+                     const void* sw, const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s) {
+  const MxFewPlan few = mx_few_plan(rows, out_f, in_f, dev);
+  if (few.better) return run_mx_few(few, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear_few");
+  return run_mx(false, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear");
+}
+
+// Workspace of the backward: the error block, dy in 8 bits, partial column sums, x in bf16.
 struct BwdLayout {
-  size_t dy_codes, dy_scales, x, total;
+  size_t dy_codes, dy_scales, sums, x, total;
 };
 BwdLayout bwd_layout(int64_t rows, int64_t in_f, int64_t out_f) {
   BwdLayout l;
   l.dy_codes = DG_ERROR_BLOCK_BYTES;
   l.dy_scales = round256(l.dy_codes + elements(rows, out_f));
-  l.x = round256(l.dy_scales + scale_bytes(rows, out_f, 1));
+  l.sums = round256(l.dy_scales + scale_bytes(rows, out_f, 1));
+  l.x = round256(l.sums + 4 * elements(fp8_quantize_sum_parts(rows, static_cast<int>(out_f)), out_f));
   l.total = round256(l.x + 2 * elements(rows, in_f));
   return l;
 }
@@ -150,6 +159,44 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
   return launched(launch_fp8_dequantize(codes, scales, x, rows, static_cast<int>(K), block_rows, s), "fp8_dequantize");
 }
 
+// Where the activations come in bf16, their codes and scales lie in the workspace behind the error block.
+static size_t linear_scales_at(int64_t rows, int64_t in_f) {
+  return round256(DG_ERROR_BLOCK_BYTES + elements(rows, in_f));
+}
+
+size_t dg_fp8_linear_bf16_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
+  if (check_linear(rows, in_features, out_features, "fp8_linear_bf16") != DG_OK) return 0;
+  return linear_scales_at(rows, in_features) + round256(scale_bytes(rows, in_features, 1));
+}
+
+dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_f, int64_t out_f, const void* x, const void* w_codes,
+                             const void* w_scales, const void* bias, void* y, void* ws, size_t ws_bytes, void* stream) {
+  dg_status st = check_linear(rows, in_f, out_f, "fp8_linear_bf16");
+  if (st != DG_OK || rows == 0) return st;
+  const size_t scales_at = linear_scales_at(rows, in_f), need = scales_at + round256(scale_bytes(rows, in_f, 1));
+  const Arg args[] = {{"x", x, 2 * elements(rows, in_f), false, false},
+                      {"w_codes", w_codes, elements(out_f, in_f), false, false},
+                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), false, false},
+                      {"bias", bias, 2 * static_cast<size_t>(out_f), true, false},
+                      {"y", y, 2 * elements(rows, out_f), false, true},
+                      {"ws", ws, ws ? need : 0, true, true}};
+  if ((st = check_args("fp8_linear_bf16", args)) != DG_OK) return st;
+  if ((st = check_error_block(ws, ws_bytes, "fp8_linear_bf16")) != DG_OK) return st;
+  if (ws_bytes < need)
+    return fail(DG_ERR_WORKSPACE, "fp8_linear_bf16: workspace has %zu bytes, needs %zu", ws_bytes, need);
+  DeviceInfo dev;
+  if ((st = device_info_ws(&dev, ws, ws_bytes, "fp8_linear_bf16")) != DG_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* codes = static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES;
+  uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at;
+  {
+    TraceScope trace("fp8_quantize", s, 0.0, 3.0 * elements(rows, in_f));
+    st = launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(in_f), 1, s), "fp8_linear_bf16");
+    if (st != DG_OK) return st;
+  }
+  return run_linear(rows, in_f, out_f, codes, scales, w_codes, w_scales, bias, y, dev, s);
+}
+
 size_t dg_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
   if (check_linear(rows, in_features, out_features, "fp8_linear") != DG_OK) return 0;
   return DG_ERROR_BLOCK_BYTES;
@@ -174,11 +221,8 @@ dg_status dg_fp8_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x
     return fail(DG_ERR_WORKSPACE, "fp8_linear: workspace has %zu bytes, needs %zu", ws_bytes, need);
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "fp8_linear")) != DG_OK) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const MxFewPlan few = mx_few_plan(rows, out_f, in_f, dev);
-  if (few.better)
-    return run_mx_few(few, rows, out_f, in_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev, s, "fp8_linear_few");
-  return run_mx(false, rows, out_f, in_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev, s, "fp8_linear");
+  return run_linear(rows, in_f, out_f, x_codes, x_scales, w_codes, w_scales, bias, y, dev,
+                    static_cast<cudaStream_t>(stream));
 }
 
 size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
@@ -218,8 +262,12 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
   }
   if (dx) {
     {
+      // the bias's gradient comes along: dy is read once for both
       TraceScope trace("fp8_bwd_quantize_dy", s, 0.0, 3.0 * yn);
-      st = launched(launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, static_cast<int>(out_f), 1, s),
+      const int K = static_cast<int>(out_f);
+      st = launched(d_bias ? launch_fp8_quantize_sum(dy, base + l.dy_codes, base + l.dy_scales, d_bias,
+                                                     reinterpret_cast<float*>(base + l.sums), rows, K, s)
+                           : launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, K, 1, s),
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
@@ -251,7 +299,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
                        2.0 * (static_cast<double>(yn) + xn + wn))) != DG_OK)
       return st;
   }
-  if (d_bias) {
+  if (d_bias && !dx) {
     TraceScope trace("fp8_linear_bwd_db", s, 0.0, 2.0 * yn + 2.0 * out_f);
     return launched(launch_column_sum(dy, d_bias, 1, static_cast<int>(rows), static_cast<int>(out_f), 0, out_f, dev, s),
                     "fp8_linear_bwd");

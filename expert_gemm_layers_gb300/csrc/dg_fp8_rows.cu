@@ -3,6 +3,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "dg_internal.h"
 
 namespace dg {
@@ -196,31 +198,31 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __rest
 
 // ------------------------------------------------------------------ root-mean-square norm
 
-// Sum over the `T` threads of a row (a power of two from 32 to blockDim.x); all of them get it, in one fixed order.
-template <int kSums>
-__device__ __forceinline__ void row_sum(float (&v)[kSums], int T, float (*part)[32]) {
+// Sums over the threads of a row: a warp (kWarp) or the whole CTA; all of them get the sums, in one fixed order.
+template <bool kWarp, int kSums>
+__device__ __forceinline__ void row_sum(float (&v)[kSums], float (*part)[32]) {
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (T == 32) return;
-  const int warp = threadIdx.x >> 5;
+  if (kWarp) return;
   __syncthreads();  // the previous sums have been read
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int k = 0; k < kSums; ++k) part[k][warp] = v[k];
+    for (int k = 0; k < kSums; ++k) part[k][threadIdx.x >> 5] = v[k];
   __syncthreads();
-  const int w0 = warp & ~((T >> 5) - 1);
+  const int warps = blockDim.x >> 5;
 #pragma unroll
   for (int k = 0; k < kSums; ++k) {
     float s = 0.0f;
-    for (int w = 0; w < (T >> 5); ++w) s += part[k][w0 + w];
+    for (int w = 0; w < warps; ++w) s += part[k][w];
     v[k] = s;
   }
 }
 
 // A row whose squares overflow binary32 is summed as (h 2^-64)^2 instead.
 constexpr float kShrink = 5.42101086242752217e-20f;  // 2^-64
+constexpr int kWarpRows = 8;                          // rows of a CTA where a warp takes one
 
 struct NormArgs {
   const __nv_bfloat16 *x, *res, *w;
@@ -231,14 +233,15 @@ struct NormArgs {
   float eps;
 };
 
-// T threads a row, C chunks of eight columns a thread (chunk i of a thread is i * T + its number:
-// 16 lanes hold a block of 128 columns).
-template <int T, int C, bool kFp8>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(const NormArgs a) {
+// A row a warp (kWarp) or CTA of T threads, C chunks of eight columns a thread, all read at once and kept in registers:
+// chunk i of thread t is i * T + t, so that 16 lanes hold a block of 128 columns.  Bound by memory: 8192 x 4096 with a
+// residual into 8 bits takes 35 us for 235 MB.
+template <bool kWarp, int C, bool kFp8, int kMaxT>
+__global__ void __launch_bounds__(kMaxT) rms_norm_kernel(const NormArgs a) {
   __shared__ float part[1][32];
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  const int t = threadIdx.x & (T - 1);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+  const int T = kWarp ? 32 : blockDim.x;
+  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   const bool live = row < a.rows;
   const int chunks = a.d / 8;
   griddep_wait();
@@ -268,26 +271,22 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_kernel(const NormA
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
   }
-  row_sum<1>(sum, T, part);
+  row_sum<kWarp, 1>(sum, part);
   const float n = static_cast<float>(a.d);
   float rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
   float pre = 1.0f;
-  // (all rows of a CTA take the slow path together: it has barriers)
-  const bool over = !(sum[0] < __int_as_float(0x7f800000));
-  if (T == 32 ? __any_sync(0xffffffffu, over) : __syncthreads_or(over)) {
-    float s2[1] = {0.0f};
+  if (!(sum[0] < __int_as_float(0x7f800000))) {  // the same for all threads of the row
+    sum[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float v[8];
       unpack8(xv[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s2[0] = fmaf(v[e] * kShrink, v[e] * kShrink, s2[0]);
+      for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[e] * kShrink, v[e] * kShrink, sum[0]);
     }
-    row_sum<1>(s2, T, part);
-    if (over) {
-      rstd = 1.0f / sqrtf(s2[0] / n);  // eps is far below the last bit
-      pre = kShrink;
-    }
+    row_sum<kWarp, 1>(sum, part);
+    rstd = 1.0f / sqrtf(sum[0] / n);  // eps is far below the last bit
+    pre = kShrink;
   }
 #pragma unroll
   for (int i = 0; i < C; ++i) {
@@ -323,43 +322,57 @@ struct NormBwdArgs {
   float eps;
 };
 
-// As rms_norm_kernel, a CTA taking every gridDim.x-th group of rows; the weight's gradient stays in
-// registers over a thread's rows and leaves as one partial sum a CTA.
-template <int T, int C>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_bwd_kernel(const NormBwdArgs a) {
+// Threads and chunks as in rms_norm_kernel; a CTA takes every gridDim.x-th row (or kWarpRows rows), the next one read
+// while this one is worked on (but for rows of over 8192 columns, whose 1024 threads have no registers for two).  The weight's gradient stays in registers over a thread's rows and leaves as one partial
+// sum a CTA.
+template <bool kWarp, int C, int kMaxT>
+__global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
   __shared__ float part[2][32];
-  extern __shared__ float wsum[];  // T < 256: [256 / T - 1][T * C * 8]
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  const int t = threadIdx.x & (T - 1);
-  const int sub = threadIdx.x / T;
+  __shared__ float wsum[kWarp ? kWarpRows - 1 : 1][kWarp ? 32 * C * 8 : 1];
+  const int T = kWarp ? 32 : blockDim.x;
+  const int t = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int sub = kWarp ? threadIdx.x >> 5 : 0;
+  constexpr int kRows = kWarp ? kWarpRows : 1;
   const int chunks = a.d / 8;
   const float n = static_cast<float>(a.d);
   griddep_wait();
   griddep_launch_dependents();
-  uint4 wv[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-    wv[i] = t + i * T < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
-  float dw[C][8] = {};
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * kRows) {
-    const int64_t row = r0 + sub;
-    const bool live = row < a.rows;
-    uint4 hv[C], yv[C], pv[C];
+  uint4 wv[C], hv[C], yv[C], pv[C];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int c = t + i * T;
-      const bool in = live && c < chunks;
+      const bool in = row < a.rows && c < chunks;
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
       hv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.h + row * a.d) + c) : z;
       yv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.dy + row * a.d) + c) : z;
       pv[i] = in && a.dh ? __ldcs(reinterpret_cast<const uint4*>(a.dh + row * a.d) + c) : z;
     }
+  };
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+    wv[i] = t + i * T < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
+  float dw[C][8] = {};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  constexpr bool kAhead = C < 4;
+  if (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * kRows + sub);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + sub;
+    if (!kAhead) fetch(row);
+    uint4 hc[C], yc[C], pc[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      hc[i] = hv[i];
+      yc[i] = yv[i];
+      pc[i] = pv[i];
+    }
+    if (kAhead && r0 + step < a.rows) fetch(row + step);
     float s[2] = {0.0f, 0.0f};  // sum h^2, sum (dy w) h
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float h[8], y[8], g[8];
-      unpack8(hv[i], h);
-      unpack8(yv[i], y);
+      unpack8(hc[i], h);
+      unpack8(yc[i], y);
       unpack8(wv[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -367,30 +380,26 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_bwd_kernel(const N
         s[1] = fmaf(y[e] * g[e], h[e], s[1]);
       }
     }
-    row_sum<2>(s, T, part);
+    row_sum<kWarp, 2>(s, part);
     float pre = 1.0f, rstd = 1.0f / sqrtf(s[0] / n + a.eps);
-    const bool over = !(s[0] < __int_as_float(0x7f800000));
-    if (T == 32 ? __any_sync(0xffffffffu, over) : __syncthreads_or(over)) {
-      float q[2] = {0.0f, 0.0f};
+    if (!(s[0] < __int_as_float(0x7f800000))) {
+      s[0] = s[1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         float h[8], y[8], g[8];
-        unpack8(hv[i], h);
-        unpack8(yv[i], y);
+        unpack8(hc[i], h);
+        unpack8(yc[i], y);
         unpack8(wv[i], g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float u = h[e] * kShrink;
-          q[0] = fmaf(u, u, q[0]);
-          q[1] = fmaf(y[e] * g[e], u, q[1]);
+          s[0] = fmaf(u, u, s[0]);
+          s[1] = fmaf(y[e] * g[e], u, s[1]);
         }
       }
-      row_sum<2>(q, T, part);
-      if (over) {
-        pre = kShrink;
-        rstd = 1.0f / sqrtf(q[0] / n);
-        s[1] = q[1];
-      }
+      row_sum<kWarp, 2>(s, part);
+      pre = kShrink;
+      rstd = 1.0f / sqrtf(s[0] / n);
     }
     // with n_h = h pre rstd (the normalised row): dx = rstd pre (dy w - n_h mean(dy w n_h)) + dh
     const float mean = s[1] * rstd / n;
@@ -398,91 +407,136 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rms_norm_bwd_kernel(const N
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float h[8], y[8], g[8], p[8];
-      unpack8(hv[i], h);
-      unpack8(yv[i], y);
+      unpack8(hc[i], h);
+      unpack8(yc[i], y);
       unpack8(wv[i], g);
-      unpack8(pv[i], p);
+      unpack8(pc[i], p);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float nh = h[e] * pre * rstd;
         dw[i][e] = fmaf(y[e], nh, dw[i][e]);
         p[e] = fmaf(out, fmaf(-nh, mean, y[e] * g[e]), p[e]);
       }
-      if (a.dx && live && t + i * T < chunks) reinterpret_cast<uint4*>(a.dx + row * a.d)[t + i * T] = pack8(p);
+      if (a.dx && row < a.rows && t + i * T < chunks) reinterpret_cast<uint4*>(a.dx + row * a.d)[t + i * T] = pack8(p);
     }
   }
   if (!a.part) return;
-  float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
-  if (kRows > 1) {
+  if (kWarp) {
     if (sub > 0)
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wsum[((sub - 1) * T * C + i * T + t) * 8 + e] = dw[i][e];
+        for (int e = 0; e < 8; ++e) wsum[sub - 1][(i * 8 + e) * 32 + t] = dw[i][e];
     __syncthreads();
     if (sub > 0) return;
+#pragma unroll
+    for (int k = 0; k < kRows - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] += wsum[k][(i * 8 + e) * 32 + t];
   }
+  float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
     if (c >= chunks) continue;
-#pragma unroll
-    for (int k = 0; k < kRows - 1; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i][e] += wsum[(k * T * C + c) * 8 + e];
     float4* o = reinterpret_cast<float4*>(out + 8 * c);
     o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
     o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
   }
 }
 
-// d_weight[c] = sum over `parts` partial sums, in order: 32 columns a CTA, 8 warps over the partials.
-__global__ void __launch_bounds__(kThreads) norm_weight_grad_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
-                                                                    int parts, int d) {
-  __shared__ float s[kThreads / 32][32];
+// out[c] = sum over `parts` partial sums part[k][c], in an order that the sizes fix: 32 columns a CTA, the partial sums
+// spread over its 32 warps, four loads in flight each.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
+                                                         int parts, int d) {
+  __shared__ float s[32][33];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
-  if (c < d)
-    for (int k = warp; k < parts; k += kThreads / 32) v += part[static_cast<int64_t>(k) * d + c];
+  if (c < d) {
+    const float* p = part + c;
+    int k = warp;
+    for (; k + 96 < parts; k += 128) {
+      float u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __ldcs(p + static_cast<int64_t>(k + 32 * i) * d);
+      v += (u[0] + u[1]) + (u[2] + u[3]);
+    }
+    for (; k < parts; k += 32) v += __ldcs(p + static_cast<int64_t>(k) * d);
+  }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < d) {
+  float r = s[lane][warp];  // warp w adds up column w
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane == 0 && col < d) out[col] = __float2bfloat16_rn(r);
+}
+
+// ------------------------------------------------------------------ quantise a gradient and sum its columns
+
+// Blocks of 1 x 128 as quant_rows_kernel, one CTA taking a column block and every gridDim.y-th group of 16 rows, so that
+// the column sums of what it reads stay in registers: part[blockIdx.y][column].
+__global__ void __launch_bounds__(kThreads) quant_rows_sum_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
+                                                                  uint8_t* __restrict__ scale, float* __restrict__ part,
+                                                                  int64_t rows, int K, int nb) {
+  __shared__ float s[kThreads / 16][128 + 4];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int c = blockIdx.x * 128 + 8 * sub;
+  float sum[8] = {};
+  const int64_t step = 16 * static_cast<int64_t>(gridDim.y);
+  // kUnits rows a thread in flight; whole groups of 16 rows, so that the lanes of a block stay together
+  constexpr int kUnits = 4;
+  for (int64_t r0 = 16 * static_cast<int64_t>(blockIdx.y); r0 < rows; r0 += kUnits * step) {
+    uint4 v[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int64_t r = r0 + i * step + group;
+      v[i] = r < rows && c < K ? __ldcs(reinterpret_cast<const uint4*>(x + r * K + c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int64_t r = r0 + i * step + group;
+      const uint32_t byte = scale_byte(max16(amax_bits8(v[i])) << 16);
+      float f[8];
+      unpack8(v[i], f);
+      if (r < rows && c < K) *reinterpret_cast<uint2*>(q + r * K + c) = codes8(f, byte);
+      if (r < rows && sub == 0) scale[r * nb + blockIdx.x] = static_cast<uint8_t>(byte);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += f[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[group][8 * sub + e] = sum[e];
+  __syncthreads();
+  const int col = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && col < K) {
     float r = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) r += s[k][lane];
-    out[c] = __float2bfloat16_rn(r);
+    for (int g = 0; g < kThreads / 16; ++g) r += s[g][threadIdx.x];
+    part[static_cast<int64_t>(blockIdx.y) * K + col] = r;
   }
 }
 
-template <int T, int C, bool kFp8>
-cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  return launch_pdl(rms_norm_kernel<T, C, kFp8>, dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)),
-                    dim3(T < 256 ? 256 : T), 0, s, a);
-}
+// Threads of a CTA that takes one row in C chunks a thread, and the instance for a row length: one warp up to 512
+// columns, then as few threads as hold the row.
+int row_threads(int d, int C) { return ((d / 8 + C - 1) / C + 31) / 32 * 32; }
 
 template <bool kFp8>
-cudaError_t norm_launch_d(const NormArgs& a, cudaStream_t s) {
-  if (a.d <= 256) return norm_launch<32, 1, kFp8>(a, s);
-  if (a.d <= 1024) return norm_launch<128, 1, kFp8>(a, s);
-  if (a.d <= 2048) return norm_launch<256, 1, kFp8>(a, s);
-  if (a.d <= 4096) return norm_launch<256, 2, kFp8>(a, s);
-  if (a.d <= 8192) return norm_launch<512, 2, kFp8>(a, s);
-  if (a.d <= 16384) return norm_launch<1024, 2, kFp8>(a, s);
-  return norm_launch<1024, 4, kFp8>(a, s);
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
+  const dim3 warp_grid(static_cast<unsigned>((a.rows + kWarpRows - 1) / kWarpRows)), grid(static_cast<unsigned>(a.rows));
+  if (a.d <= 256) return launch_pdl(rms_norm_kernel<true, 1, kFp8, 256>, warp_grid, dim3(32 * kWarpRows), 0, s, a);
+  if (a.d <= 512) return launch_pdl(rms_norm_kernel<true, 2, kFp8, 256>, warp_grid, dim3(32 * kWarpRows), 0, s, a);
+  if (a.d <= 2048) return launch_pdl(rms_norm_kernel<false, 1, kFp8, 256>, grid, dim3(row_threads(a.d, 1)), 0, s, a);
+  if (a.d <= 8192) return launch_pdl(rms_norm_kernel<false, 2, kFp8, 512>, grid, dim3(row_threads(a.d, 2)), 0, s, a);
+  return launch_pdl(rms_norm_kernel<false, 4, kFp8, 1024>, grid, dim3(row_threads(a.d, 4)), 0, s, a);
 }
-
-template <int T, int C>
-cudaError_t norm_bwd_launch(const NormBwdArgs& a, int grid, cudaStream_t s) {
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  return launch_pdl(rms_norm_bwd_kernel<T, C>, dim3(grid), dim3(T < 256 ? 256 : T),
-                    sizeof(float) * (kRows - 1) * T * C * 8, s, a);
-}
-
-int norm_threads(int d) { return d <= 256 ? 32 : d <= 1024 ? 128 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
 
 }  // namespace
 
@@ -516,13 +570,14 @@ cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void*
   const NormArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res),
                    static_cast<const __nv_bfloat16*>(w), static_cast<__nv_bfloat16*>(h), static_cast<__nv_bfloat16*>(y),
                    static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, d, (d + 127) / 128, eps};
-  return codes ? norm_launch_d<true>(a, s) : norm_launch_d<false>(a, s);
+  return codes ? norm_launch<true>(a, s) : norm_launch<false>(a, s);
 }
 
 int rms_norm_bwd_parts(int64_t rows, int d) {
-  const int T = norm_threads(d);
-  const int64_t groups = T < 256 ? (rows + 256 / T - 1) / (256 / T) : rows;
-  const int64_t most = 152 * (T <= 256 ? 3 : T == 512 ? 2 : 1);
+  const bool warp = d <= 512;
+  const int64_t groups = warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
+  // as many CTAs as run at once on 152 SMs: their registers hold two rows a thread
+  const int64_t most = 152 * (warp ? 2 : d <= 2048 ? std::max(2, 640 / row_threads(d, 1)) : d <= 8192 ? std::max(1, 512 / row_threads(d, 2)) : 1);
   return static_cast<int>(groups < most ? groups : most);
 }
 
@@ -532,16 +587,38 @@ cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, co
                       static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dh),
                       static_cast<__nv_bfloat16*>(dx),       d_weight ? part : nullptr, rows, d, eps};
   const int parts = rms_norm_bwd_parts(rows, d);
-  cudaError_t e = d <= 256    ? norm_bwd_launch<32, 1>(a, parts, s)
-                  : d <= 1024 ? norm_bwd_launch<128, 1>(a, parts, s)
-                  : d <= 2048 ? norm_bwd_launch<256, 1>(a, parts, s)
-                  : d <= 4096 ? norm_bwd_launch<256, 2>(a, parts, s)
-                  : d <= 8192 ? norm_bwd_launch<512, 2>(a, parts, s)
-                  : d <= 16384 ? norm_bwd_launch<1024, 2>(a, parts, s)
-                               : norm_bwd_launch<1024, 4>(a, parts, s);
+  const dim3 grid(parts);
+  cudaError_t e;
+  if (d <= 256)
+    e = launch_pdl(rms_norm_bwd_kernel<true, 1, 256>, grid, dim3(32 * kWarpRows), 0, s, a);
+  else if (d <= 512)
+    e = launch_pdl(rms_norm_bwd_kernel<true, 2, 256>, grid, dim3(32 * kWarpRows), 0, s, a);
+  else if (d <= 2048)
+    e = launch_pdl(rms_norm_bwd_kernel<false, 1, 256>, grid, dim3(row_threads(d, 1)), 0, s, a);
+  else if (d <= 8192)
+    e = launch_pdl(rms_norm_bwd_kernel<false, 2, 512>, grid, dim3(row_threads(d, 2)), 0, s, a);
+  else
+    e = launch_pdl(rms_norm_bwd_kernel<false, 4, 1024>, grid, dim3(row_threads(d, 4)), 0, s, a);
   if (e != cudaSuccess || !d_weight) return e;
-  return launch_pdl(norm_weight_grad_kernel, dim3((d + 31) / 32), dim3(kThreads), 0, s, static_cast<const float*>(part),
+  return launch_pdl(sum_parts_kernel, dim3((d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
                     static_cast<__nv_bfloat16*>(d_weight), parts, d);
+}
+
+int fp8_quantize_sum_parts(int64_t rows, int K) {
+  const int64_t nb = (K + 127) / 128, groups = (rows + 15) / 16;
+  const int64_t want = (152 * 8 + nb - 1) / nb;  // CTAs that run at once
+  return static_cast<int>(groups < want ? groups : want);
+}
+
+cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
+                                    int K, cudaStream_t s) {
+  const int nb = (K + 127) / 128, parts = fp8_quantize_sum_parts(rows, K);
+  cudaError_t e = launch_pdl(quant_rows_sum_kernel, dim3(nb, parts), dim3(kThreads), 0, s,
+                             static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(codes),
+                             static_cast<uint8_t*>(scales), part, rows, K, nb);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(sum_parts_kernel, dim3((K + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
+                    static_cast<__nv_bfloat16*>(sums), parts, K);
 }
 
 }  // namespace dg

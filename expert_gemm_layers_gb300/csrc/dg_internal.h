@@ -407,6 +407,12 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
                                   cudaStream_t s);
 
+// x [rows, K] to codes and scales of 1 x 128 blocks and sums [K] = column sums of x, read once;
+// part [fp8_quantize_sum_parts][K] binary32.
+int fp8_quantize_sum_parts(int64_t rows, int K);
+cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
+                                    int K, cudaStream_t s);
+
 // h = x + res (res NULL: h is x and not written); the norm of h into y, or into codes and scales where codes is given.
 cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
                             int64_t rows, int d, float eps, cudaStream_t s);

@@ -104,25 +104,32 @@ def fp8_linear(x, weight, bias: torch.Tensor | None = None, out: torch.Tensor | 
 
     x: activations in 8 bits (codes, scales), as fp8_quantize and rms_norm(..., fp8=True) return them, or bf16
     [..., in], which is quantised on the way.  weight: (codes, scales) of fp8_quantize(W [out, in], 128).  Sums in
-    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, its error block zeroed; default:
+    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, or dg_fp8_linear_bf16_workspace_bytes; its error block zeroed; default:
     this stream's own) is not shared by calls that run at the same time."""
-    if isinstance(x, torch.Tensor):
+    lib, plain = load(), isinstance(x, torch.Tensor)
+    if plain:
         index = _device(x, "x", BF16)
-        x = fp8_quantize(x)
+        _check(x, "x", BF16, x.shape, index)
+        xc = x
     else:
         index = _device(_pair(x, "x")[0], "x codes", E4M3)
-    lib, (xc, xs) = load(), _need_rows(x, "x", index)
+        xc, xs = _need_rows(x, "x", index)
     in_f = _size(xc, -1)
     wc, wscale = _need_weight(weight, "weight", in_f, index)
-    out_f, rows = _size(wc, 0), _rows(xc)
+    out_f, lead, rows = _size(wc, 0), xc.shape[:-1], _rows(xc)
     if bias is not None:
         _check(bias, "bias", BF16, (out_f,), index)
     if out is None:
-        out = torch.empty((*xc.shape[:-1], out_f), dtype=BF16, device=xc.device)
+        out = torch.empty((*lead, out_f), dtype=BF16, device=xc.device)
     else:
-        _check(out, "out", BF16, (*xc.shape[:-1], out_f), index)
-    _launch_with(workspace, lib.dg_fp8_linear_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear, index, rows, in_f,
-                 out_f, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), wscale.data_ptr(), _p(bias), out.data_ptr())
+        _check(out, "out", BF16, (*lead, out_f), index)
+    if plain:
+        _launch_with(workspace, lib.dg_fp8_linear_bf16_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear_bf16, index,
+                     rows, in_f, out_f, x.data_ptr(), wc.data_ptr(), wscale.data_ptr(), _p(bias), out.data_ptr())
+    else:
+        _launch_with(workspace, lib.dg_fp8_linear_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear, index, rows,
+                     in_f, out_f, xc.data_ptr(), xs.data_ptr(), wc.data_ptr(), wscale.data_ptr(), _p(bias),
+                     out.data_ptr())
     return out
 
 

@@ -517,6 +517,9 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
  * in_features % 16 == 0, out_features % 16 == 0; rows >= 0 (0 = nothing to do).
  * ws (dg_fp8_linear_workspace_bytes): the error block, then scratch; nothing in it outlives the call.
  *
+ * dg_fp8_linear_bf16: the same with activations x [rows, in_features] bf16, quantised on the way (dg_fp8_quantize with
+ * block_rows 1 into ws).
+ *
  * dg_fp8_linear_bwd: the gradients for dy [rows, out_features] bf16, given what the forward read (the activations
  * need not be kept in any other form):
  *   dx       [rows, in_features]   = q(dy) W, where q(dy) is dy through dg_fp8_quantize with block_rows 1
@@ -531,6 +534,12 @@ size_t dg_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t 
 dg_status dg_fp8_linear(int64_t rows, int64_t in_features, int64_t out_features, const void* x_codes,
                         const void* x_scales, const void* w_codes, const void* w_scales, const void* bias, void* y,
                         void* ws, size_t ws_bytes, void* stream);
+
+size_t dg_fp8_linear_bf16_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
+
+dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_features, int64_t out_features, const void* x,
+                             const void* w_codes, const void* w_scales, const void* bias, void* y, void* ws,
+                             size_t ws_bytes, void* stream);
 
 size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
 

@@ -60,6 +60,23 @@ def test_linear(lib, mem):
     assert lib.dg_fp8_linear_workspace_bytes(2, 136, 16) == 0 and lib.dg_fp8_linear_workspace_bytes(2, 128, 16) >= 256
 
 
+def test_linear_bf16(lib, mem):
+    ok = dict(rows=2, K=128, N=16, x=mem[0], wc=mem[2], ws=mem[3], b=mem[4], y=mem[5], w=mem[6], n=1 << 16)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return lib.dg_fp8_linear_bf16(*(a[k] for k in ("rows", "K", "N", "x", "wc", "ws", "b", "y", "w", "n")), None)
+
+    assert call(rows=-1) == INVALID and call(K=136) == INVALID and call(N=24) == INVALID
+    for name in ("x", "wc", "ws", "y"):
+        assert call(**{name: None}) == INVALID and b"NULL" in lib.dg_last_error()
+    assert call(y=ok["x"]) == INVALID and call(y=ok["w"]) == INVALID and call(w=None) == WORKSPACE
+    need = lib.dg_fp8_linear_bf16_workspace_bytes(2, 128, 16)
+    assert need >= 256 + 2 * 128 + 2 and call(n=need - 1) == WORKSPACE
+    assert lib.dg_fp8_linear_bf16_workspace_bytes(2, 136, 16) == 0
+    assert call(rows=0, x=None, wc=None, ws=None, b=None, y=None, w=None) == OK
+
+
 def test_linear_bwd(lib, mem):
     ok = dict(rows=2, K=128, N=16, xc=mem[0], xs=mem[1], wc=mem[2], ws=mem[3], dy=mem[4], dx=mem[5], dw=mem[6],
               db=mem[7], w=mem[8], n=1 << 16)
