@@ -56,9 +56,11 @@ dg_status check_norm(int64_t rows, int64_t d, float eps, const char* what) {
   return DG_OK;
 }
 
-// One block-scaled product D [M, N] = A [M, K] B^T (+ bias), B [N, K], or [K, N] where b_mn_major.
-dg_status run_mx(bool b_mn_major, int64_t M, int64_t N, int64_t K, const void* a, const void* sa, const void* b,
-                 const void* sb, const void* bias, void* d, const DeviceInfo& dev, cudaStream_t s, const char* name) {
+// One block-scaled product D [M, N] = A [M, K] B^T (+ bias), B [N, K], or [K, N] where b_mn_major.  sb are the scales of
+// B's 128 x 128 blocks, [N][K], or [K][N] where sb_turned.
+dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t K, const void* a, const void* sa,
+                 const void* b, const void* sb, const void* bias, void* d, const DeviceInfo& dev, cudaStream_t s,
+                 const char* name) {
   CUtensorMap ma, mb, md;
   dg_status st;
   const uint64_t m = M, n = N, k = K;
@@ -74,8 +76,8 @@ dg_status run_mx(bool b_mn_major, int64_t M, int64_t N, int64_t K, const void* a
   p.sa = static_cast<const uint8_t*>(sa);
   p.ka = static_cast<int32_t>(blocks128(K));
   p.sb = static_cast<const uint8_t*>(sb);
-  p.sb_n = b_mn_major ? 1 : p.ka;
-  p.sb_k = b_mn_major ? static_cast<int32_t>(blocks128(N)) : 1;
+  p.sb_n = sb_turned ? 1 : p.ka;
+  p.sb_k = sb_turned ? static_cast<int32_t>(blocks128(N)) : 1;
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.err = dev.err;
   const double w = static_cast<double>(N) * K;
@@ -102,19 +104,27 @@ dg_status run_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x, c
                      const void* sw, const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s) {
   const MxFewPlan few = mx_few_plan(rows, out_f, in_f, dev);
   if (few.better) return run_mx_few(few, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear_few");
-  return run_mx(false, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear");
+  return run_mx(false, false, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear");
 }
 
-// Workspace of the backward: the error block, dy in 8 bits, partial column sums, x in bf16.
+// Workspace of the backward: the error block, dy in 8 bits, partial column sums, the weight's codes turned, x in bf16.
+// With many rows the product for dx takes the weight's codes with the contraction along their rows: as they lie, a
+// CTA's 112 columns of a 224-column tile begin anywhere in a 128-byte line, and the copies cost 25 of 100 of its time
+// (8192 rows, 14336 to 4096: 349 us against 276); turning them costs 2 bytes of traffic a weight, which pays from about
+// 2000 rows on.
+constexpr int64_t kTurnRows = 2048;
 struct BwdLayout {
-  size_t dy_codes, dy_scales, sums, x, total;
+  size_t dy_codes, dy_scales, sums, w_turned, x, total;
+  bool turn;
 };
 BwdLayout bwd_layout(int64_t rows, int64_t in_f, int64_t out_f) {
   BwdLayout l;
   l.dy_codes = DG_ERROR_BLOCK_BYTES;
   l.dy_scales = round256(l.dy_codes + elements(rows, out_f));
   l.sums = round256(l.dy_scales + scale_bytes(rows, out_f, 1));
-  l.x = round256(l.sums + 4 * elements(fp8_quantize_sum_parts(rows, static_cast<int>(out_f)), out_f));
+  l.turn = rows >= kTurnRows && out_f <= 65535 * 128;
+  l.w_turned = round256(l.sums + 4 * elements(fp8_quantize_sum_parts(rows, static_cast<int>(out_f)), out_f));
+  l.x = round256(l.w_turned + (l.turn ? elements(out_f, in_f) : 0));
   l.total = round256(l.x + 2 * elements(rows, in_f));
   return l;
 }
@@ -271,7 +281,15 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
-    if ((st = run_mx(true, rows, in_f, out_f, base + l.dy_codes, base + l.dy_scales, w_codes, w_scales, nullptr, dx,
+    const void* b = w_codes;
+    if (l.turn) {
+      TraceScope trace("fp8_bwd_turn_w", s, 0.0, 2.0 * wn);
+      b = base + l.w_turned;
+      st = launched(launch_transpose_codes(w_codes, base + l.w_turned, static_cast<int>(out_f), static_cast<int>(in_f), s),
+                    "fp8_linear_bwd");
+      if (st != DG_OK) return st;
+    }
+    if ((st = run_mx(!l.turn, true, rows, in_f, out_f, base + l.dy_codes, base + l.dy_scales, b, w_scales, nullptr, dx,
                      dev, s, "fp8_linear_bwd_dx")) != DG_OK)
       return st;
   }
@@ -335,7 +353,7 @@ dg_status dg_rms_norm(int64_t rows, int64_t d, float eps, const void* x, const v
 
 size_t dg_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
   if (check_norm(rows, d, 1.0f, "rms_norm_bwd") != DG_OK) return 0;
-  return DG_ERROR_BLOCK_BYTES + elements(rms_norm_bwd_parts(rows, static_cast<int>(d)), d) * sizeof(float);
+  return DG_ERROR_BLOCK_BYTES + rms_norm_bwd_scratch_bytes(rows, static_cast<int>(d));
 }
 
 dg_status dg_rms_norm_bwd(int64_t rows, int64_t d, float eps, const void* h, const void* weight, const void* dy,
@@ -363,8 +381,7 @@ dg_status dg_rms_norm_bwd(int64_t rows, int64_t d, float eps, const void* h, con
   }
   TraceScope trace("rms_norm_bwd", s, 0.0, (dh ? 8.0 : 6.0) * n);
   return launched(launch_rms_norm_bwd(h, weight, dy, dh, dx, d_weight,
-                                      reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES), rows,
-                                      static_cast<int>(d), eps, s),
+                                      static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES, rows, static_cast<int>(d), eps, s),
                   "rms_norm_bwd");
 }
 

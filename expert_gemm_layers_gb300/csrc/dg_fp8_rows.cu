@@ -57,6 +57,12 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
     v[2 * i + 1] = f.y;
   }
 }
+__device__ __forceinline__ void unpack4x2(const uint4& u, float2 (&v)[4]) {
+  v[0] = unpack_bf16x2(u.x);
+  v[1] = unpack_bf16x2(u.y);
+  v[2] = unpack_bf16x2(u.z);
+  v[3] = unpack_bf16x2(u.w);
+}
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
@@ -118,17 +124,20 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat1
 
 // ------------------------------------------------------------------ quantise, blocks of 128 x 128
 
-// One CTA a block: 16 lanes across its columns, 16 rows at a time, all eight reads before the maximum.
-__global__ void __launch_bounds__(kThreads) quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
-                                                               uint8_t* __restrict__ scale, int64_t rows, int K, int nb) {
-  __shared__ uint32_t part[kThreads / 32];
+// One CTA takes kBlocks blocks side by side (256 bytes of each row apiece): 16 lanes across a block, 16 rows at a time,
+// all eight reads before the maximum.
+template <int kBlocks>
+__global__ void __launch_bounds__(256 * kBlocks) quant_tiles_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
+                                                                    uint8_t* __restrict__ scale, int64_t rows, int K, int nb) {
+  __shared__ uint32_t part[kBlocks][16];
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t tile = blockIdx.x;
-  const int64_t rb = tile / nb;
-  const int kb = static_cast<int>(tile - rb * nb);
-  const int c = kb * 128 + 8 * (threadIdx.x & 15);
-  const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
+  const int across = (nb + kBlocks - 1) / kBlocks;
+  const int64_t rb = blockIdx.x / across;
+  const int kb = kBlocks * static_cast<int>(blockIdx.x - rb * across);
+  const int at = threadIdx.x % (16 * kBlocks), row = threadIdx.x / (16 * kBlocks), side = at >> 4;
+  const int c = kb * 128 + 8 * at;
+  const int64_t r0 = rb * 128 + row;
   uint4 v[8];
   uint32_t m = 0u;
 #pragma unroll
@@ -138,11 +147,11 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(const __nv_bfloat
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, amax_bits8(v[i]));
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  m = max16(m);
+  if ((threadIdx.x & 15) == 0) part[side][row] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w]);
+  for (int w = 0; w < 16; ++w) m = max(m, part[side][w]);
   const uint32_t byte = scale_byte(m << 16);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -151,7 +160,47 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(const __nv_bfloat
     unpack8(v[i], f);
     if (r < rows && c < K) *reinterpret_cast<uint2*>(q + r * K + c) = codes8(f, byte);
   }
-  if (threadIdx.x == 0) scale[tile] = static_cast<uint8_t>(byte);
+  if (row == 0 && (at & 15) == 0 && kb + side < nb) scale[rb * nb + kb + side] = static_cast<uint8_t>(byte);
+}
+
+// ------------------------------------------------------------------ transpose of codes
+
+// out [K][rows] = in [rows][K], bytes, one 128 x 128 tile a CTA through shared memory (both sizes multiples of 16).  A
+// thread turns 4 x 4 bytes; its warp takes 8 such blocks down and 4 across, which with rows of 33 words are 32 banks.
+__global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t* __restrict__ in, uint8_t* __restrict__ out,
+                                                                   int rows, int K) {
+  __shared__ uint32_t tile[128][33];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (threadIdx.x >> 3) + 32 * i, c = 16 * (threadIdx.x & 7);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r0 + r < rows && c0 + c < K) v = __ldg(reinterpret_cast<const uint4*>(in + static_cast<int64_t>(r0 + r) * K + c0 + c));
+    uint32_t* t = &tile[r][c / 4];
+    t[0] = v.x;
+    t[1] = v.y;
+    t[2] = v.z;
+    t[3] = v.w;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // the tile's 32 x 32 blocks as 4 x 8 groups of 8 x 4; a warp takes four of the 32
+    const int group = warp * 4 + i, r4 = 8 * (group & 3) + (lane & 7), c4 = 4 * (group >> 2) + (lane >> 3);
+    const uint32_t a = tile[4 * r4][c4], b = tile[4 * r4 + 1][c4], c = tile[4 * r4 + 2][c4], d = tile[4 * r4 + 3][c4];
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    const uint32_t o[4] = {__byte_perm(ab0, cd0, 0x5410), __byte_perm(ab0, cd0, 0x7632), __byte_perm(ab1, cd1, 0x5410),
+                           __byte_perm(ab1, cd1, 0x7632)};
+    if (r0 + 4 * r4 < rows)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c0 + 4 * c4 + k < K)
+          *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(c0 + 4 * c4 + k) * rows + r0 + 4 * r4) = o[k];
+  }
 }
 
 // ------------------------------------------------------------------ dequantise
@@ -323,12 +372,12 @@ struct NormBwdArgs {
 };
 
 // Threads and chunks as in rms_norm_kernel; a CTA takes every gridDim.x-th row (or kWarpRows rows), the next one read
-// while this one is worked on (but for rows of over 8192 columns, whose 1024 threads have no registers for two).  The weight's gradient stays in registers over a thread's rows and leaves as one partial
+// while this one is worked on.  The weight's gradient stays in registers over a thread's rows and leaves as one partial
 // sum a CTA.
 template <bool kWarp, int C, int kMaxT>
-__global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(kMaxT, kWarp ? 2 : C == 1 ? 3 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
   __shared__ float part[2][32];
-  __shared__ float wsum[kWarp ? kWarpRows - 1 : 1][kWarp ? 32 * C * 8 : 1];
+  __shared__ float2 wsum[kWarp ? kWarpRows - 1 : 1][kWarp ? 32 * C * 4 : 1];
   const int T = kWarp ? 32 : blockDim.x;
   const int t = kWarp ? threadIdx.x & 31 : threadIdx.x;
   const int sub = kWarp ? threadIdx.x >> 5 : 0;
@@ -352,13 +401,15 @@ __global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArg
 #pragma unroll
   for (int i = 0; i < C; ++i)
     wv[i] = t + i * T < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
-  float dw[C][8] = {};
+  float2 dw[C][4];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dw[i][e] = make_float2(0.0f, 0.0f);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  constexpr bool kAhead = C < 4;
-  if (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * kRows + sub);
+  fetch(static_cast<int64_t>(blockIdx.x) * kRows + sub);
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
     const int64_t row = r0 + sub;
-    if (!kAhead) fetch(row);
     uint4 hc[C], yc[C], pc[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -366,58 +417,54 @@ __global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArg
       yc[i] = yv[i];
       pc[i] = pv[i];
     }
-    if (kAhead && r0 + step < a.rows) fetch(row + step);
-    float s[2] = {0.0f, 0.0f};  // sum h^2, sum (dy w) h
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      float h[8], y[8], g[8];
-      unpack8(hc[i], h);
-      unpack8(yc[i], y);
-      unpack8(wv[i], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s[0] = fmaf(h[e], h[e], s[0]);
-        s[1] = fmaf(y[e] * g[e], h[e], s[1]);
-      }
-    }
-    row_sum<kWarp, 2>(s, part);
-    float pre = 1.0f, rstd = 1.0f / sqrtf(s[0] / n + a.eps);
-    if (!(s[0] < __int_as_float(0x7f800000))) {
-      s[0] = s[1] = 0.0f;
+    if (r0 + step < a.rows) fetch(row + step);
+    // sum h^2 and sum (dy w) h, or with k = 2^-64 those of h k
+    auto sums = [&](float k, float (&s)[2]) {
+      float2 q = make_float2(0.0f, 0.0f), r = q;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        float h[8], y[8], g[8];
-        unpack8(hc[i], h);
-        unpack8(yc[i], y);
-        unpack8(wv[i], g);
+        float2 h[4], y[4], g[4];
+        unpack4x2(hc[i], h);
+        unpack4x2(yc[i], y);
+        unpack4x2(wv[i], g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float u = h[e] * kShrink;
-          s[0] = fmaf(u, u, s[0]);
-          s[1] = fmaf(y[e] * g[e], u, s[1]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = mul2(h[e], splat2(k));
+          q = fma2(u, u, q);
+          r = fma2(mul2(y[e], g[e]), u, r);
         }
       }
+      s[0] = q.x + q.y;
+      s[1] = r.x + r.y;
       row_sum<kWarp, 2>(s, part);
+    };
+    float s[2];
+    sums(1.0f, s);
+    float pre = 1.0f, rstd = 1.0f / sqrtf(s[0] / n + a.eps);
+    if (!(s[0] < __int_as_float(0x7f800000))) {
       pre = kShrink;
+      sums(pre, s);
       rstd = 1.0f / sqrtf(s[0] / n);
     }
     // with n_h = h pre rstd (the normalised row): dx = rstd pre (dy w - n_h mean(dy w n_h)) + dh
-    const float mean = s[1] * rstd / n;
-    const float out = rstd * pre;
+    const float2 mean = splat2(-s[1] * rstd / n), out = splat2(rstd * pre);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float h[8], y[8], g[8], p[8];
-      unpack8(hc[i], h);
-      unpack8(yc[i], y);
-      unpack8(wv[i], g);
-      unpack8(pc[i], p);
+      float2 h[4], y[4], g[4], p[4];
+      unpack4x2(hc[i], h);
+      unpack4x2(yc[i], y);
+      unpack4x2(wv[i], g);
+      unpack4x2(pc[i], p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float nh = h[e] * pre * rstd;
-        dw[i][e] = fmaf(y[e], nh, dw[i][e]);
-        p[e] = fmaf(out, fmaf(-nh, mean, y[e] * g[e]), p[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 nh = mul2(h[e], out);
+        dw[i][e] = fma2(y[e], nh, dw[i][e]);
+        p[e] = fma2(out, fma2(nh, mean, mul2(y[e], g[e])), p[e]);
       }
-      if (a.dx && row < a.rows && t + i * T < chunks) reinterpret_cast<uint4*>(a.dx + row * a.d)[t + i * T] = pack8(p);
+      if (a.dx && row < a.rows && t + i * T < chunks)
+        reinterpret_cast<uint4*>(a.dx + row * a.d)[t + i * T] =
+            make_uint4(pack_bf16x2(p[0].x, p[0].y), pack_bf16x2(p[1].x, p[1].y), pack_bf16x2(p[2].x, p[2].y),
+                       pack_bf16x2(p[3].x, p[3].y));
     }
   }
   if (!a.part) return;
@@ -426,7 +473,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArg
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wsum[sub - 1][(i * 8 + e) * 32 + t] = dw[i][e];
+        for (int e = 0; e < 4; ++e) wsum[sub - 1][(i * 4 + e) * 32 + t] = dw[i][e];
     __syncthreads();
     if (sub > 0) return;
 #pragma unroll
@@ -434,7 +481,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArg
 #pragma unroll
       for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] += wsum[k][(i * 8 + e) * 32 + t];
+        for (int e = 0; e < 4; ++e) dw[i][e] = add2(dw[i][e], wsum[k][(i * 4 + e) * 32 + t]);
   }
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
 #pragma unroll
@@ -442,9 +489,87 @@ __global__ void __launch_bounds__(kMaxT, 1) rms_norm_bwd_kernel(const NormBwdArg
     const int c = t + i * T;
     if (c >= chunks) continue;
     float4* o = reinterpret_cast<float4*>(out + 8 * c);
-    o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-    o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    o[0] = make_float4(dw[i][0].x, dw[i][0].y, dw[i][1].x, dw[i][1].y);
+    o[1] = make_float4(dw[i][2].x, dw[i][2].y, dw[i][3].x, dw[i][3].y);
   }
+}
+
+// The backward in two passes, for rows too long for a CTA's registers.  First, a CTA a row: k = 1 / sqrt(mean h^2 + eps)
+// and mean(dy w h) k.
+__global__ void __launch_bounds__(256) norm_bwd_rows_kernel(const NormBwdArgs a, float2* __restrict__ coef) {
+  __shared__ float part[2][32];
+  const int64_t row = blockIdx.x;
+  const int chunks = a.d / 8;
+  const float n = static_cast<float>(a.d);
+  griddep_wait();
+  griddep_launch_dependents();
+  float pre = 1.0f, rstd = 0.0f, s[2];
+  for (int pass = 0; pass < 2; ++pass) {
+    s[0] = s[1] = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < chunks; c += 256) {
+      float h[8], y[8], g[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(a.h + row * a.d) + c), h);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(a.dy + row * a.d) + c), y);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(a.w) + c), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float u = h[e] * pre;
+        s[0] = fmaf(u, u, s[0]);
+        s[1] = fmaf(y[e] * g[e], u, s[1]);
+      }
+    }
+    row_sum<false, 2>(s, part);
+    rstd = 1.0f / sqrtf(pre == 1.0f ? s[0] / n + a.eps : s[0] / n);
+    if (pre != 1.0f || s[0] < __int_as_float(0x7f800000)) break;
+    pre = kShrink;
+  }
+  if (threadIdx.x == 0) coef[row] = make_float2(rstd * pre, s[1] * rstd / n);
+}
+
+// Then, for 2048 columns a CTA over every gridDim.y-th row: dx, and the weight's gradient in registers.
+__global__ void __launch_bounds__(256) norm_bwd_apply_kernel(const NormBwdArgs a, const float2* __restrict__ coef) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = 8 * (blockIdx.x * 256 + threadIdx.x);
+  if (c >= a.d) return;
+  float g[8], dw[8] = {};
+  unpack8(__ldg(reinterpret_cast<const uint4*>(a.w + c)), g);
+  constexpr int kUnits = 4;  // rows in flight
+  const int64_t step = gridDim.y;
+  for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += kUnits * step) {
+    uint4 hv[kUnits], yv[kUnits], pv[kUnits];
+    float2 k[kUnits];
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int64_t r = r0 + i * step;
+      const bool in = r < a.rows;
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      hv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.h + r * a.d + c)) : z;
+      yv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.dy + r * a.d + c)) : z;
+      pv[i] = in && a.dh ? __ldcs(reinterpret_cast<const uint4*>(a.dh + r * a.d + c)) : z;
+      k[i] = in ? __ldg(coef + r) : make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int64_t r = r0 + i * step;
+      float h[8], y[8], p[8];
+      unpack8(hv[i], h);
+      unpack8(yv[i], y);
+      unpack8(pv[i], p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float nh = h[e] * k[i].x;
+        dw[e] = fmaf(y[e], nh, dw[e]);
+        p[e] = fmaf(k[i].x, fmaf(-nh, k[i].y, y[e] * g[e]), p[e]);
+      }
+      if (a.dx && r < a.rows) *reinterpret_cast<uint4*>(a.dx + r * a.d + c) = pack8(p);
+    }
+  }
+  if (!a.part) return;
+  float4* o = reinterpret_cast<float4*>(a.part + static_cast<int64_t>(blockIdx.y) * a.d + c);
+  o[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+  o[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
 }
 
 // out[c] = sum over `parts` partial sums part[k][c], in an order that the sizes fix: 32 columns a CTA, the partial sums
@@ -552,8 +677,14 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
     return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb)
                         : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb);
   }
-  const int64_t tiles = (rows + 127) / 128 * nb;
-  return launch_pdl(quant_tiles_kernel, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, s, xp, q, sc, rows, K, nb);
+  // Two blocks a CTA where there are many (28672 x 4096, with 7168: 58 us against 62), one where not (1003 x 2064: 2.5
+  // us against 3.4; 8192 x 4096, 2048: 16.8 against 18.5).
+  const int64_t row_blocks = (rows + 127) / 128;
+  if (row_blocks * nb >= 4096)
+    return launch_pdl(quant_tiles_kernel<2>, dim3(static_cast<unsigned>(row_blocks * ((nb + 1) / 2))), dim3(512), 0, s, xp, q,
+                      sc, rows, K, nb);
+  return launch_pdl(quant_tiles_kernel<1>, dim3(static_cast<unsigned>(row_blocks * nb)), dim3(256), 0, s, xp, q, sc, rows, K,
+                    nb);
 }
 
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
@@ -565,6 +696,11 @@ cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x
                     rows, K, nb, block_rows == 1 ? 0 : 7, spans);
 }
 
+cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s) {
+  return launch_pdl(transpose_codes_kernel, dim3((K + 127) / 128, (rows + 127) / 128), dim3(kThreads), 0, s,
+                    static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, K);
+}
+
 cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
                             int64_t rows, int d, float eps, cudaStream_t s) {
   const NormArgs a{static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(res),
@@ -573,32 +709,53 @@ cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void*
   return codes ? norm_launch<true>(a, s) : norm_launch<false>(a, s);
 }
 
+namespace {
+
+// One pass up to 8192 columns; beyond, two (2048 x 16384: 280 us in one with spilled registers, 65 us in two).
+bool norm_bwd_one_pass(int d) { return d <= 8192; }
+
+}  // namespace
+
 int rms_norm_bwd_parts(int64_t rows, int d) {
+  if (!norm_bwd_one_pass(d)) {
+    const int64_t across = (d + 2047) / 2048, want = (152 * 4 + across - 1) / across;
+    return static_cast<int>(rows < want ? rows : want);
+  }
+  // as many CTAs as run at once on 152 SMs: 24 warps of 80 registers a thread with one chunk, 16 of 128 with two
+  // (8192 x 1280: 26 us with a part of the CTAs left for a second turn, 16 us)
   const bool warp = d <= 512;
   const int64_t groups = warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
-  // as many CTAs as run at once on 152 SMs: their registers hold two rows a thread
-  const int64_t most = 152 * (warp ? 2 : d <= 2048 ? std::max(2, 640 / row_threads(d, 1)) : d <= 8192 ? std::max(1, 512 / row_threads(d, 2)) : 1);
+  const int64_t most = 152 * (warp ? 2 : d <= 2048 ? 768 / row_threads(d, 1) : 512 / row_threads(d, 2));
   return static_cast<int>(groups < most ? groups : most);
 }
 
+size_t rms_norm_bwd_scratch_bytes(int64_t rows, int d) {
+  const size_t coef = norm_bwd_one_pass(d) ? 0 : (static_cast<size_t>(rows) * sizeof(float2) + 255) / 256 * 256;
+  return coef + static_cast<size_t>(rms_norm_bwd_parts(rows, d)) * d * sizeof(float);
+}
+
 cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, const void* dh, void* dx, void* d_weight,
-                                float* part, int64_t rows, int d, float eps, cudaStream_t s) {
+                                void* scratch, int64_t rows, int d, float eps, cudaStream_t s) {
+  const int parts = rms_norm_bwd_parts(rows, d);
+  const size_t coef_bytes = rms_norm_bwd_scratch_bytes(rows, d) - static_cast<size_t>(parts) * d * sizeof(float);
+  float2* coef = static_cast<float2*>(scratch);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + coef_bytes);
   const NormBwdArgs a{static_cast<const __nv_bfloat16*>(h),  static_cast<const __nv_bfloat16*>(w),
                       static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dh),
                       static_cast<__nv_bfloat16*>(dx),       d_weight ? part : nullptr, rows, d, eps};
-  const int parts = rms_norm_bwd_parts(rows, d);
-  const dim3 grid(parts);
   cudaError_t e;
-  if (d <= 256)
-    e = launch_pdl(rms_norm_bwd_kernel<true, 1, 256>, grid, dim3(32 * kWarpRows), 0, s, a);
+  if (!norm_bwd_one_pass(d)) {
+    e = launch_pdl(norm_bwd_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a, coef);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(norm_bwd_apply_kernel, dim3((d + 2047) / 2048, parts), dim3(256), 0, s, a, static_cast<const float2*>(coef));
+  } else if (d <= 256)
+    e = launch_pdl(rms_norm_bwd_kernel<true, 1, 256>, dim3(parts), dim3(32 * kWarpRows), 0, s, a);
   else if (d <= 512)
-    e = launch_pdl(rms_norm_bwd_kernel<true, 2, 256>, grid, dim3(32 * kWarpRows), 0, s, a);
+    e = launch_pdl(rms_norm_bwd_kernel<true, 2, 256>, dim3(parts), dim3(32 * kWarpRows), 0, s, a);
   else if (d <= 2048)
-    e = launch_pdl(rms_norm_bwd_kernel<false, 1, 256>, grid, dim3(row_threads(d, 1)), 0, s, a);
-  else if (d <= 8192)
-    e = launch_pdl(rms_norm_bwd_kernel<false, 2, 512>, grid, dim3(row_threads(d, 2)), 0, s, a);
+    e = launch_pdl(rms_norm_bwd_kernel<false, 1, 256>, dim3(parts), dim3(row_threads(d, 1)), 0, s, a);
   else
-    e = launch_pdl(rms_norm_bwd_kernel<false, 4, 1024>, grid, dim3(row_threads(d, 4)), 0, s, a);
+    e = launch_pdl(rms_norm_bwd_kernel<false, 2, 512>, dim3(parts), dim3(row_threads(d, 2)), 0, s, a);
   if (e != cudaSuccess || !d_weight) return e;
   return launch_pdl(sum_parts_kernel, dim3((d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
                     static_cast<__nv_bfloat16*>(d_weight), parts, d);

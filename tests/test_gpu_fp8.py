@@ -168,7 +168,7 @@ def test_tiny_and_huge_scales():
 
 
 @pytest.mark.parametrize("rows,K,N", [(1, 16, 16), (2, 128, 240), (17, 528, 464), (100, 1296, 2064), (129, 256, 512),
-                                      (257, 384, 688), (1000, 272, 1296), (640, 2048, 224)])
+                                      (257, 384, 688), (1000, 272, 1296), (640, 2048, 224), (2048, 144, 272), (2100, 528, 400)])
 def test_linear_backward(rows, K, N):
     (x8, x), (w8, w) = held(spread(rows, K, rows)), held(randn((N, K), N, K**-0.5), 128)
     dy = spread(rows, N, 9)
