@@ -150,7 +150,7 @@ dg_status dg_fp8_quantize(int64_t rows, int64_t K, int32_t block_rows, const voi
   if ((st = device_info(&dev)) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope trace("fp8_quantize", s, 0.0, 3.0 * n);
-  return launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(K), block_rows, s), "fp8_quantize");
+  return launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(K), block_rows, nullptr, s), "fp8_quantize");
 }
 
 dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const void* codes, const void* scales,
@@ -166,7 +166,7 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
   if ((st = device_info(&dev)) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope trace("fp8_dequantize", s, 0.0, 3.0 * n);
-  return launched(launch_fp8_dequantize(codes, scales, x, rows, static_cast<int>(K), block_rows, s), "fp8_dequantize");
+  return launched(launch_fp8_dequantize(codes, scales, x, rows, static_cast<int>(K), block_rows, nullptr, s), "fp8_dequantize");
 }
 
 // Where the activations come in bf16, their codes and scales lie in the workspace behind the error block.
@@ -201,7 +201,7 @@ dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_f, int64_t out_f, const vo
   uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at;
   {
     TraceScope trace("fp8_quantize", s, 0.0, 3.0 * elements(rows, in_f));
-    st = launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(in_f), 1, s), "fp8_linear_bf16");
+    st = launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(in_f), 1, dev.err, s), "fp8_linear_bf16");
     if (st != DG_OK) return st;
   }
   return run_linear(rows, in_f, out_f, codes, scales, w_codes, w_scales, bias, y, dev, s);
@@ -276,8 +276,8 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
       TraceScope trace("fp8_bwd_quantize_dy", s, 0.0, 3.0 * yn);
       const int K = static_cast<int>(out_f);
       st = launched(d_bias ? launch_fp8_quantize_sum(dy, base + l.dy_codes, base + l.dy_scales, d_bias,
-                                                     reinterpret_cast<float*>(base + l.sums), rows, K, s)
-                           : launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, K, 1, s),
+                                                     reinterpret_cast<float*>(base + l.sums), rows, K, dev.err, s)
+                           : launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, K, 1, dev.err, s),
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
@@ -285,7 +285,8 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
     if (l.turn) {
       TraceScope trace("fp8_bwd_turn_w", s, 0.0, 2.0 * wn);
       b = base + l.w_turned;
-      st = launched(launch_transpose_codes(w_codes, base + l.w_turned, static_cast<int>(out_f), static_cast<int>(in_f), s),
+      st = launched(launch_transpose_codes(w_codes, base + l.w_turned, static_cast<int>(out_f), static_cast<int>(in_f),
+                                           dev.err, s),
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
@@ -298,7 +299,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
     uint8_t* x = base + l.x;
     {
       TraceScope trace("fp8_bwd_expand_x", s, 0.0, 3.0 * xn);
-      st = launched(launch_fp8_dequantize(x_codes, x_scales, x, rows, static_cast<int>(in_f), 1, s), "fp8_linear_bwd");
+      st = launched(launch_fp8_dequantize(x_codes, x_scales, x, rows, static_cast<int>(in_f), 1, dev.err, s), "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
     const uint64_t R = rows, I = in_f, O = out_f;
@@ -381,7 +382,8 @@ dg_status dg_rms_norm_bwd(int64_t rows, int64_t d, float eps, const void* h, con
   }
   TraceScope trace("rms_norm_bwd", s, 0.0, (dh ? 8.0 : 6.0) * n);
   return launched(launch_rms_norm_bwd(h, weight, dy, dh, dx, d_weight,
-                                      static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES, rows, static_cast<int>(d), eps, s),
+                                      static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES, rows, static_cast<int>(d), eps, dev.err,
+                                      s),
                   "rms_norm_bwd");
 }
 

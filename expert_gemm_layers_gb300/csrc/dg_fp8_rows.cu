@@ -83,15 +83,21 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 constexpr int kThreads = 256;
 
+// The kernels take the error word of their call's workspace (NULL for calls without one): after a recorded failure they
+// write nothing.  It is asked for with the first data and looked at before the first store.
+__device__ __forceinline__ uint32_t error_word(const uint32_t* err) { return err ? ld_volatile_u32(err) : 0u; }
+
 // ------------------------------------------------------------------ quantise, blocks of 1 x 128
 
 // Half a warp takes a block of 128 columns, eight columns a lane, kQuantUnits blocks in flight.
 constexpr int kQuantUnits = 4;
 template <bool kWhole>  // whole: K is a multiple of 128, blocks lie one after another
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
-                                                              uint8_t* __restrict__ scale, int64_t blocks, int K, int nb) {
+                                                              uint8_t* __restrict__ scale, int64_t blocks, int K, int nb,
+                                                              const uint32_t* err) {
   griddep_wait();
   griddep_launch_dependents();
+  const uint32_t failed = error_word(err);
   const int sub = threadIdx.x & 15;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kQuantUnits * kThreads + threadIdx.x) >> 4;
   uint4 v[kQuantUnits];
@@ -111,6 +117,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat1
     }
     v[i] = in[i] ? __ldcs(reinterpret_cast<const uint4*>(x + at[i])) : make_uint4(0u, 0u, 0u, 0u);
   }
+  if (failed) return;
 #pragma unroll
   for (int i = 0; i < kQuantUnits; ++i) {
     const int64_t b = first + i * (kThreads / 16);
@@ -168,10 +175,11 @@ __global__ void __launch_bounds__(256 * kBlocks) quant_tiles_kernel(const __nv_b
 // out [K][rows] = in [rows][K], bytes, one 128 x 128 tile a CTA through shared memory (both sizes multiples of 16).  A
 // thread turns 4 x 4 bytes; its warp takes 8 such blocks down and 4 across, which with rows of 33 words are 32 banks.
 __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t* __restrict__ in, uint8_t* __restrict__ out,
-                                                                   int rows, int K) {
+                                                                   int rows, int K, const uint32_t* err) {
   __shared__ uint32_t tile[128][33];
   griddep_wait();
   griddep_launch_dependents();
+  const uint32_t failed = error_word(err);
   const int r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -185,6 +193,7 @@ __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t
     t[3] = v.w;
   }
   __syncthreads();
+  if (failed) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -209,9 +218,10 @@ __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t
 constexpr int kDeqUnits = 4;
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                            __nv_bfloat16* __restrict__ x, int64_t rows, int K, int nb,
-                                                           int row_shift, int spans) {
+                                                           int row_shift, int spans, const uint32_t* err) {
   griddep_wait();
   griddep_launch_dependents();
+  const uint32_t failed = error_word(err);
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int64_t row = w / spans;
   if (row >= rows) return;
@@ -229,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __rest
       s[i] = scale_value(__ldg(srow + (c >> 7)));
     }
   }
+  if (failed) return;
 #pragma unroll
   for (int i = 0; i < kDeqUnits; ++i) {
     const int c = c0 + 256 * i;
@@ -369,6 +380,7 @@ struct NormBwdArgs {
   int64_t rows;
   int d;
   float eps;
+  const uint32_t* err;
 };
 
 // Threads and chunks as in rms_norm_kernel; a CTA takes every gridDim.x-th row (or kWarpRows rows), the next one read
@@ -386,6 +398,7 @@ __global__ void __launch_bounds__(kMaxT, kWarp ? 2 : C == 1 ? 3 : 1) rms_norm_bw
   const float n = static_cast<float>(a.d);
   griddep_wait();
   griddep_launch_dependents();
+  const uint32_t failed = error_word(a.err);
   uint4 wv[C], hv[C], yv[C], pv[C];
   auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -408,6 +421,7 @@ __global__ void __launch_bounds__(kMaxT, kWarp ? 2 : C == 1 ? 3 : 1) rms_norm_bw
     for (int e = 0; e < 4; ++e) dw[i][e] = make_float2(0.0f, 0.0f);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
   fetch(static_cast<int64_t>(blockIdx.x) * kRows + sub);
+  if (failed) return;
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
     const int64_t row = r0 + sub;
     uint4 hc[C], yc[C], pc[C];
@@ -524,7 +538,7 @@ __global__ void __launch_bounds__(256) norm_bwd_rows_kernel(const NormBwdArgs a,
     if (pre != 1.0f || s[0] < __int_as_float(0x7f800000)) break;
     pre = kShrink;
   }
-  if (threadIdx.x == 0) coef[row] = make_float2(rstd * pre, s[1] * rstd / n);
+  if (threadIdx.x == 0 && !error_word(a.err)) coef[row] = make_float2(rstd * pre, s[1] * rstd / n);
 }
 
 // Then, for 2048 columns a CTA over every gridDim.y-th row: dx, and the weight's gradient in registers.
@@ -532,7 +546,7 @@ __global__ void __launch_bounds__(256) norm_bwd_apply_kernel(const NormBwdArgs a
   griddep_wait();
   griddep_launch_dependents();
   const int c = 8 * (blockIdx.x * 256 + threadIdx.x);
-  if (c >= a.d) return;
+  if (c >= a.d || error_word(a.err)) return;
   float g[8], dw[8] = {};
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.w + c)), g);
   constexpr int kUnits = 4;  // rows in flight
@@ -575,10 +589,11 @@ __global__ void __launch_bounds__(256) norm_bwd_apply_kernel(const NormBwdArgs a
 // out[c] = sum over `parts` partial sums part[k][c], in an order that the sizes fix: 32 columns a CTA, the partial sums
 // spread over its 32 warps, four loads in flight each.
 __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ out,
-                                                         int parts, int d) {
+                                                         int parts, int d, const uint32_t* err) {
   __shared__ float s[32][33];
   griddep_wait();
   griddep_launch_dependents();
+  const uint32_t failed = error_word(err);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
   const int col = blockIdx.x * 32 + warp;
-  if (lane == 0 && col < d) out[col] = __float2bfloat16_rn(r);
+  if (lane == 0 && col < d && !failed) out[col] = __float2bfloat16_rn(r);
 }
 
 // ------------------------------------------------------------------ quantise a gradient and sum its columns
@@ -608,10 +623,11 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 // the column sums of what it reads stay in registers: part[blockIdx.y][column].
 __global__ void __launch_bounds__(kThreads) quant_rows_sum_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
                                                                   uint8_t* __restrict__ scale, float* __restrict__ part,
-                                                                  int64_t rows, int K, int nb) {
+                                                                  int64_t rows, int K, int nb, const uint32_t* err) {
   __shared__ float s[kThreads / 16][128 + 4];
   griddep_wait();
   griddep_launch_dependents();
+  if (error_word(err)) return;
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int c = blockIdx.x * 128 + 8 * sub;
   float sum[8] = {};
@@ -666,7 +682,7 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
-                                cudaStream_t s) {
+                                const uint32_t* err, cudaStream_t s) {
   const int nb = (K + 127) / 128;
   auto* xp = static_cast<const __nv_bfloat16*>(x);
   auto* q = static_cast<uint8_t*>(codes);
@@ -674,8 +690,8 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
   if (block_rows == 1) {
     const int64_t blocks = rows * nb, per = kThreads / 16 * kQuantUnits;
     const dim3 grid(static_cast<unsigned>((blocks + per - 1) / per));
-    return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb)
-                        : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb);
+    return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb, err)
+                        : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb, err);
   }
   // Two blocks a CTA where there are many (28672 x 4096, with 7168: 58 us against 62), one where not (1003 x 2064: 2.5
   // us against 3.4; 8192 x 4096, 2048: 16.8 against 18.5).
@@ -688,17 +704,17 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
 }
 
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
-                                  cudaStream_t s) {
+                                  const uint32_t* err, cudaStream_t s) {
   const int nb = (K + 127) / 128, spans = (K + 256 * kDeqUnits - 1) / (256 * kDeqUnits);
   const int64_t warps = rows * spans;
   return launch_pdl(dequant_kernel, dim3(static_cast<unsigned>((warps * 32 + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
                     static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), static_cast<__nv_bfloat16*>(x),
-                    rows, K, nb, block_rows == 1 ? 0 : 7, spans);
+                    rows, K, nb, block_rows == 1 ? 0 : 7, spans, err);
 }
 
-cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s) {
+cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, const uint32_t* err, cudaStream_t s) {
   return launch_pdl(transpose_codes_kernel, dim3((K + 127) / 128, (rows + 127) / 128), dim3(kThreads), 0, s,
-                    static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, K);
+                    static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, K, err);
 }
 
 cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
@@ -735,14 +751,14 @@ size_t rms_norm_bwd_scratch_bytes(int64_t rows, int d) {
 }
 
 cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, const void* dh, void* dx, void* d_weight,
-                                void* scratch, int64_t rows, int d, float eps, cudaStream_t s) {
+                                void* scratch, int64_t rows, int d, float eps, const uint32_t* err, cudaStream_t s) {
   const int parts = rms_norm_bwd_parts(rows, d);
   const size_t coef_bytes = rms_norm_bwd_scratch_bytes(rows, d) - static_cast<size_t>(parts) * d * sizeof(float);
   float2* coef = static_cast<float2*>(scratch);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + coef_bytes);
   const NormBwdArgs a{static_cast<const __nv_bfloat16*>(h),  static_cast<const __nv_bfloat16*>(w),
                       static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(dh),
-                      static_cast<__nv_bfloat16*>(dx),       d_weight ? part : nullptr, rows, d, eps};
+                      static_cast<__nv_bfloat16*>(dx),       d_weight ? part : nullptr, rows, d, eps, err};
   cudaError_t e;
   if (!norm_bwd_one_pass(d)) {
     e = launch_pdl(norm_bwd_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, a, coef);
@@ -758,7 +774,7 @@ cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, co
     e = launch_pdl(rms_norm_bwd_kernel<false, 2, 512>, dim3(parts), dim3(row_threads(d, 2)), 0, s, a);
   if (e != cudaSuccess || !d_weight) return e;
   return launch_pdl(sum_parts_kernel, dim3((d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
-                    static_cast<__nv_bfloat16*>(d_weight), parts, d);
+                    static_cast<__nv_bfloat16*>(d_weight), parts, d, err);
 }
 
 int fp8_quantize_sum_parts(int64_t rows, int K) {
@@ -768,14 +784,14 @@ int fp8_quantize_sum_parts(int64_t rows, int K) {
 }
 
 cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
-                                    int K, cudaStream_t s) {
+                                    int K, const uint32_t* err, cudaStream_t s) {
   const int nb = (K + 127) / 128, parts = fp8_quantize_sum_parts(rows, K);
   cudaError_t e = launch_pdl(quant_rows_sum_kernel, dim3(nb, parts), dim3(kThreads), 0, s,
                              static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(codes),
-                             static_cast<uint8_t*>(scales), part, rows, K, nb);
+                             static_cast<uint8_t*>(scales), part, rows, K, nb, err);
   if (e != cudaSuccess) return e;
   return launch_pdl(sum_parts_kernel, dim3((K + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
-                    static_cast<__nv_bfloat16*>(sums), parts, K);
+                    static_cast<__nv_bfloat16*>(sums), parts, K, err);
 }
 
 }  // namespace dg

@@ -402,19 +402,20 @@ cudaError_t smem_limit_once(const void* kern, int bytes, int dev);
 // ---------------------------------------------------------------- block-scaled e4m3 (dg_fp8_rows.cu, dg_mx_gemm.cu)
 
 // x [rows, K] bf16 <-> codes [rows, K] and scales [ceil(rows / block_rows), ceil(K / 128)]; block_rows 1 or 128.
+// err here and below: the error word of the call's workspace, or NULL.
 cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
-                                cudaStream_t s);
+                                const uint32_t* err, cudaStream_t s);
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
-                                  cudaStream_t s);
+                                  const uint32_t* err, cudaStream_t s);
 
 // Codes [rows, K] -> [K, rows]; rows and K multiples of 16, rows <= 65535 * 128.
-cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s);
+cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, const uint32_t* err, cudaStream_t s);
 
 // x [rows, K] to codes and scales of 1 x 128 blocks and sums [K] = column sums of x, read once;
 // part [fp8_quantize_sum_parts][K] binary32.
 int fp8_quantize_sum_parts(int64_t rows, int K);
 cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
-                                    int K, cudaStream_t s);
+                                    int K, const uint32_t* err, cudaStream_t s);
 
 // h = x + res (res NULL: h is x and not written); the norm of h into y, or into codes and scales where codes is given.
 cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
@@ -422,7 +423,7 @@ cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void*
 // scratch of rms_norm_bwd_scratch_bytes, 16-byte aligned; d_weight, dx and dh may be NULL.
 size_t rms_norm_bwd_scratch_bytes(int64_t rows, int d);
 cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, const void* dh, void* dx, void* d_weight,
-                                void* scratch, int64_t rows, int d, float eps, cudaStream_t s);
+                                void* scratch, int64_t rows, int d, float eps, const uint32_t* err, cudaStream_t s);
 
 // One launch of the block-scaled GEMM (dg_mx.cuh); p.tiles_* and p.n_fastest are filled in.  Box heights of the maps:
 // A 128 rows, a K-major B kMxTileN / 2 rows, an MN-major B 128 columns by 128 rows, D 32 columns by 32 rows.

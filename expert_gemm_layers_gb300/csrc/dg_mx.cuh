@@ -165,7 +165,7 @@ struct ScaleFeed {
     if (wide) {
       uint4 q = make_uint4(kScaleOnes, kScaleOnes, kScaleOnes, kScaleOnes);
       if (tid < kRows && row0 + tid < rows)
-        q = __ldg(reinterpret_cast<const uint4*>(sa + static_cast<int64_t>(row0 + tid) * ka + kb));
+        q = __ldcg(reinterpret_cast<const uint4*>(sa + static_cast<int64_t>(row0 + tid) * ka + kb));
       v[0] = q.x;
       v[1] = q.y;
       v[2] = q.z;
@@ -174,11 +174,11 @@ struct ScaleFeed {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int r = row0 + warp * (kRows / 4) + 2 * i + (lane >> 4), k = kb + (lane & 15);
-        v[i] = r < rows && k < kend ? __ldg(sa + static_cast<int64_t>(r) * ka + k) : 127u;
+        v[i] = r < rows && k < kend ? __ldcg(sa + static_cast<int64_t>(r) * ka + k) : 127u;
       }
     }
     const int k = kb + lane;
-    w = warp < kBlocks && lane < 16 && block0 + warp < blocks && k < kend ? __ldg(sb + (block0 + warp) * sb_n + k * sb_k)
+    w = warp < kBlocks && lane < 16 && block0 + warp < blocks && k < kend ? __ldcg(sb + (block0 + warp) * sb_n + k * sb_k)
                                                                          : 127u;
   }
   __device__ __forceinline__ void publish(int half) {
