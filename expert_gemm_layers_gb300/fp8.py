@@ -57,6 +57,17 @@ def _rows(t) -> int:
     return t.numel() // t.shape[-1] if t.dim() and t.shape[-1] else 0
 
 
+def _activations(x, name: str) -> tuple:
+    """Checks a contiguous bf16 CUDA tensor [..., d]; returns (device index, leading sizes, rows, d)."""
+    index = _device(x, name, BF16)
+    if x.dtype is not BF16 or not x.is_contiguous() or not x.dim():
+        _check(x, name, BF16, x.shape, index)
+        raise ValueError(f"{name} must have a last dimension")
+    shape = x.shape
+    d = shape[-1]
+    return index, shape[:-1], x.numel() // d if d else 0, d
+
+
 # ------------------------------------------------------------------ the format
 
 def fp8_quantize(x: torch.Tensor, block_rows: int = 1):
@@ -65,12 +76,11 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1):
 
     A scale is the least power of two (from 2^-124) for which no code exceeds 448, 1 for a block of zeros; a block
     with a NaN or an infinity becomes NaN."""
-    index = _device(x, "x", BF16)
-    _check(x, "x", BF16, x.shape, index)
-    if block_rows not in (1, 128) or x.dim() < 1 or (block_rows == 128 and x.dim() != 2):
-        raise ValueError(f"block_rows must be 1, or 128 with x [N, K]; got {block_rows} with shape {tuple(x.shape)}")
-    K, rows = x.shape[-1], _rows(x)
-    lead = x.shape[:-1] if block_rows == 1 else (_blocks(rows),)
+    index, lead, rows, K = _activations(x, "x")
+    if block_rows != 1:
+        if block_rows != 128 or x.dim() != 2:
+            raise ValueError(f"block_rows must be 1, or 128 with x [N, K]; got {block_rows} with shape {tuple(x.shape)}")
+        lead = (_blocks(rows),)
     codes = torch.empty(x.shape, dtype=E4M3, device=x.device)
     scales = torch.empty((*lead, _blocks(K)), dtype=E8M0, device=x.device)
     _launch(load().dg_fp8_quantize, index, rows, K, block_rows, x.data_ptr(), codes.data_ptr(), scales.data_ptr())
@@ -108,15 +118,14 @@ def fp8_linear(x, weight, bias: torch.Tensor | None = None, out: torch.Tensor | 
     this stream's own) is not shared by calls that run at the same time."""
     lib, plain = load(), isinstance(x, torch.Tensor)
     if plain:
-        index = _device(x, "x", BF16)
-        _check(x, "x", BF16, x.shape, index)
+        index, lead, rows, in_f = _activations(x, "x")
         xc = x
     else:
         index = _device(_pair(x, "x")[0], "x codes", E4M3)
         xc, xs = _need_rows(x, "x", index)
-    in_f = _size(xc, -1)
+        lead, rows, in_f = xc.shape[:-1], _rows(xc), _size(xc, -1)
     wc, wscale = _need_weight(weight, "weight", in_f, index)
-    out_f, lead, rows = _size(wc, 0), xc.shape[:-1], _rows(xc)
+    out_f = wc.shape[0]
     if bias is not None:
         _check(bias, "bias", BF16, (out_f,), index)
     if out is None:
@@ -140,9 +149,7 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
     "x" = q(dy) W, where q(dy) is dy through fp8_quantize, "weight" = dy^T x (dy as it is), "bias" = column sums of
     dy; bf16, None where not needed.  x or weight may be None where its product is not needed (then the other gives
     the sizes)."""
-    lib, index = load(), _device(dy, "dy", BF16)
-    _check(dy, "dy", BF16, dy.shape, index)
-    out_f, lead, rows = _size(dy, -1), dy.shape[:-1], _rows(dy)
+    lib, (index, lead, rows, out_f) = load(), _activations(dy, "dy")
     xc = xs = wc = ws = None
     if x is None and (need_dw or weight is None) or weight is None and need_dx:
         raise ValueError("x is needed for the weight's gradient, weight for that of x")
@@ -197,9 +204,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     y is bf16, or with fp8 activations in 8 bits (codes, scales) for fp8_linear, from the binary32 values.  Returns y,
     or (y, h) where a residual is given.  x, residual [..., d], weight [d] bf16; d % 8 == 0 (16 with fp8),
     d <= 32768, eps >= 1e-30."""
-    index = _device(x, "x", BF16)
-    _check(x, "x", BF16, x.shape, index)
-    d = _size(x, -1)
+    index, lead, rows, d = _activations(x, "x")
     _check(weight, "weight", BF16, (d,), index)
     h = y = codes = scales = None
     if residual is not None:
@@ -207,10 +212,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
         h = torch.empty_like(x)
     if fp8:
         codes = torch.empty(x.shape, dtype=E4M3, device=x.device)
-        scales = torch.empty((*x.shape[:-1], _blocks(d)), dtype=E8M0, device=x.device)
+        scales = torch.empty((*lead, _blocks(d)), dtype=E8M0, device=x.device)
     else:
         y = torch.empty_like(x)
-    _launch(load().dg_rms_norm, index, _rows(x), d, eps, x.data_ptr(), _p(residual), weight.data_ptr(), _p(h), _p(y),
+    _launch(load().dg_rms_norm, index, rows, d, eps, x.data_ptr(), _p(residual), weight.data_ptr(), _p(h), _p(y),
             _p(codes), _p(scales))
     y = (codes, scales) if fp8 else y
     return y if residual is None else (y, h)
@@ -221,9 +226,7 @@ def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, d
                       workspace: torch.Tensor | None = None) -> dict:
     """Gradients of rms_norm from h (x, where there was no residual), dy and, if h had other uses, their gradient dh:
     "x" (also the residual's) and "weight", bf16."""
-    lib, index = load(), _device(h, "h", BF16)
-    _check(h, "h", BF16, h.shape, index)
-    d, rows = _size(h, -1), _rows(h)
+    lib, (index, _, rows, d) = load(), _activations(h, "h")
     _check(weight, "weight", BF16, (d,), index)
     _check(dy, "dy", BF16, h.shape, index)
     if dh is not None:

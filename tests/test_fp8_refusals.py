@@ -140,6 +140,13 @@ def test_wrappers_refuse_before_the_device():
             call()
     with pytest.raises(TypeError):
         dg.fp8_quantize(x.float())
+    for other in (None, 3, "x"):
+        with pytest.raises(TypeError):
+            dg.fp8_quantize(other)
+        with pytest.raises(TypeError):
+            dg.rms_norm(other, x)
+        with pytest.raises(TypeError):
+            dg.fp8_linear(other, pair)
     with pytest.raises(TypeError):
         dg.fp8_linear(pair[0], pair)
     with pytest.raises(TypeError, match="codes, scales"):
