@@ -95,7 +95,7 @@ dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, con
   if ((st = make_map_3d(&mx, false, x, k, m, 1, k, m * k, 128, plan.nt, 1, "codes")) != DG_OK) return st;
   const double wn = static_cast<double>(N) * K;
   TraceScope trace(name, s, 2.0 * M * wn, static_cast<double>(M) * K + wn + 2.0 * M * N);
-  return launched(launch_mx_few(plan, mw, mx, w, sw, sx, bias, y, static_cast<int>(M), static_cast<int>(N),
+  return launched(launch_mx_few(plan, mw, mx, sw, sx, bias, y, static_cast<int>(M), static_cast<int>(N),
                                 static_cast<int>(K), dev, s),
                   name);
 }

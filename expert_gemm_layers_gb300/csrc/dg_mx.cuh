@@ -57,7 +57,8 @@ struct MxCfg {
   static constexpr int EPI_WARPS = 4;
   static constexpr int CHUNK = 32;                     // output columns per staging buffer
   static constexpr int EPI_BUF_BYTES = 32 * CHUNK * 2;
-  static constexpr int EPI_BYTES = EPI_WARPS * 2 * EPI_BUF_BYTES;
+  static constexpr int EPI_BUFS = 2;                   // staging buffers a warp (four: no change)
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUFS * EPI_BUF_BYTES;
   static constexpr int SF_WARPS = 4;
   static constexpr int SF_BUFS = 4;
   static constexpr int SF_COLS = 16;                   // A words at +0, B words at +8
@@ -122,6 +123,14 @@ static __device__ __forceinline__ void tmem_st_wait() {
 static __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// Cluster barrier in two halves: every thread of the cluster arrives, and waits later.  No memory is passed on by it
+// (barriers' initialisation has a fence of its own), so the arrival is relaxed: a releasing one first waits for the
+// thread's accesses, 2000 cycles in a prologue that has just asked for memory.
+static __device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+static __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // mbar_wait by a whole warp: all lanes go on or none does.
 static __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t site) {
@@ -252,7 +261,9 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
   }
   griddep_wait();
   tc_fence_before_sync();
-  cluster_sync_all();
+  cluster_arrive();
+  cluster_wait();
+  __syncthreads();  // the TMEM address in shared memory
   tc_fence_after_sync();
   const uint32_t tmem_base = *tmem_holder;
 
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
   } else if (warp < 2 + Cfg::EPI_WARPS) {
     // ------------------------------------------------------------ epilogue
     const int lg = warp & 3;
-    uint8_t* stg = epi_base + (warp - 2) * 2 * Cfg::EPI_BUF_BYTES;
+    uint8_t* stg = epi_base + (warp - 2) * Cfg::EPI_BUFS * Cfg::EPI_BUF_BYTES;
     uint32_t tphase = 0, ctr = 0;
     const bool aborted = ld_volatile_u32(p.err) != 0u;
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(32 * lg) << 16);
@@ -396,13 +407,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
         if (lane == 0) mbar_arrive_pair(mapa_shared(smem_u32(&tempty[acc]), 0));
       };
       if (nchunks == 0) release_acc();
-      for (int j = 0; j < nchunks; ++j, ++ctr) {
-        const int c0 = n0 + Cfg::CHUNK * j;
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(lane_addr + static_cast<uint32_t>(acc * Cfg::BN + Cfg::CHUNK * j), r);
-        tmem_ld_wait();
-        tmem_regs_after_wait(r);
-        if (j + 1 == nchunks) release_acc();
+      auto store_chunk = [&](const uint32_t (&r)[32], int c0) {
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
@@ -421,9 +426,10 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
             }
           }
         }
-        uint8_t* sbuf = stg + (ctr & 1u) * Cfg::EPI_BUF_BYTES;
+        uint8_t* sbuf = stg + (ctr & (Cfg::EPI_BUFS - 1)) * Cfg::EPI_BUF_BYTES;
+        ++ctr;
         // the store that last read this buffer must be done
-        if (lane == 0) bulk_wait_group_read<1>();
+        if (lane == 0) bulk_wait_group_read<Cfg::EPI_BUFS - 1>();
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -436,9 +442,22 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
           tma_store_3d(&tmD, sbuf, c0, row0, 0);
           bulk_commit_group();
         }
+      };
+      const uint32_t acc_addr = lane_addr + static_cast<uint32_t>(acc * Cfg::BN);
+      for (int j = 0; j < nchunks; j += 2) {
+        uint32_t r0[32], r1[32];
+        const bool two = j + 1 < nchunks;
+        tmem_ld_32x32b_x32(acc_addr + static_cast<uint32_t>(Cfg::CHUNK * j), r0);
+        if (two) tmem_ld_32x32b_x32(acc_addr + static_cast<uint32_t>(Cfg::CHUNK * (j + 1)), r1);
+        tmem_ld_wait();
+        tmem_regs_after_wait(r0);
+        tmem_regs_after_wait(r1);
+        if (j + 2 >= nchunks) release_acc();
+        store_chunk(r0, n0 + Cfg::CHUNK * j);
+        if (two) store_chunk(r1, n0 + Cfg::CHUNK * (j + 1));
       }
     }
-    if (lane == 0) bulk_wait_group<0>();
+    if (lane == 0) bulk_wait_group_read<0>();  // the staging buffers have been read
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales
@@ -503,7 +522,8 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
 
   griddep_launch_dependents();
   tc_fence_before_sync();
-  cluster_sync_all();
+  cluster_arrive();
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, 512);

@@ -9,10 +9,7 @@
 // (the same result every time).
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 bring
-// the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.  Before they
-// wait for the kernel that makes x, they ask for the CTA's first weight tiles in L2:
-// these are on their way while that kernel still runs, and L2 holds whatever was
-// written last, so this is no early read.
+// the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.
 #include "dg_internal.h"
 #include "dg_mx.cuh"
 
@@ -49,17 +46,11 @@ struct FewCfg {
 
 struct FewParams {
   int32_t M, N, kb;            // rows of x, features, K blocks
-  int32_t K;
-  const uint8_t* w;            // codes of the weight [N][K]
   const uint8_t *sx, *sw;      // [M][kb], [ceil(N/128)][kb]
   const __nv_bfloat16* bias;
   __nv_bfloat16* y;
   uint32_t* err;
 };
-
-// Split cluster barrier: every thread of the cluster arrives, and waits later.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // 16 bytes into a cluster CTA's shared memory, counted on an mbarrier of the same CTA.
 __device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, float c, float d, uint32_t bar) {
@@ -75,10 +66,6 @@ __device__ __forceinline__ void dsmem_bulk_copy(uint32_t dst, uint32_t src, uint
                : "memory");
 }
 
-// Asks for a line in L2.
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-constexpr int kPrefetchTiles = 16;
 
 template <int NT>
 __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
@@ -131,13 +118,6 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
   if (warp == 1) {
     tmem_alloc(tmem_holder, Cfg::TMEM_COLS);
     tmem_relinquish();
-  }
-  if (warp >= 2) {
-    const int n = n0 + static_cast<int>(threadIdx.x) - 64;
-    if (n < p.N)
-      for (int i = 0; i < num_kb && i < kPrefetchTiles; ++i)
-        prefetch_l2(p.w + static_cast<int64_t>(n) * p.K + static_cast<int64_t>(kb0 + i) * 128);
-    if (threadIdx.x == 64) prefetch_l2(p.sw + static_cast<int64_t>(blockIdx.x) * p.kb + kb0);
   }
   griddep_wait();
   tc_fence_before_sync();
@@ -388,11 +368,9 @@ MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
   return plan;
 }
 
-cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* w_codes,
-                          const void* sw, const void* sx, const void* bias, void* y, int M, int N, int K,
+cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* sw, const void* sx, const void* bias, void* y, int M, int N, int K,
                           const DeviceInfo& dev, cudaStream_t s) {
-  const FewParams p{M, N, (K + 127) / 128, K, static_cast<const uint8_t*>(w_codes),
-                    static_cast<const uint8_t*>(sx), static_cast<const uint8_t*>(sw),
+  const FewParams p{M, N, (K + 127) / 128, static_cast<const uint8_t*>(sx), static_cast<const uint8_t*>(sw),
                     static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), dev.err};
   switch (plan.nt) {
     case 16: return few_launch<16>(w, x, p, plan.split, dev, s);
