@@ -65,8 +65,9 @@ dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t 
   dg_status st;
   const uint64_t m = M, n = N, k = K;
   if ((st = make_map_3d(&ma, false, a, k, m, 1, k, m * k, 128, 128, 1, "codes")) != DG_OK) return st;
+  const int tile_n = mx_tile_n(b_mn_major, M, N, dev);
   st = b_mn_major ? make_map_3d(&mb, false, b, n, k, 1, n, n * k, 128, 128, 1, "weight codes (N-major)")
-                  : make_map_3d(&mb, false, b, k, n, 1, k, n * k, 128, kMxTileN / 2, 1, "weight codes");
+                  : make_map_3d(&mb, false, b, k, n, 1, k, n * k, 128, tile_n / 2, 1, "weight codes");
   if (st != DG_OK) return st;
   if ((st = make_map_3d_sw(&md, true, d, n, m, 1, 2 * n, 2 * n * m, 32, 32, 1, 64, "output")) != DG_OK) return st;
   MxParams p{};
@@ -82,7 +83,7 @@ dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t 
   p.err = dev.err;
   const double w = static_cast<double>(N) * K;
   TraceScope trace(name, s, 2.0 * M * w, static_cast<double>(M) * K + w + 2.0 * M * N);
-  return launched(launch_gemm_mx(b_mn_major, ma, mb, md, p, dev, s), name);
+  return launched(launch_gemm_mx(b_mn_major, tile_n, ma, mb, md, p, dev, s), name);
 }
 
 // The product for few rows.
@@ -150,7 +151,7 @@ dg_status dg_fp8_quantize(int64_t rows, int64_t K, int32_t block_rows, const voi
   if ((st = device_info(&dev)) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope trace("fp8_quantize", s, 0.0, 3.0 * n);
-  return launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(K), block_rows, nullptr, s), "fp8_quantize");
+  return launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(K), block_rows, s), "fp8_quantize");
 }
 
 dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const void* codes, const void* scales,
@@ -166,7 +167,7 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
   if ((st = device_info(&dev)) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope trace("fp8_dequantize", s, 0.0, 3.0 * n);
-  return launched(launch_fp8_dequantize(codes, scales, x, rows, static_cast<int>(K), block_rows, nullptr, s), "fp8_dequantize");
+  return launched(launch_fp8_dequantize(codes, scales, x, rows, static_cast<int>(K), block_rows, s), "fp8_dequantize");
 }
 
 // Where the activations come in bf16, their codes and scales lie in the workspace behind the error block.
@@ -201,7 +202,7 @@ dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_f, int64_t out_f, const vo
   uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at;
   {
     TraceScope trace("fp8_quantize", s, 0.0, 3.0 * elements(rows, in_f));
-    st = launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(in_f), 1, dev.err, s), "fp8_linear_bf16");
+    st = launched(launch_fp8_quantize(x, codes, scales, rows, static_cast<int>(in_f), 1, s), "fp8_linear_bf16");
     if (st != DG_OK) return st;
   }
   return run_linear(rows, in_f, out_f, codes, scales, w_codes, w_scales, bias, y, dev, s);
@@ -277,7 +278,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
       const int K = static_cast<int>(out_f);
       st = launched(d_bias ? launch_fp8_quantize_sum(dy, base + l.dy_codes, base + l.dy_scales, d_bias,
                                                      reinterpret_cast<float*>(base + l.sums), rows, K, dev.err, s)
-                           : launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, K, 1, dev.err, s),
+                           : launch_fp8_quantize(dy, base + l.dy_codes, base + l.dy_scales, rows, K, 1, s),
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
@@ -285,8 +286,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
     if (l.turn) {
       TraceScope trace("fp8_bwd_turn_w", s, 0.0, 2.0 * wn);
       b = base + l.w_turned;
-      st = launched(launch_transpose_codes(w_codes, base + l.w_turned, static_cast<int>(out_f), static_cast<int>(in_f),
-                                           dev.err, s),
+      st = launched(launch_transpose_codes(w_codes, base + l.w_turned, static_cast<int>(out_f), static_cast<int>(in_f), s),
                     "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
@@ -299,7 +299,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
     uint8_t* x = base + l.x;
     {
       TraceScope trace("fp8_bwd_expand_x", s, 0.0, 3.0 * xn);
-      st = launched(launch_fp8_dequantize(x_codes, x_scales, x, rows, static_cast<int>(in_f), 1, dev.err, s), "fp8_linear_bwd");
+      st = launched(launch_fp8_dequantize(x_codes, x_scales, x, rows, static_cast<int>(in_f), 1, s), "fp8_linear_bwd");
       if (st != DG_OK) return st;
     }
     const uint64_t R = rows, I = in_f, O = out_f;

@@ -83,9 +83,10 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 constexpr int kThreads = 256;
 
-// The kernels take the error word of their call's workspace (NULL for calls without one): after a recorded failure they
-// write nothing.  It is asked for with the first data and looked at before the first store.
-__device__ __forceinline__ uint32_t error_word(const uint32_t* err) { return err ? ld_volatile_u32(err) : 0u; }
+// Kernels that write a call's results look at the error word of its workspace: after a recorded failure they write
+// nothing.  It is asked for with the first data and looked at before the first store.  Those that only fill scratch do
+// not (read by every warp of 8192 x 14336 it cost 4 of 52 us).
+__device__ __forceinline__ uint32_t error_word(const uint32_t* err) { return ld_volatile_u32(err); }
 
 // ------------------------------------------------------------------ quantise, blocks of 1 x 128
 
@@ -93,11 +94,9 @@ __device__ __forceinline__ uint32_t error_word(const uint32_t* err) { return err
 constexpr int kQuantUnits = 4;
 template <bool kWhole>  // whole: K is a multiple of 128, blocks lie one after another
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
-                                                              uint8_t* __restrict__ scale, int64_t blocks, int K, int nb,
-                                                              const uint32_t* err) {
+                                                              uint8_t* __restrict__ scale, int64_t blocks, int K, int nb) {
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t failed = error_word(err);
   const int sub = threadIdx.x & 15;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * kQuantUnits * kThreads + threadIdx.x) >> 4;
   uint4 v[kQuantUnits];
@@ -117,7 +116,6 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __nv_bfloat1
     }
     v[i] = in[i] ? __ldcs(reinterpret_cast<const uint4*>(x + at[i])) : make_uint4(0u, 0u, 0u, 0u);
   }
-  if (failed) return;
 #pragma unroll
   for (int i = 0; i < kQuantUnits; ++i) {
     const int64_t b = first + i * (kThreads / 16);
@@ -175,11 +173,10 @@ __global__ void __launch_bounds__(256 * kBlocks) quant_tiles_kernel(const __nv_b
 // out [K][rows] = in [rows][K], bytes, one 128 x 128 tile a CTA through shared memory (both sizes multiples of 16).  A
 // thread turns 4 x 4 bytes; its warp takes 8 such blocks down and 4 across, which with rows of 33 words are 32 banks.
 __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t* __restrict__ in, uint8_t* __restrict__ out,
-                                                                   int rows, int K, const uint32_t* err) {
+                                                                   int rows, int K) {
   __shared__ uint32_t tile[128][33];
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t failed = error_word(err);
   const int r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -193,7 +190,6 @@ __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t
     t[3] = v.w;
   }
   __syncthreads();
-  if (failed) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -218,10 +214,9 @@ __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t
 constexpr int kDeqUnits = 4;
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                            __nv_bfloat16* __restrict__ x, int64_t rows, int K, int nb,
-                                                           int row_shift, int spans, const uint32_t* err) {
+                                                           int row_shift, int spans) {
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t failed = error_word(err);
   const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int64_t row = w / spans;
   if (row >= rows) return;
@@ -239,7 +234,6 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __rest
       s[i] = scale_value(__ldg(srow + (c >> 7)));
     }
   }
-  if (failed) return;
 #pragma unroll
   for (int i = 0; i < kDeqUnits; ++i) {
     const int c = c0 + 256 * i;
@@ -623,11 +617,10 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 // the column sums of what it reads stay in registers: part[blockIdx.y][column].
 __global__ void __launch_bounds__(kThreads) quant_rows_sum_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
                                                                   uint8_t* __restrict__ scale, float* __restrict__ part,
-                                                                  int64_t rows, int K, int nb, const uint32_t* err) {
+                                                                  int64_t rows, int K, int nb) {
   __shared__ float s[kThreads / 16][128 + 4];
   griddep_wait();
   griddep_launch_dependents();
-  if (error_word(err)) return;
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int c = blockIdx.x * 128 + 8 * sub;
   float sum[8] = {};
@@ -682,7 +675,7 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
-                                const uint32_t* err, cudaStream_t s) {
+                                cudaStream_t s) {
   const int nb = (K + 127) / 128;
   auto* xp = static_cast<const __nv_bfloat16*>(x);
   auto* q = static_cast<uint8_t*>(codes);
@@ -690,8 +683,8 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
   if (block_rows == 1) {
     const int64_t blocks = rows * nb, per = kThreads / 16 * kQuantUnits;
     const dim3 grid(static_cast<unsigned>((blocks + per - 1) / per));
-    return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb, err)
-                        : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb, err);
+    return K % 128 == 0 ? launch_pdl(quant_rows_kernel<true>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb)
+                        : launch_pdl(quant_rows_kernel<false>, grid, dim3(kThreads), 0, s, xp, q, sc, blocks, K, nb);
   }
   // Two blocks a CTA where there are many (28672 x 4096, with 7168: 58 us against 62), one where not (1003 x 2064: 2.5
   // us against 3.4; 8192 x 4096, 2048: 16.8 against 18.5).
@@ -704,17 +697,17 @@ cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_
 }
 
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
-                                  const uint32_t* err, cudaStream_t s) {
+                                  cudaStream_t s) {
   const int nb = (K + 127) / 128, spans = (K + 256 * kDeqUnits - 1) / (256 * kDeqUnits);
   const int64_t warps = rows * spans;
   return launch_pdl(dequant_kernel, dim3(static_cast<unsigned>((warps * 32 + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
                     static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), static_cast<__nv_bfloat16*>(x),
-                    rows, K, nb, block_rows == 1 ? 0 : 7, spans, err);
+                    rows, K, nb, block_rows == 1 ? 0 : 7, spans);
 }
 
-cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, const uint32_t* err, cudaStream_t s) {
+cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s) {
   return launch_pdl(transpose_codes_kernel, dim3((K + 127) / 128, (rows + 127) / 128), dim3(kThreads), 0, s,
-                    static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, K, err);
+                    static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, K);
 }
 
 cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void* h, void* y, void* codes, void* scales,
@@ -788,7 +781,7 @@ cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, vo
   const int nb = (K + 127) / 128, parts = fp8_quantize_sum_parts(rows, K);
   cudaError_t e = launch_pdl(quant_rows_sum_kernel, dim3(nb, parts), dim3(kThreads), 0, s,
                              static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(codes),
-                             static_cast<uint8_t*>(scales), part, rows, K, nb, err);
+                             static_cast<uint8_t*>(scales), part, rows, K, nb);
   if (e != cudaSuccess) return e;
   return launch_pdl(sum_parts_kernel, dim3((K + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
                     static_cast<__nv_bfloat16*>(sums), parts, K, err);

@@ -402,17 +402,16 @@ cudaError_t smem_limit_once(const void* kern, int bytes, int dev);
 // ---------------------------------------------------------------- block-scaled e4m3 (dg_fp8_rows.cu, dg_mx_gemm.cu)
 
 // x [rows, K] bf16 <-> codes [rows, K] and scales [ceil(rows / block_rows), ceil(K / 128)]; block_rows 1 or 128.
-// err here and below: the error word of the call's workspace, or NULL.
 cudaError_t launch_fp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int K, int block_rows,
-                                const uint32_t* err, cudaStream_t s);
+                                cudaStream_t s);
 cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x, int64_t rows, int K, int block_rows,
-                                  const uint32_t* err, cudaStream_t s);
+                                  cudaStream_t s);
 
 // Codes [rows, K] -> [K, rows]; rows and K multiples of 16, rows <= 65535 * 128.
-cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, const uint32_t* err, cudaStream_t s);
+cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s);
 
 // x [rows, K] to codes and scales of 1 x 128 blocks and sums [K] = column sums of x, read once;
-// part [fp8_quantize_sum_parts][K] binary32.
+// part [fp8_quantize_sum_parts][K] binary32.  err here and below: the error word of the call's workspace.
 int fp8_quantize_sum_parts(int64_t rows, int K);
 cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
                                     int K, const uint32_t* err, cudaStream_t s);
@@ -426,10 +425,12 @@ cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, co
                                 void* scratch, int64_t rows, int d, float eps, const uint32_t* err, cudaStream_t s);
 
 // One launch of the block-scaled GEMM (dg_mx.cuh); p.tiles_* and p.n_fastest are filled in.  Box heights of the maps:
-// A 128 rows, a K-major B kMxTileN / 2 rows, an MN-major B 128 columns by 128 rows, D 32 columns by 32 rows.
+// A 128 rows, a K-major B tile_n / 2 rows, an MN-major B 128 columns by 128 rows, D 32 columns by 32 rows.
 struct MxParams;
 constexpr int kMxTileN = 224;
-cudaError_t launch_gemm_mx(bool b_mn_major, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d,
+// Columns of a tile for these sizes, and how many tiles a pair of CTAs then takes one after another.
+int mx_tile_n(bool b_mn_major, int64_t M, int64_t N, const DeviceInfo& dev, int64_t* turns = nullptr);
+cudaError_t launch_gemm_mx(bool b_mn_major, int tile_n, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d,
                            const MxParams& p, const DeviceInfo& dev, cudaStream_t s);
 
 // The same product for few rows (dg_mx_few.cu): rows of x a tile has, the CTAs that share its K, and whether it is

@@ -359,12 +359,13 @@ MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
   plan.split = 1;
   for (int c = 2; c <= FewCfg<16>::MAX_SPLIT; c *= 2)
     if (tiles * c * 100 <= places * 85 && kb >= (c == 8 ? 64 : 2 * c)) plan.split = c;
-  // Above 64 rows the tiles of dg_mx.cuh may take less time: both sides measured at 11, 32 and 112 K blocks and 96 to
-  // 512 rows, about 11 us + 0.31 us a K block of a CTA here and 7.3 us + 0.245 us there (128 rows: 14.4 against 15.2 us
-  // for 4096 to 4096, 17.1 against 15.4 for 4096 to 6144, 21.7 against 34.8 for 14336 to 4096).
+  // Above 64 rows the tiles of dg_mx.cuh may take less time.  Both sides measured at 11, 32 and 112 K blocks and 96 to 512
+  // rows: here about 11 us and 0.3 us a K block of a CTA, there 7.3 us and a turn's K blocks at 0.2 us (tiles of 128
+  // columns) or 0.245 us (192 rows: 16.8 against 13.4 us for 4096 to 4096, 27.6 against 30.5 us for 14336 to 4096).
+  int64_t turns;
+  const int unit = mx_tile_n(false, M, N, dev, &turns) == 128 ? 16 : 20;
   const int64_t waves = (tiles * plan.split + places - 1) / places, blocks = (kb + plan.split - 1) / plan.split;
-  const int64_t pairs = dev.num_sms / 2, wide = (M + 255) / 256 * ((N + kMxTileN - 1) / kMxTileN);
-  plan.better = M <= 64 || (M <= 512 && 60 + 5 * waves * blocks < 4 * ((wide + pairs - 1) / pairs) * kb);
+  plan.better = M <= 64 || (M <= 512 && 300 + 25 * waves * blocks < unit * turns * kb);
   return plan;
 }
 

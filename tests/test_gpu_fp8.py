@@ -107,7 +107,7 @@ def test_dequantize_every_scale():
 LINEAR = [(1, 16, 16), (1, 4096, 256), (2, 128, 240), (7, 144, 224), (16, 512, 448), (17, 528, 464), (33, 2064, 128),
           (64, 1024, 1024), (100, 1296, 2064), (128, 640, 272), (129, 256, 512), (256, 896, 224), (257, 384, 688),
           (511, 2048, 480), (1000, 272, 1296), (3, 8192, 144), (40, 8208, 272), (65, 4112, 128), (100, 8192, 528),
-          (128, 8208, 400), (300, 12288, 272)]
+          (128, 8208, 400), (300, 12288, 272), (260, 400, 7168), (1300, 272, 4112)]
 
 
 @pytest.mark.parametrize("rows,K,N", LINEAR)
