@@ -73,7 +73,6 @@ dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t 
   MxParams p{};
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
-  p.K = static_cast<int32_t>(K);
   p.sa = static_cast<const uint8_t*>(sa);
   p.ka = static_cast<int32_t>(blocks128(K));
   p.sb = static_cast<const uint8_t*>(sb);
@@ -145,7 +144,7 @@ dg_status dg_fp8_quantize(int64_t rows, int64_t K, int32_t block_rows, const voi
   const size_t n = elements(rows, K);
   const Arg args[] = {{"x", x, 2 * n, false, false},
                       {"codes", codes, n, false, true},
-                      {"scales", scales, scale_bytes(rows, K, block_rows), false, true}};
+                      {"scales", scales, scale_bytes(rows, K, block_rows), false, true, true}};
   if ((st = check_args("fp8_quantize", args)) != DG_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != DG_OK) return st;
@@ -160,7 +159,7 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
   if (st != DG_OK || rows == 0) return st;
   const size_t n = elements(rows, K);
   const Arg args[] = {{"codes", codes, n, false, false},
-                      {"scales", scales, scale_bytes(rows, K, block_rows), false, false},
+                      {"scales", scales, scale_bytes(rows, K, block_rows), false, false, true},
                       {"x", x, 2 * n, false, true}};
   if ((st = check_args("fp8_dequantize", args)) != DG_OK) return st;
   DeviceInfo dev;
@@ -187,7 +186,7 @@ dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_f, int64_t out_f, const vo
   const size_t scales_at = linear_scales_at(rows, in_f), need = scales_at + round256(scale_bytes(rows, in_f, 1));
   const Arg args[] = {{"x", x, 2 * elements(rows, in_f), false, false},
                       {"w_codes", w_codes, elements(out_f, in_f), false, false},
-                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), false, false},
+                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), false, false, true},
                       {"bias", bias, 2 * static_cast<size_t>(out_f), true, false},
                       {"y", y, 2 * elements(rows, out_f), false, true},
                       {"ws", ws, ws ? need : 0, true, true}};
@@ -220,9 +219,9 @@ dg_status dg_fp8_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x
   if (st != DG_OK || rows == 0) return st;
   const size_t need = dg_fp8_linear_workspace_bytes(rows, in_f, out_f);
   const Arg args[] = {{"x_codes", x_codes, elements(rows, in_f), false, false},
-                      {"x_scales", x_scales, scale_bytes(rows, in_f, 1), false, false},
+                      {"x_scales", x_scales, scale_bytes(rows, in_f, 1), false, false, true},
                       {"w_codes", w_codes, elements(out_f, in_f), false, false},
-                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), false, false},
+                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), false, false, true},
                       {"bias", bias, 2 * static_cast<size_t>(out_f), true, false},
                       {"y", y, 2 * elements(rows, out_f), false, true},
                       {"ws", ws, ws ? need : 0, true, true}};
@@ -250,9 +249,9 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
   const BwdLayout l = bwd_layout(rows, in_f, out_f);
   const bool any = rows > 0;
   const Arg args[] = {{"x_codes", x_codes, xn, !(any && d_weight), false},
-                      {"x_scales", x_scales, scale_bytes(rows, in_f, 1), !(any && d_weight), false},
+                      {"x_scales", x_scales, scale_bytes(rows, in_f, 1), !(any && d_weight), false, true},
                       {"w_codes", w_codes, wn, !(any && dx), false},
-                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), !(any && dx), false},
+                      {"w_scales", w_scales, scale_bytes(out_f, in_f, 128), !(any && dx), false, true},
                       {"dy", dy, 2 * yn, !(any && (dx || d_weight || d_bias)), false},
                       {"dx", dx, 2 * xn, true, true},
                       {"d_weight", d_weight, 2 * wn, true, true},
@@ -342,7 +341,7 @@ dg_status dg_rms_norm(int64_t rows, int64_t d, float eps, const void* x, const v
   const Arg args[] = {{"x", x, 2 * n, false, false},         {"residual", residual, 2 * n, true, false},
                       {"weight", weight, 2 * static_cast<size_t>(d), false, false},
                       {"h", h, 2 * n, true, true},           {"y", y, 2 * n, true, true},
-                      {"codes", codes, n, true, true},       {"scales", scales, scale_bytes(rows, d, 1), true, true}};
+                      {"codes", codes, n, true, true},       {"scales", scales, scale_bytes(rows, d, 1), true, true, true}};
   if ((st = check_args("rms_norm", args)) != DG_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != DG_OK) return st;

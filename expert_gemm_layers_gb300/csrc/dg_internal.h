@@ -27,13 +27,15 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 // A tensor of a call: its name, address and bytes, whether it may be NULL
-// (then it takes no part) and whether the call writes it.
+// (then it takes no part), whether the call writes it, and whether it may lie
+// at any address.
 struct Arg {
   const char* name;
   const void* p;
   size_t bytes;
   bool optional;
   bool written;
+  bool anywhere = false;
 };
 
 // NULL, alignment and overlap rules of all tensors of one call.
@@ -41,7 +43,7 @@ template <int N>
 dg_status check_args(const char* what, const Arg (&a)[N]) {
   for (const Arg& t : a) {
     if (!t.p && !t.optional) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is NULL", what, t.name);
-    if (!aligned16(t.p)) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", what, t.name);
+    if (!t.anywhere && !aligned16(t.p)) return fail(DG_ERR_INVALID_ARGUMENT, "%s: %s is not 16-byte aligned", what, t.name);
   }
   for (int i = 0; i < N; ++i)
     for (int j = 0; j < N; ++j)

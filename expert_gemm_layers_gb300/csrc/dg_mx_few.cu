@@ -6,7 +6,8 @@
 // along the weight.  One CTA takes 128 features and a part of K; the CTAs of a
 // cluster share the features and split K, leave their binary32 sums in shared
 // memory and add them through distributed shared memory in the order of their ranks
-// (the same result every time).
+// (the same result every time).  One row, 4096 to 6144: 8 to 9 us with the kernel in
+// front, 25 MB; 4 rows, 4096 to 28672: 22.5 us, 5.2 TB/s.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 bring
 // the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.
@@ -65,7 +66,6 @@ __device__ __forceinline__ void dsmem_bulk_copy(uint32_t dst, uint32_t src, uint
                "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-
 
 template <int NT>
 __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
     feed.rows = p.M;
     feed.blocks = 1;
     feed.tid = static_cast<int>(threadIdx.x) - 64;
-    feed.wide = ((p.kb | kb0) & 15) == 0;
+    feed.wide = ((p.kb | kb0) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
     feed.fetch(t0, 0, kb0, kb1);
     int half = 0;
     for (int kb = kb0; kb < kb1; kb += 16, half ^= 1) {

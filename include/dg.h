@@ -499,7 +499,8 @@ dg_status dg_moe_swiglu_w4(const dg_moe_shape* shape, int32_t group, const void*
  * max |x| <= 448 * 2^e (1 for a block of zeros), code = the e4m3 value nearest to x / scale, ties to even.  A block
  * that holds a NaN or an infinity gets NaN for its scale and all its codes.
  * dg_fp8_dequantize writes the values, rounded to bf16 (exact for what the quantiser wrote).
- * K % 16 == 0; rows >= 0 (0 = nothing to do).
+ * K % 16 == 0; rows >= 0 (0 = nothing to do).  Scales may lie at any address here and below, so that a part of the
+ * rows can be taken.
  * ------------------------------------------------------------------------ */
 dg_status dg_fp8_quantize(int64_t rows, int64_t K, int32_t block_rows, const void* x, void* codes, void* scales,
                           void* stream);

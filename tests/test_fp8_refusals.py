@@ -53,6 +53,7 @@ def test_linear(lib, mem):
     assert call(N=(1 << 31) - 1024, K=16) == UNSUPPORTED and call(rows=(1 << 31) - 1024) == UNSUPPORTED
     for name in ("xc", "xs", "wc", "ws", "y"):
         assert call(**{name: None}) == INVALID
+    for name in ("xc", "wc", "y", "b"):
         assert call(**{name: ok[name] + 4}) == INVALID and b"aligned" in lib.dg_last_error()
     assert call(y=ok["xc"]) == INVALID and call(y=ok["w"]) == INVALID and call(b=ok["y"]) == INVALID
     assert call(w=None) == WORKSPACE and call(n=255) == WORKSPACE

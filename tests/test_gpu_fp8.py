@@ -146,6 +146,21 @@ def test_linear_from_bf16_and_leading_dimensions():
     assert dg.fp8_linear(x.to(DEV)[:0], w8).shape == (0, 3, 160)
 
 
+@pytest.mark.parametrize("K", [272, 2048])
+def test_parts_of_the_rows(K):
+    """Activations sliced by rows: their scales begin at any byte."""
+    x, w8, dy = randn((300, K), 1).to(DEV), dg.fp8_quantize(randn((160, K), 2).to(DEV), 128), randn((300, 160), 3).to(DEV)
+    codes, scales = dg.fp8_quantize(x)
+    xv, wv = fp8.values(u8(codes), u8(scales)), fp8.values(u8(w8[0]), u8(w8[1]), 128)
+    for a, b in ((3, 20), (7, 300), (299, 300)):
+        part = codes[a:b], scales[a:b]
+        assert torch.equal(dg.fp8_linear(part, w8), dg.fp8_linear(tuple(t.clone() for t in part), w8))
+        within(dg.fp8_linear(part, w8), fp8.linear(xv[a:b], wv), "rows of y")
+        assert torch.equal(dg.fp8_dequantize(*part), dg.fp8_dequantize(codes, scales)[a:b])
+        assert torch.equal(dg.fp8_linear_backward(part, w8, dy[a:b])["weight"],
+                           dg.fp8_linear_backward(tuple(t.clone() for t in part), w8, dy[a:b])["weight"])
+
+
 @pytest.mark.parametrize("rows", [1, 5, 40, 200])
 def test_what_is_not_finite_stays_in_its_row(rows):
     x, w = randn((rows, 512), 1), randn((288, 512), 2)
