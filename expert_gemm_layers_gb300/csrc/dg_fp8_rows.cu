@@ -83,6 +83,9 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
 
 constexpr int kThreads = 256;
 
+// A kernel here may begin while the one that makes its input still runs (it then waits), so no load may go through the
+// path for data that stays as it is for the whole of a kernel: __ldca, __ldcg and __ldcs, no __ldg.
+//
 // Kernels that write a call's results look at the error word of its workspace: after a recorded failure they write
 // nothing.  It is asked for with the first data and looked at before the first store.  Those that only fill scratch do
 // not (read by every warp of 8192 x 14336 it cost 4 of 52 us).
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) transpose_codes_kernel(const uint8_t
   for (int i = 0; i < 4; ++i) {
     const int r = (threadIdx.x >> 3) + 32 * i, c = 16 * (threadIdx.x & 7);
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r0 + r < rows && c0 + c < K) v = __ldg(reinterpret_cast<const uint4*>(in + static_cast<int64_t>(r0 + r) * K + c0 + c));
+    if (r0 + r < rows && c0 + c < K) v = __ldcg(reinterpret_cast<const uint4*>(in + static_cast<int64_t>(r0 + r) * K + c0 + c));
     uint32_t* t = &tile[r][c / 4];
     t[0] = v.x;
     t[1] = v.y;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const uint8_t* __rest
     s[i] = 0.0f;
     if (c < K) {
       v[i] = __ldcs(reinterpret_cast<const uint2*>(q + row * K + c));
-      s[i] = scale_value(__ldg(srow + (c >> 7)));
+      s[i] = scale_value(__ldca(srow + (c >> 7)));
     }
   }
 #pragma unroll
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kMaxT) rms_norm_kernel(const NormArgs a) {
   for (int i = 0; i < C; ++i) {
     const int c = t + i * T;
     const bool in = live && c < chunks;
-    const uint4 wv = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 wv = c < chunks ? __ldca(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
     float v[8], g[8];
     unpack8(xv[i], v);
     unpack8(wv, g);
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kMaxT, kWarp ? 2 : C == 1 ? 3 : 1) rms_norm_bw
   };
 #pragma unroll
   for (int i = 0; i < C; ++i)
-    wv[i] = t + i * T < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
+    wv[i] = t + i * T < chunks ? __ldca(reinterpret_cast<const uint4*>(a.w) + t + i * T) : make_uint4(0u, 0u, 0u, 0u);
   float2 dw[C][4];
 #pragma unroll
   for (int i = 0; i < C; ++i)
@@ -517,9 +520,9 @@ __global__ void __launch_bounds__(256) norm_bwd_rows_kernel(const NormBwdArgs a,
 #pragma unroll 4
     for (int c = threadIdx.x; c < chunks; c += 256) {
       float h[8], y[8], g[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(a.h + row * a.d) + c), h);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(a.dy + row * a.d) + c), y);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(a.w) + c), g);
+      unpack8(__ldcg(reinterpret_cast<const uint4*>(a.h + row * a.d) + c), h);
+      unpack8(__ldcg(reinterpret_cast<const uint4*>(a.dy + row * a.d) + c), y);
+      unpack8(__ldca(reinterpret_cast<const uint4*>(a.w) + c), g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float u = h[e] * pre;
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(256) norm_bwd_apply_kernel(const NormBwdArgs a
   const int c = 8 * (blockIdx.x * 256 + threadIdx.x);
   if (c >= a.d || error_word(a.err)) return;
   float g[8], dw[8] = {};
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.w + c)), g);
+  unpack8(__ldca(reinterpret_cast<const uint4*>(a.w + c)), g);
   constexpr int kUnits = 4;  // rows in flight
   const int64_t step = gridDim.y;
   for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += kUnits * step) {
@@ -556,7 +559,7 @@ __global__ void __launch_bounds__(256) norm_bwd_apply_kernel(const NormBwdArgs a
       hv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.h + r * a.d + c)) : z;
       yv[i] = in ? __ldcs(reinterpret_cast<const uint4*>(a.dy + r * a.d + c)) : z;
       pv[i] = in && a.dh ? __ldcs(reinterpret_cast<const uint4*>(a.dh + r * a.d + c)) : z;
-      k[i] = in ? __ldg(coef + r) : make_float2(0.0f, 0.0f);
+      k[i] = in ? __ldca(coef + r) : make_float2(0.0f, 0.0f);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {

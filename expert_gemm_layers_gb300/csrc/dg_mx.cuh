@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (c0 + 8 * q < p.N) {
-              const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + c0 + 8 * q));
+              const uint4 bv = __ldca(reinterpret_cast<const uint4*>(p.bias + c0 + 8 * q));
               const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
   cluster_arrive();
   cluster_wait();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc_pair(tmem_base, 512);
   }

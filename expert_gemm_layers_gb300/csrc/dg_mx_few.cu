@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
           v1.z += b.z;
           v1.w += b.w;
         }
-        const float2 bias = p.bias ? unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(p.bias + n))) : make_float2(0.f, 0.f);
+        const float2 bias = p.bias ? unpack_bf16x2(__ldca(reinterpret_cast<const uint32_t*>(p.bias + n))) : make_float2(0.f, 0.f);
         const uint32_t o[4] = {pack_bf16x2(v0.x + bias.x, v1.x + bias.y), pack_bf16x2(v0.y + bias.x, v1.y + bias.y),
                                pack_bf16x2(v0.z + bias.x, v1.z + bias.y), pack_bf16x2(v0.w + bias.x, v1.w + bias.y)};
         uint32_t* y = reinterpret_cast<uint32_t*>(p.y + static_cast<int64_t>(t0 + 4 * t4) * p.N + n);
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
   }
   cluster_wait();  // no CTA leaves while a peer may still send to it
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
   }
