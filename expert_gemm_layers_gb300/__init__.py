@@ -22,6 +22,8 @@ TMA/mbarrier pipelines):
 * rms_norm      the root-mean-square norm with the residual's addition, its
                 result in bf16 or block-scaled e4m3 (forward, backward,
                 autograd; fp8_norm_linear_layer joins it with the linear)
+* *_keep8       tp_linear_layer and tp_swiglu_layer with their inputs kept in
+                8 bits for the backward
 
 The library is loaded lazily on first use and fails loudly if it is missing.
 """
@@ -32,8 +34,9 @@ from .ops import (A2AFFN, DG_FFN_COMP_ONLY, DG_FFN_FUSED_GATE, DG_FFN_SEPARATE_G
                   ffn_shape, gemm_fp8, tp_swiglu, tp_linear, tp_linear_backward, tp_linear_layer, TPLinear,
                   tp_swiglu_backward, tp_swiglu_layer, trace_begin, trace_end)
 from .few import moe_layer, moe_route, moe_swiglu, moe_swiglu_w4, w4_dequantize, w4_linear, w4_quantize
-from .fp8 import (FP8Linear, FP8NormLinear, RMSNorm, fp8_dequantize, fp8_linear, fp8_linear_backward, fp8_linear_layer,
-                  fp8_norm_linear_layer, fp8_quantize, rms_norm, rms_norm_backward, rms_norm_layer)
+from .fp8 import (FP8Linear, FP8NormLinear, RMSNorm, TPLinearKeep8, TPSwiGLUKeep8, fp8_dequantize, fp8_linear,
+                  fp8_linear_backward, fp8_linear_layer, fp8_norm_linear_layer, fp8_quantize, rms_norm,
+                  rms_norm_backward, rms_norm_layer, tp_linear_layer_keep8, tp_swiglu_layer_keep8)
 
 __all__ = [
     "A2AFFN", "DG_FFN_COMP_ONLY", "DG_FFN_FUSED_GATE", "DG_FFN_SEPARATE_GATE", "FFN_PARAM_NAMES", "a2a_combine",
@@ -44,5 +47,5 @@ __all__ = [
     "tp_linear_layer", "trace_begin", "trace_end", "moe_layer", "moe_route", "moe_swiglu", "moe_swiglu_w4",
     "w4_dequantize", "w4_linear", "w4_quantize", "FP8Linear", "FP8NormLinear", "RMSNorm", "fp8_dequantize", "fp8_linear",
     "fp8_linear_backward", "fp8_linear_layer", "fp8_norm_linear_layer", "fp8_quantize", "rms_norm", "rms_norm_backward",
-    "rms_norm_layer",
+    "rms_norm_layer", "TPLinearKeep8", "TPSwiGLUKeep8", "tp_linear_layer_keep8", "tp_swiglu_layer_keep8",
 ]

@@ -292,7 +292,7 @@ struct NormArgs {
 
 // A row a warp (kWarp) or CTA of T threads, C chunks of eight columns a thread, all read at once and kept in registers:
 // chunk i of thread t is i * T + t, so that 16 lanes hold a block of 128 columns.  Bound by memory: 8192 x 4096 with a
-// residual into 8 bits takes 35 us for 235 MB.
+// residual into 8 bits takes 38 us for 235 MB (6.2 TB/s).
 template <bool kWarp, int C, bool kFp8, int kMaxT>
 __global__ void __launch_bounds__(kMaxT) rms_norm_kernel(const NormArgs a) {
   __shared__ float part[1][32];

@@ -19,9 +19,11 @@ from torch.autograd.function import once_differentiable
 
 from ._lib import load
 from .few import BF16, _check, _device, _launch, _launch_with, _p, _size
+from .ops import tp_linear, tp_linear_backward, tp_swiglu, tp_swiglu_backward
 
 __all__ = ["fp8_quantize", "fp8_dequantize", "fp8_linear", "fp8_linear_backward", "FP8Linear", "fp8_linear_layer",
-           "rms_norm", "rms_norm_backward", "RMSNorm", "rms_norm_layer", "FP8NormLinear", "fp8_norm_linear_layer"]
+           "rms_norm", "rms_norm_backward", "RMSNorm", "rms_norm_layer", "FP8NormLinear", "fp8_norm_linear_layer",
+           "TPLinearKeep8", "tp_linear_layer_keep8", "TPSwiGLUKeep8", "tp_swiglu_layer_keep8"]
 
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
@@ -301,3 +303,52 @@ def fp8_norm_linear_layer(x: torch.Tensor, norm_weight: torch.Tensor, weight: to
     with a residual.  Between forward and backward it keeps h (bf16, the residual stream itself) and 8 bits a value of
     the norm's result and of the weight."""
     return FP8NormLinear.apply(x, norm_weight, weight, bias, residual, eps)
+
+
+# ------------------------------------------------------------------ bf16 layers that keep 8-bit activations
+
+class TPLinearKeep8(torch.autograd.Function):
+    """tp_linear, its input kept in 8 bits for the weight's gradient."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias):
+        y = tp_linear(x, weight, bias)
+        ctx.save_for_backward(*fp8_quantize(x), weight)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        codes, scales, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = tp_linear_backward(fp8_dequantize(codes, scales), weight, dy.contiguous(), need[0], need[1], need[2])
+        return g["x"], g["weight"], g["bias"]
+
+
+def tp_linear_layer_keep8(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
+    """tp_linear_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: the
+    weight's gradient is dy^T times what the codes stand for, the others are as there.  in % 16 == 0."""
+    return TPLinearKeep8.apply(x, weight, bias)
+
+
+class TPSwiGLUKeep8(torch.autograd.Function):
+    """tp_swiglu, its input kept in 8 bits; the backward recomputes [a|b] from these."""
+
+    @staticmethod
+    def forward(ctx, x_shards, w13, w2):
+        y = tp_swiglu(x_shards, w13, w2)
+        ctx.save_for_backward(*fp8_quantize(x_shards), w13, w2)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        codes, scales, w13, w2 = ctx.saved_tensors
+        g = tp_swiglu_backward(fp8_dequantize(codes, scales), w13, w2, dy.contiguous())
+        return g["x"], g["w13"], g["w2"]
+
+
+def tp_swiglu_layer_keep8(x_shards: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
+    """tp_swiglu_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: its
+    gradients are tp_swiglu_backward's at what the codes stand for.  d % 16 == 0."""
+    return TPSwiGLUKeep8.apply(x_shards, w13, w2)

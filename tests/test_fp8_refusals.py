@@ -136,7 +136,8 @@ def test_wrappers_refuse_before_the_device():
     x, pair = torch.zeros(2, 64, dtype=bf), (torch.zeros(2, 64).to(torch.float8_e4m3fn), torch.ones(2, 1).to(torch.float8_e8m0fnu))
     for call in (lambda: dg.fp8_quantize(x), lambda: dg.fp8_dequantize(*pair), lambda: dg.fp8_linear(x, pair),
                  lambda: dg.fp8_linear(pair, pair), lambda: dg.fp8_linear_backward(pair, pair, x), lambda: dg.rms_norm(x, x[0]),
-                 lambda: dg.rms_norm_backward(x, x[0], x), lambda: dg.fp8_linear_layer(x, x)):
+                 lambda: dg.rms_norm_backward(x, x[0], x), lambda: dg.fp8_linear_layer(x, x),
+                 lambda: dg.tp_linear_layer_keep8(x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
     with pytest.raises(TypeError):

@@ -341,6 +341,41 @@ def test_norm_linear_layer(residual):
         assert torch.equal(g[4], g[0])
 
 
+def test_tp_layers_that_keep_8_bits():
+    """The forward is the bf16 layer's bit for bit, the backward that of the values that the codes stand for."""
+    x, w, b, dy = leaf(randn((2, 33, 144), 1)), leaf(randn((176, 144), 2, 0.1)), leaf(randn((176,), 3)), randn((2, 33, 176), 4).to(DEV)
+    y = dg.tp_linear_layer_keep8(x, w, b)
+    assert torch.equal(y, dg.tp_linear(x.detach(), w.detach(), b.detach()))
+    g = torch.autograd.grad(y, (x, w, b), dy)
+    xv = dg.fp8_dequantize(*dg.fp8_quantize(x.detach()))
+    ref = dg.tp_linear_backward(xv, w.detach(), dy, need_db=True)
+    assert all(torch.equal(a, ref[n]) for a, n in zip(g, ("x", "weight", "bias")))
+    exact = f64(dy).reshape(66, 176).T @ held(x.detach().cpu().view(66, 144))[1]
+    within(g[1], (exact, fp8.product_bound(f64(dy).reshape(66, 176).T, f64(xv).reshape(66, 144), exact)), "weight")
+
+    x, w13, w2, dy = leaf(randn((2, 1, 16, 64), 5)), leaf(randn((2, 64, 64), 6, 0.2)), leaf(randn((64, 64), 7, 0.2)), randn((2, 1, 16, 64), 8).to(DEV)
+    y = dg.tp_swiglu_layer_keep8(x, w13, w2)
+    assert torch.equal(y, dg.tp_swiglu(x.detach(), w13.detach(), w2.detach()))
+    g = torch.autograd.grad(y, (x, w13, w2), dy)
+    ref = dg.tp_swiglu_backward(dg.fp8_dequantize(*dg.fp8_quantize(x.detach())), w13.detach(), w2.detach(), dy)
+    assert all(torch.equal(a, ref[n]) for a, n in zip(g, ("x", "w13", "w2")))
+
+
+@pytest.mark.parametrize("layer", ["fp8_linear_layer", "tp_linear_layer_keep8", "fp8_norm_linear_layer"])
+def test_what_a_layer_keeps(layer):
+    """Bytes held for the backward: one a value of the input (and one scale in 128), not two."""
+    x, w = leaf(randn((512, 256), 1)), leaf(randn((128, 256), 2))
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (kept.append(t), t)[1], lambda t: t):
+        if layer == "fp8_norm_linear_layer":
+            dg.fp8_norm_linear_layer(x, leaf(randn((256,), 3)), w)
+            kept = [t for t in kept if t.data_ptr() != x.data_ptr()]   # the residual stream itself
+        else:
+            getattr(dg, layer)(x, w)
+    held_bytes = sum(t.numel() * t.element_size() for t in kept if t.shape[:1] == (512,))
+    assert held_bytes == 512 * 256 + 512 * 2
+
+
 def test_layers_refuse_a_second_derivative():
     x, w = leaf(randn((4, 32), 1)), leaf(randn((16, 32), 2))
     (g,) = torch.autograd.grad(dg.fp8_linear_layer(x, w).sum(), (x,), create_graph=True)
