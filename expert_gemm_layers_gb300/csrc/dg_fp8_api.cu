@@ -85,18 +85,19 @@ dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t 
   return launched(launch_gemm_mx(b_mn_major, tile_n, ma, mb, md, p, dev, s), name);
 }
 
-// The product for few rows.
-dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, const void* x, const void* sx, const void* w, const void* sw,
-                     const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s, const char* name) {
+// The product for few rows; sx NULL: x is bf16.
+dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, const void* x, const void* sx,
+                     const void* w, const void* sw, const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s, const char* name) {
   CUtensorMap mw, mx;
   dg_status st;
   const uint64_t m = M, n = N, k = K;
   if ((st = make_map_3d(&mw, false, w, k, n, 1, k, n * k, 128, 128, 1, "weight codes")) != DG_OK) return st;
-  if ((st = make_map_3d(&mx, false, x, k, m, 1, k, m * k, 128, plan.nt, 1, "codes")) != DG_OK) return st;
+  if (sx && (st = make_map_3d(&mx, false, x, k, m, 1, k, m * k, 128, plan.nt, 1, "codes")) != DG_OK) return st;
   const double wn = static_cast<double>(N) * K;
   TraceScope trace(name, s, 2.0 * M * wn, static_cast<double>(M) * K + wn + 2.0 * M * N);
-  return launched(launch_mx_few(plan, mw, mx, sw, sx, bias, y, static_cast<int>(M), static_cast<int>(N),
-                                static_cast<int>(K), dev, s),
+  const int Mi = static_cast<int>(M), Ni = static_cast<int>(N), Ki = static_cast<int>(K);
+  return launched(sx ? launch_mx_few(plan, mw, mx, sw, sx, bias, y, Mi, Ni, Ki, dev, s)
+                     : launch_mx_few_bf16(plan, mw, x, sw, bias, y, Mi, Ni, Ki, dev, s),
                   name);
 }
 
@@ -197,6 +198,9 @@ dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_f, int64_t out_f, const vo
   DeviceInfo dev;
   if ((st = device_info_ws(&dev, ws, ws_bytes, "fp8_linear_bf16")) != DG_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const MxFewPlan few = mx_few_plan(rows, out_f, in_f, dev);
+  if (rows <= kMxFewBf16Rows)
+    return run_mx_few(few, rows, out_f, in_f, x, nullptr, w_codes, w_scales, bias, y, dev, s, "fp8_linear_few_bf16");
   uint8_t* codes = static_cast<uint8_t*>(ws) + DG_ERROR_BLOCK_BYTES;
   uint8_t* scales = static_cast<uint8_t*>(ws) + scales_at;
   {

@@ -443,8 +443,13 @@ struct MxFewPlan {
   bool better;
 };
 MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
-cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* sw, const void* sx, const void* bias, void* y, int M, int N, int K,
-                          const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* sw,
+                          const void* sx, const void* bias, void* y, int M, int N, int K, const DeviceInfo& dev,
+                          cudaStream_t s);
+// The same from x [M, K] in bf16, M <= kMxFewBf16Rows.
+constexpr int kMxFewBf16Rows = 4;
+cudaError_t launch_mx_few_bf16(const MxFewPlan& plan, const CUtensorMap& w, const void* x, const void* sw,
+                               const void* bias, void* y, int M, int N, int K, const DeviceInfo& dev, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights (dg_w4.cu)
 

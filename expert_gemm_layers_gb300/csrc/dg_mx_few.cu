@@ -10,7 +10,11 @@
 // front, 25 MB; 4 rows, 4096 to 28672: 22.5 us, 5.2 TB/s.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 bring
-// the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.
+// the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.  Where x comes in
+// bf16 and has at most four rows, they also quantise it into the stages, every CTA its
+// part of K: one launch fewer.  (With up to 32 rows that is too much work for four warps:
+// 24 rows, 14336 to 4096, took 19.7 us against 16.2 with a quantiser in front.)
+#include "dg_fp8.cuh"
 #include "dg_internal.h"
 #include "dg_mx.cuh"
 
@@ -18,7 +22,7 @@ namespace dg {
 
 namespace {
 
-template <int NT>
+template <int NT, bool kBf16>
 struct FewCfg {
   static constexpr int BM = 128;                 // features a CTA
   static constexpr int STAGES = NT == 16 ? 5 : NT == 64 ? 3 : 4;
@@ -29,6 +33,9 @@ struct FewCfg {
   static constexpr int SF_COLS = 16;             // W words at +0, x words at +8
   static constexpr int SF_BASE = NT < 32 ? 32 : NT;
   static constexpr int X_WORDS = (NT + 31) / 32;
+  static constexpr int LOAD_BYTES = W_BYTES + (kBf16 ? 0 : X_BYTES);  // by TMA, a stage
+  static constexpr int FULL_COUNT = kBf16 ? 2 : 1;  // arrivals: the producer, and the warp that writes x
+  static constexpr int X_ROWS = 4;               // bf16: most rows
   static constexpr uint32_t TMEM_COLS = SF_BASE + SF_BUFS * SF_COLS <= 128 ? 128 : 256;
   static constexpr int MAX_SPLIT = 8;
   // Sums that arrive from the cluster: [rank][feature of this CTA][ROW_F], padded against bank conflicts.
@@ -43,10 +50,12 @@ struct FewCfg {
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + RECV_BYTES + FEED_BYTES + BAR_BYTES;
   static constexpr uint32_t IDESC = ((NT >> 3) << 17) | (1u << 23) | ((BM >> 4) << 24);
   static_assert(NUM_BARS * 8 + 4 <= BAR_BYTES && SMEM_BYTES <= 232448, "shared memory");
+  static_assert(!kBf16 || STAGES >= 4, "x is quantised four stages at a time");
 };
 
 struct FewParams {
-  int32_t M, N, kb;            // rows of x, features, K blocks
+  int32_t M, N, K, kb;         // rows of x, features, columns and K blocks
+  const __nv_bfloat16* x;      // [M][K] (kBf16; then no codes and sx)
   const uint8_t *sx, *sw;      // [M][kb], [ceil(N/128)][kb]
   const __nv_bfloat16* bias;
   __nv_bfloat16* y;
@@ -67,10 +76,10 @@ __device__ __forceinline__ void dsmem_bulk_copy(uint32_t dst, uint32_t src, uint
                : "memory");
 }
 
-template <int NT>
-__global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
+template <int NT, bool kBf16>
+__global__ void __launch_bounds__(FewCfg<NT, kBf16>::NUM_THREADS)
     mx_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const FewParams p) {
-  using Cfg = FewCfg<NT>;
+  using Cfg = FewCfg<NT, kBf16>;
   extern __shared__ uint8_t smem_raw[];
 
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], Cfg::FULL_COUNT);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < Cfg::SF_BUFS; ++b) {
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
                                        (Cfg::BULK ? static_cast<uint32_t>(Cfg::ROW_F) * 4u : static_cast<uint32_t>(rows4) * 16u));
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
+    if (!kBf16) tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, Cfg::TMEM_COLS);
@@ -135,9 +144,9 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
       for (int i = 0; i < num_kb; ++i) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, p.err, SITE_EMPTY)) break;
         uint8_t* sw = stage_base + stage * Cfg::STAGE_BYTES;
-        mbar_arrive_expect_tx(&full[stage], Cfg::STAGE_BYTES);
+        mbar_arrive_expect_tx(&full[stage], Cfg::LOAD_BYTES);
         tma_load_3d(sw, &tmW, &full[stage], (kb0 + i) * 128, n0, 0);
-        tma_load_3d(sw + Cfg::W_BYTES, &tmX, &full[stage], (kb0 + i) * 128, t0, 0);
+        if (!kBf16) tma_load_3d(sw + Cfg::W_BYTES, &tmX, &full[stage], (kb0 + i) * 128, t0, 0);
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == Cfg::STAGES) {
@@ -199,31 +208,59 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
     int buf = 0;
     uint32_t phase = 0;
     bool ok = true;
-    ScaleFeed<NT, 1> feed;
-    feed.smem = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::RECV_BYTES);
-    feed.sa = p.sx;
-    feed.sb = p.sw + static_cast<int64_t>(blockIdx.x) * p.kb;  // a tile is one block of the weight's rows
-    feed.sb_n = 0;
-    feed.sb_k = 1;
-    feed.ka = p.kb;
-    feed.rows = p.M;
-    feed.blocks = 1;
-    feed.tid = static_cast<int>(threadIdx.x) - 64;
-    feed.wide = ((p.kb | kb0) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
-    feed.fetch(t0, 0, kb0, kb1);
-    int half = 0;
-    for (int kb = kb0; kb < kb1; kb += 16, half ^= 1) {
-      feed.publish(half);
-      if (kb + 16 < kb1) feed.fetch(t0, 0, kb + 16, kb1);
-      for (int g = 0; g < 4 && kb + 4 * g < kb1; ++g) {
-        const uint32_t ww = feed.block(half, g, 0);
-        const uint32_t a[4] = {ww, ww, ww, ww};
-        uint32_t b[4] = {kScaleOnes, kScaleOnes, kScaleOnes, kScaleOnes};
+    const uint8_t* sw = p.sw + static_cast<int64_t>(blockIdx.x) * p.kb;  // a tile is one block of the weight's rows
+    if (kBf16) {
+      // x in bf16: a warp takes one of four K blocks (a scale word), four columns a lane, the next four blocks asked for
+      // while these are turned into codes
+      const int q = warp - 2;
+      uint32_t* words = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::RECV_BYTES);  // [2][NT]
+      uint2 v[Cfg::X_ROWS];
+      uint32_t ww;
+      auto fetch = [&](int kb) {
+        const int c = (kb + q) * 128 + 4 * lane;
 #pragma unroll
-        for (int j = 0; j < Cfg::X_WORDS; ++j) b[j] = feed.row(half, g, (lane + 32 * j) & (NT - 1));
-        // after a failed wait the warp only keeps the others company at the feed's barrier
+        for (int r = 0; r < Cfg::X_ROWS; ++r)
+          v[r] = kb + q < kb1 && c < p.K && r < rows
+                     ? __ldca(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t0 + r) * p.K + c))
+                     : make_uint2(0u, 0u);
+        ww = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          ww |= static_cast<uint32_t>(kb + i < kb1 ? __ldcg(sw + kb + i) : 127) << (8 * i);
+      };
+      fetch(kb0);
+      int half = 0;
+      for (int kb = kb0; kb < kb1; kb += 4, half ^= 1) {
+        const uint32_t a[4] = {ww, ww, ww, ww};
+        uint32_t codes[Cfg::X_ROWS];
+#pragma unroll
+        for (int r = 0; r < Cfg::X_ROWS; ++r) {
+          const uint32_t m2 = __vmaxu2(v[r].x & 0x7fff7fffu, v[r].y & 0x7fff7fffu);
+          const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16)) << 16);
+          const float2 lo = unpack_bf16x2(v[r].x), hi = unpack_bf16x2(v[r].y);
+          const float k = scale_inverse(byte);
+          codes[r] = byte == kScaleNan ? kCodeNan4 : e4m3x4(lo.x * k, lo.y * k, hi.x * k, hi.y * k);
+          if (lane == 0) reinterpret_cast<uint8_t*>(words + half * NT + r)[q] = static_cast<uint8_t>(byte);
+        }
+        if (kb + 4 < kb1) fetch(kb + 4);
+        const int i = kb - kb0 + q;  // the block's place in the ring
+        if (i < num_kb) {
+          const int stage = i % Cfg::STAGES;
+          // after a failed wait the warp only keeps the others company at the barrier below
+          ok = ok && warp_wait(&empty[stage], (static_cast<uint32_t>(i / Cfg::STAGES) & 1u) ^ 1u, p.err, SITE_EMPTY);
+          uint8_t* xt = stage_base + stage * Cfg::STAGE_BYTES + Cfg::W_BYTES;
+#pragma unroll
+          for (int r = 0; r < Cfg::X_ROWS; ++r)
+            if (ok && r < rows)
+              *reinterpret_cast<uint32_t*>(xt + r * 128 + (((lane >> 2) ^ r) << 4) + 4 * (lane & 3)) = codes[r];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&full[stage]);
+        }
+        asm volatile("bar.sync 2, 128;" ::: "memory");  // the rows' scale words
+        const uint32_t b[4] = {lane < rows ? words[half * NT + lane] : kScaleOnes, kScaleOnes, kScaleOnes, kScaleOnes};
         ok = ok && warp_wait(&sf_empty[buf], phase ^ 1u, p.err, SITE_SF_EMPTY);
-        if (!ok) break;
+        if (!ok) continue;
         tc_fence_after_sync();
         const uint32_t at = lane_addr + static_cast<uint32_t>(Cfg::SF_BASE + buf * Cfg::SF_COLS);
         tmem_st_32x32b_x4(at, a);
@@ -235,6 +272,46 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
         if (++buf == Cfg::SF_BUFS) {
           buf = 0;
           phase ^= 1u;
+        }
+      }
+    } else {
+      ScaleFeed<NT, 1> feed;
+      feed.smem = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::RECV_BYTES);
+      feed.sa = p.sx;
+      feed.sb = sw;
+      feed.sb_n = 0;
+      feed.sb_k = 1;
+      feed.ka = p.kb;
+      feed.rows = p.M;
+      feed.blocks = 1;
+      feed.tid = static_cast<int>(threadIdx.x) - 64;
+      feed.wide = ((p.kb | kb0) & 15) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 15) == 0;
+      feed.fetch(t0, 0, kb0, kb1);
+      int half = 0;
+      for (int kb = kb0; kb < kb1; kb += 16, half ^= 1) {
+        feed.publish(half);
+        if (kb + 16 < kb1) feed.fetch(t0, 0, kb + 16, kb1);
+        for (int g = 0; g < 4 && kb + 4 * g < kb1; ++g) {
+          const uint32_t ww = feed.block(half, g, 0);
+          const uint32_t a[4] = {ww, ww, ww, ww};
+          uint32_t b[4] = {kScaleOnes, kScaleOnes, kScaleOnes, kScaleOnes};
+  #pragma unroll
+          for (int j = 0; j < Cfg::X_WORDS; ++j) b[j] = feed.row(half, g, (lane + 32 * j) & (NT - 1));
+          // after a failed wait the warp only keeps the others company at the feed's barrier
+          ok = ok && warp_wait(&sf_empty[buf], phase ^ 1u, p.err, SITE_SF_EMPTY);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint32_t at = lane_addr + static_cast<uint32_t>(Cfg::SF_BASE + buf * Cfg::SF_COLS);
+          tmem_st_32x32b_x4(at, a);
+          tmem_st_32x32b_x4(at + 8, b);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sf_full[buf]);
+          if (++buf == Cfg::SF_BUFS) {
+            buf = 0;
+            phase ^= 1u;
+          }
         }
       }
     }
@@ -334,11 +411,11 @@ __global__ void __launch_bounds__(FewCfg<NT>::NUM_THREADS)
 
 int few_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
-template <int NT>
+template <int NT, bool kBf16 = false>
 cudaError_t few_launch(const CUtensorMap& w, const CUtensorMap& x, const FewParams& p, int split, const DeviceInfo& dev,
                        cudaStream_t s) {
-  using Cfg = FewCfg<NT>;
-  auto kern = mx_few_kernel<NT>;
+  using Cfg = FewCfg<NT, kBf16>;
+  auto kern = mx_few_kernel<NT, kBf16>;
   cudaError_t e = smem_limit_once(reinterpret_cast<const void*>(kern), Cfg::SMEM_BYTES, dev.device);
   if (e != cudaSuccess) return e;
   return launch_pdl_clusters_z(kern, dim3((p.N + Cfg::BM - 1) / Cfg::BM, (p.M + NT - 1) / NT, split), dim3(Cfg::NUM_THREADS),
@@ -358,7 +435,7 @@ MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
   // 12.8 us where 48 of 5 took 10.3) and have two K blocks each; eight ways for long K only (4096 to 4096, one row:
   // 7.6 us four ways, 8.2 eight; 14336 to 4096, 24 rows: 16.4 and 16.6).
   plan.split = 1;
-  for (int c = 2; c <= FewCfg<16>::MAX_SPLIT; c *= 2)
+  for (int c = 2; c <= FewCfg<16, false>::MAX_SPLIT; c *= 2)
     if (tiles * c * 100 <= places * 85 && kb >= (c == 8 ? 64 : 2 * c)) plan.split = c;
   // Above 64 rows the tiles of dg_mx.cuh may take less time.  Both sides measured at 11, 32 and 112 K blocks and 96 to 512
   // rows: here about 11 us and 0.3 us a K block of a CTA, there 7.3 us and a turn's K blocks at 0.2 us (tiles of 128
@@ -370,16 +447,26 @@ MxFewPlan mx_few_plan(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev) {
   return plan;
 }
 
-cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* sw, const void* sx, const void* bias, void* y, int M, int N, int K,
-                          const DeviceInfo& dev, cudaStream_t s) {
-  const FewParams p{M, N, (K + 127) / 128, static_cast<const uint8_t*>(sx), static_cast<const uint8_t*>(sw),
-                    static_cast<const __nv_bfloat16*>(bias), static_cast<__nv_bfloat16*>(y), dev.err};
+cudaError_t launch_mx_few(const MxFewPlan& plan, const CUtensorMap& w, const CUtensorMap& x, const void* sw,
+                          const void* sx, const void* bias, void* y, int M, int N, int K, const DeviceInfo& dev,
+                          cudaStream_t s) {
+  const FewParams p{M, N, K, (K + 127) / 128, nullptr, static_cast<const uint8_t*>(sx),
+                    static_cast<const uint8_t*>(sw), static_cast<const __nv_bfloat16*>(bias),
+                    static_cast<__nv_bfloat16*>(y), dev.err};
   switch (plan.nt) {
     case 16: return few_launch<16>(w, x, p, plan.split, dev, s);
     case 32: return few_launch<32>(w, x, p, plan.split, dev, s);
     case 64: return few_launch<64>(w, x, p, plan.split, dev, s);
     default: return few_launch<128>(w, x, p, plan.split, dev, s);
   }
+}
+
+cudaError_t launch_mx_few_bf16(const MxFewPlan& plan, const CUtensorMap& w, const void* x, const void* sw,
+                               const void* bias, void* y, int M, int N, int K, const DeviceInfo& dev, cudaStream_t s) {
+  const FewParams p{M, N, K, (K + 127) / 128, static_cast<const __nv_bfloat16*>(x), nullptr,
+                    static_cast<const uint8_t*>(sw), static_cast<const __nv_bfloat16*>(bias),
+                    static_cast<__nv_bfloat16*>(y), dev.err};
+  return few_launch<16, true>(w, w, p, plan.split, dev, s);
 }
 
 }  // namespace dg

@@ -146,6 +146,17 @@ def test_linear_from_bf16_and_leading_dimensions():
     assert dg.fp8_linear(x.to(DEV)[:0], w8).shape == (0, 3, 160)
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 17, 200])
+@pytest.mark.parametrize("K,N", [(16, 16), (144, 240), (640, 400), (2064, 272), (8208, 144)])
+def test_bf16_rows_give_what_their_codes_give(rows, K, N):
+    """Up to four rows the product quantises x itself: the same codes, the same sums."""
+    x = odd_values(rows, K, rows + K)
+    w8, b = dg.fp8_quantize(randn((N, K), 2, K**-0.5).to(DEV), 128), randn((N,), 3).to(DEV)
+    y = dg.fp8_linear(x.to(DEV), w8, b)
+    assert torch.equal(y.view(torch.int16), dg.fp8_linear(dg.fp8_quantize(x.to(DEV)), w8, b).view(torch.int16)) or \
+        torch.equal(torch.nan_to_num(y, 7.0), torch.nan_to_num(dg.fp8_linear(dg.fp8_quantize(x.to(DEV)), w8, b), 7.0))
+
+
 @pytest.mark.parametrize("K", [272, 2048])
 def test_parts_of_the_rows(K):
     """Activations sliced by rows: their scales begin at any byte."""
