@@ -38,21 +38,33 @@ def _pair(pair, what: str):
     return pair
 
 
-def _need_rows(pair, what: str, index: int) -> tuple:
-    """Checks activations in 8 bits; returns (codes, scales)."""
+# As in few.py: one expression where nothing is wrong, the exact checks only to say what is.
+
+def _held(pair, what: str) -> tuple:
+    """Checks activations in 8 bits; returns (codes, scales, device index, leading sizes, rows, d)."""
     codes, scales = _pair(pair, what)
-    _check(codes, what + " codes", E4M3, codes.shape if isinstance(codes, torch.Tensor) else None, index)
-    _check(scales, what + " scales", E8M0, (*codes.shape[:-1], _blocks(_size(codes, -1))), index)
-    return codes, scales
+    if isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and codes.dim():
+        shape, index = codes.shape, codes.get_device()
+        lead, d = shape[:-1], shape[-1]
+        if codes.dtype is E4M3 and scales.dtype is E8M0 and 0 <= index == scales.get_device() and \
+                scales.shape == (*lead, (d + 127) // 128) and codes.is_contiguous() and scales.is_contiguous():
+            return codes, scales, index, lead, codes.numel() // d if d else 0, d
+    index = _device(codes, f"{what} codes", E4M3)
+    _check(codes, f"{what} codes", E4M3, codes.shape, index)
+    _check(scales, f"{what} scales", E8M0, (*codes.shape[:-1], _blocks(_size(codes, -1))), index)
+    raise ValueError(f"{what} codes must have a last dimension")
 
 
 def _need_weight(pair, what: str, in_f: int, index: int) -> tuple:
-    """Checks a weight [out, in_f] in 8 bits; returns (codes, scales)."""
+    """Checks a weight [out, in_f] in 8 bits; returns (codes, scales, out)."""
     codes, scales = _pair(pair, what)
     out_f = _size(codes, 0)
-    _check(codes, what + " codes", E4M3, (out_f, in_f), index)
-    _check(scales, what + " scales", E8M0, (_blocks(out_f), _blocks(in_f)), index)
-    return codes, scales
+    if not (out_f and isinstance(scales, torch.Tensor) and codes.dtype is E4M3 and scales.dtype is E8M0
+            and codes.shape == (out_f, in_f) and scales.shape == ((out_f + 127) // 128, (in_f + 127) // 128)
+            and codes.get_device() == index == scales.get_device() and codes.is_contiguous() and scales.is_contiguous()):
+        _check(codes, f"{what} codes", E4M3, (out_f, in_f), index)
+        _check(scales, f"{what} scales", E8M0, (_blocks(out_f), _blocks(in_f)), index)
+    return codes, scales, out_f
 
 
 def _rows(t) -> int:
@@ -116,25 +128,23 @@ def fp8_linear(x, weight, bias: torch.Tensor | None = None, out: torch.Tensor | 
 
     x: activations in 8 bits (codes, scales), as fp8_quantize and rms_norm(..., fp8=True) return them, or bf16
     [..., in], which is quantised on the way.  weight: (codes, scales) of fp8_quantize(W [out, in], 128).  Sums in
-    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, or dg_fp8_linear_bf16_workspace_bytes; its error block zeroed; default:
-    this stream's own) is not shared by calls that run at the same time."""
-    lib, plain = load(), isinstance(x, torch.Tensor)
-    if plain:
+    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, or for bf16
+    dg_fp8_linear_bf16_workspace_bytes; its error block zeroed; default: this stream's own) is not shared by calls
+    that run at the same time."""
+    lib = load()
+    if isinstance(x, torch.Tensor):
         index, lead, rows, in_f = _activations(x, "x")
-        xc = x
+        xc, xs = x, None
     else:
-        index = _device(_pair(x, "x")[0], "x codes", E4M3)
-        xc, xs = _need_rows(x, "x", index)
-        lead, rows, in_f = xc.shape[:-1], _rows(xc), _size(xc, -1)
-    wc, wscale = _need_weight(weight, "weight", in_f, index)
-    out_f = wc.shape[0]
+        xc, xs, index, lead, rows, in_f = _held(x, "x")
+    wc, wscale, out_f = _need_weight(weight, "weight", in_f, index)
     if bias is not None:
         _check(bias, "bias", BF16, (out_f,), index)
     if out is None:
         out = torch.empty((*lead, out_f), dtype=BF16, device=xc.device)
     else:
         _check(out, "out", BF16, (*lead, out_f), index)
-    if plain:
+    if xs is None:
         _launch_with(workspace, lib.dg_fp8_linear_bf16_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear_bf16, index,
                      rows, in_f, out_f, x.data_ptr(), wc.data_ptr(), wscale.data_ptr(), _p(bias), out.data_ptr())
     else:
@@ -156,13 +166,13 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
     if x is None and (need_dw or weight is None) or weight is None and need_dx:
         raise ValueError("x is needed for the weight's gradient, weight for that of x")
     if x is not None:
-        xc, xs = _need_rows(x, "x", index)
-        if xc.shape[:-1] != lead:
-            raise ValueError(f"x codes have shape {tuple(xc.shape)} beside dy {tuple(dy.shape)}")
+        xc, xs, at, *_ = _held(x, "x")
+        if xc.shape[:-1] != lead or at != index:
+            raise ValueError(f"x codes have shape {tuple(xc.shape)} on device {at} beside dy {tuple(dy.shape)} on {index}")
     in_f = _size(xc if xc is not None else _pair(weight, "weight")[0], -1)
     if weight is not None:
-        wc, ws = _need_weight(weight, "weight", in_f, index)
-        if wc.shape[0] != out_f:
+        wc, ws, n = _need_weight(weight, "weight", in_f, index)
+        if n != out_f:
             raise ValueError(f"weight codes have shape {tuple(wc.shape)} beside dy {tuple(dy.shape)}")
     new = lambda shape: torch.empty(shape, dtype=BF16, device=dy.device)
     g = dict(x=new((*lead, in_f)) if need_dx else None, weight=new((out_f, in_f)) if need_dw else None,
