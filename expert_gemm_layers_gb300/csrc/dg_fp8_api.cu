@@ -87,7 +87,8 @@ dg_status run_mx(bool b_mn_major, bool sb_turned, int64_t M, int64_t N, int64_t 
 
 // The product for few rows; sx NULL: x is bf16.
 dg_status run_mx_few(const MxFewPlan& plan, int64_t M, int64_t N, int64_t K, const void* x, const void* sx,
-                     const void* w, const void* sw, const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s, const char* name) {
+                     const void* w, const void* sw, const void* bias, void* y, const DeviceInfo& dev, cudaStream_t s,
+                     const char* name) {
   CUtensorMap mw, mx;
   dg_status st;
   const uint64_t m = M, n = N, k = K;
