@@ -182,13 +182,23 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
     return g
 
 
+def _pair_or_none(codes, scales):
+    return None if codes is None else (codes, scales)
+
+
+_NO_PAIR = (None, None)
+
+
 class FP8Linear(torch.autograd.Function):
-    """Autograd wrapper of fp8_linear on bf16 tensors: quantises both operands and keeps them in 8 bits."""
+    """Autograd wrapper of fp8_linear on bf16 tensors: quantises both operands and keeps, in 8 bits, those that the
+    gradients asked for read."""
 
     @staticmethod
     def forward(ctx, x, weight, bias):
         x8, w8 = fp8_quantize(x), fp8_quantize(weight, 128)
-        ctx.save_for_backward(*x8, *w8)
+        need_x, need_w, _ = ctx.needs_input_grad
+        # one of the two at least: the bias's gradient alone takes its sizes from there
+        ctx.save_for_backward(*(x8 if need_w else _NO_PAIR), *(w8 if need_x or not need_w else _NO_PAIR))
         return fp8_linear(x8, w8, bias)
 
     @staticmethod
@@ -196,14 +206,14 @@ class FP8Linear(torch.autograd.Function):
     def backward(ctx, dy):
         xc, xs, wc, ws = ctx.saved_tensors
         need = ctx.needs_input_grad
-        g = fp8_linear_backward((xc, xs), (wc, ws), dy.contiguous(), need[0], need[1], need[2])
+        g = fp8_linear_backward(_pair_or_none(xc, xs), _pair_or_none(wc, ws), dy.contiguous(), *need)
         return g["x"], g["weight"], g["bias"]
 
 
 def fp8_linear_layer(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable y = x @ weight^T (+ bias): x [..., in], weight [out, in] and bias bf16, products in block-scaled
-    e4m3.  Of x the backward keeps 8 bits a value; its gradients are fp8_linear_backward's, passed through the
-    quantisers."""
+    e4m3.  Of x the backward keeps 8 bits a value, nothing where the weight is frozen; its gradients are
+    fp8_linear_backward's, passed through the quantisers."""
     return FP8Linear.apply(x, weight, bias)
 
 
@@ -289,7 +299,7 @@ class FP8NormLinear(torch.autograd.Function):
         n8, h = normed if residual is not None else (normed, x)
         w8 = fp8_quantize(weight, 128)
         y = fp8_linear(n8, w8, bias)
-        ctx.save_for_backward(h, norm_weight, *n8, *w8)
+        ctx.save_for_backward(h, norm_weight, *(n8 if ctx.needs_input_grad[2] else _NO_PAIR), *w8)
         return y if residual is None else (y, h)
 
     @staticmethod
@@ -300,7 +310,7 @@ class FP8NormLinear(torch.autograd.Function):
         if dy is None:
             dy = torch.zeros((*h.shape[:-1], wc.shape[0]), dtype=BF16, device=h.device)
         through = need_x or need_nw or need_r
-        g = fp8_linear_backward((nc, ns), (wc, ws), dy.contiguous(), through, need_w, need_b)
+        g = fp8_linear_backward(_pair_or_none(nc, ns), (wc, ws), dy.contiguous(), through, need_w, need_b)
         dx = dnw = dr = None
         if through:
             dx, dnw, dr = _norm_grads(h, norm_weight, g["x"], dh, ctx.eps, (need_x, need_nw, need_r))
@@ -311,7 +321,7 @@ def fp8_norm_linear_layer(x: torch.Tensor, norm_weight: torch.Tensor, weight: to
                           bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, eps: float = 1e-6):
     """Differentiable rms_norm(x + residual) @ weight^T (+ bias), the norm's result in block-scaled e4m3: y, or (y, h)
     with a residual.  Between forward and backward it keeps h (bf16, the residual stream itself) and 8 bits a value of
-    the norm's result and of the weight."""
+    the norm's result (where the weight is trained) and of the weight."""
     return FP8NormLinear.apply(x, norm_weight, weight, bias, residual, eps)
 
 
@@ -323,7 +333,7 @@ class TPLinearKeep8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
         y = tp_linear(x, weight, bias)
-        ctx.save_for_backward(*fp8_quantize(x), weight)
+        ctx.save_for_backward(*(fp8_quantize(x) if ctx.needs_input_grad[1] else _NO_PAIR), weight)
         return y
 
     @staticmethod
@@ -331,13 +341,16 @@ class TPLinearKeep8(torch.autograd.Function):
     def backward(ctx, dy):
         codes, scales, weight = ctx.saved_tensors
         need = ctx.needs_input_grad
-        g = tp_linear_backward(fp8_dequantize(codes, scales), weight, dy.contiguous(), need[0], need[1], need[2])
+        # with a frozen weight nothing reads x: its place only gives the sizes
+        x = dy.new_empty((*dy.shape[:-1], weight.shape[1])) if codes is None else fp8_dequantize(codes, scales)
+        g = tp_linear_backward(x, weight, dy.contiguous(), *need)
         return g["x"], g["weight"], g["bias"]
 
 
 def tp_linear_layer_keep8(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """tp_linear_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: the
-    weight's gradient is dy^T times what the codes stand for, the others are as there.  in % 16 == 0."""
+    weight's gradient is dy^T times what the codes stand for, the others are as there.  Of x nothing is kept where the
+    weight is frozen.  in % 16 == 0."""
     return TPLinearKeep8.apply(x, weight, bias)
 
 

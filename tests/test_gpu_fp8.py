@@ -392,3 +392,27 @@ def test_layers_refuse_a_second_derivative():
     (g,) = torch.autograd.grad(dg.fp8_linear_layer(x, w).sum(), (x,), create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+@pytest.mark.parametrize("layer", ["fp8_linear_layer", "tp_linear_layer_keep8", "fp8_norm_linear_layer"])
+@pytest.mark.parametrize("trained", ["x", "w", "b", "xw", "xb", "wb"])
+def test_layers_with_frozen_inputs(layer, trained):
+    """The gradients that are asked for are bit for bit those of the layer with everything trained; of x nothing more
+    than the layer's input is kept where the weight is frozen."""
+    x, w, b, dy = randn((70, 272), 1), randn((176, 272), 2, 0.1), randn((176,), 3), randn((70, 176), 4).to(DEV)
+    nw = randn((272,), 5).to(DEV)
+
+    def grads(names):
+        t = {n: v.to(DEV).requires_grad_(n in names) for n, v in (("x", x), ("w", w), ("b", b))}
+        kept = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda v: (kept.append(v), v)[1], lambda v: v):
+            if layer == "fp8_norm_linear_layer":
+                y = dg.fp8_norm_linear_layer(t["x"], nw, t["w"], t["b"])
+            else:
+                y = getattr(dg, layer)(t["x"], t["w"], t["b"])
+        if "w" not in names:
+            assert not [v for v in kept if v.shape[:1] == (70,) and v.data_ptr() != t["x"].data_ptr()]
+        return dict(zip(names, torch.autograd.grad(y, [t[n] for n in names], dy)))
+
+    every, some = grads("xwb"), grads(trained)
+    assert all(torch.equal(some[n], every[n]) for n in trained)
