@@ -363,10 +363,12 @@ __global__ void __launch_bounds__(FewCfg<NT, kBf16>::NUM_THREADS)
     }
     tc_fence_before_sync();
     __syncwarp();
-    cluster_arrive();  // this thread has sent all it sends
-    if (!warp_wait(arrived, 0, p.err, SITE_CLOAD)) {
-      __nanosleep(100000);  // failed: let what peers still send land before this CTA's memory goes back
-    } else if (!aborted) {
+    const bool summed = warp_wait(arrived, 0, p.err, SITE_CLOAD);
+    if (!summed) __nanosleep(100000);  // failed: let what is still under way land before shared memory goes back
+    // Only now: once all CTAs have what they receive, every bulk copy has read its source in the sender's stages too.
+    // Its completion is counted at the receiver alone, so an arrival right after sending would let the sender go.
+    cluster_arrive();
+    if (summed && !aborted) {
       // four rows of two neighbouring features a thread: a warp stores 128 bytes of each row
       const int pairs = f_count / 2;
       for (int u = static_cast<int>(threadIdx.x) - 64; u < rows4 * pairs; u += 128) {
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(FewCfg<NT, kBf16>::NUM_THREADS)
     cluster_wait();
     cluster_arrive();
   }
-  cluster_wait();  // no CTA leaves while a peer may still send to it
+  cluster_wait();  // no CTA leaves while a peer may still send to it or copy out of it
   if (warp == 1) {
     __syncwarp();
     tc_fence_after_sync();
