@@ -125,9 +125,10 @@ static __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Cluster barrier in two halves: every thread of the cluster arrives, and waits later.  No memory is passed on by it
-// (barriers' initialisation has a fence of its own), so the arrival is relaxed: a releasing one first waits for the
-// thread's accesses, 2000 cycles in a prologue that has just asked for memory.
+// Cluster barrier in two halves: every thread of the cluster arrives, and waits later.  The arrival is relaxed, for
+// where no memory is passed on (barriers' initialisation has a fence of its own) and none of the thread's accesses to
+// a peer can still be under way: a releasing one first waits for the thread's accesses, 2000 cycles in a prologue that
+// has just asked for memory.
 static __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
 }
@@ -520,10 +521,11 @@ __global__ void __launch_bounds__(MxCfg<kBMN, kBN>::NUM_THREADS, 1)
     __syncwarp();
   }
 
+  // The last arrivals on the leader's `tempty` have no reader; this barrier, whose arrival releases, is what keeps the
+  // leader's shared memory until they have landed.
   griddep_launch_dependents();
   tc_fence_before_sync();
-  cluster_arrive();
-  cluster_wait();
+  cluster_sync_all();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after_sync();
