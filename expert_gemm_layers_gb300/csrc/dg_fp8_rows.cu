@@ -215,8 +215,10 @@ __device__ __forceinline__ void row_sum(float (&v)[kSums], float (*part)[32]) {
   }
 }
 
-// A row whose squares overflow binary32 is summed as (h 2^-64)^2 instead.
+// A row whose mean square and eps together overflow binary32 is summed as (h 2^-64)^2 instead, beside eps 2^-128.
 constexpr float kShrink = 5.42101086242752217e-20f;  // 2^-64
+__device__ __forceinline__ bool overflows(float mean) { return !(mean < __int_as_float(0x7f800000)); }
+__device__ __forceinline__ float shrunk_mean(float sum, float n, float eps) { return sum / n + eps * kShrink * kShrink; }
 constexpr int kWarpRows = 8;                          // rows of a CTA where a warp takes one
 
 struct NormArgs {
@@ -268,9 +270,10 @@ __global__ void __launch_bounds__(kMaxT) rms_norm_kernel(const NormArgs a) {
   }
   row_sum<kWarp, 1>(sum, part);
   const float n = static_cast<float>(a.d);
-  float rstd = 1.0f / sqrtf(sum[0] / n + a.eps);
+  const float mean = sum[0] / n + a.eps;
+  float rstd = 1.0f / sqrtf(mean);
   float pre = 1.0f;
-  if (!(sum[0] < __int_as_float(0x7f800000))) {  // the same for all threads of the row
+  if (overflows(mean)) {  // the same for all threads of the row
     sum[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kMaxT) rms_norm_kernel(const NormArgs a) {
       for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[e] * kShrink, v[e] * kShrink, sum[0]);
     }
     row_sum<kWarp, 1>(sum, part);
-    rstd = 1.0f / sqrtf(sum[0] / n);  // eps is far below the last bit
+    rstd = 1.0f / sqrtf(shrunk_mean(sum[0], n, a.eps));
     pre = kShrink;
   }
 #pragma unroll
@@ -389,11 +392,12 @@ __global__ void __launch_bounds__(kMaxT, kWarp ? 2 : C == 1 ? 3 : 1) rms_norm_bw
     };
     float s[2];
     sums(1.0f, s);
-    float pre = 1.0f, rstd = 1.0f / sqrtf(s[0] / n + a.eps);
-    if (!(s[0] < __int_as_float(0x7f800000))) {
+    const float square = s[0] / n + a.eps;
+    float pre = 1.0f, rstd = 1.0f / sqrtf(square);
+    if (overflows(square)) {
       pre = kShrink;
       sums(pre, s);
-      rstd = 1.0f / sqrtf(s[0] / n);
+      rstd = 1.0f / sqrtf(shrunk_mean(s[0], n, a.eps));
     }
     // with n_h = h pre rstd (the normalised row): dx = rstd pre (dy w - n_h mean(dy w n_h)) + dh
     const float2 mean = splat2(-s[1] * rstd / n), out = splat2(rstd * pre);
@@ -469,8 +473,9 @@ __global__ void __launch_bounds__(256) norm_bwd_rows_kernel(const NormBwdArgs a,
       }
     }
     row_sum<false, 2>(s, part);
-    rstd = 1.0f / sqrtf(pre == 1.0f ? s[0] / n + a.eps : s[0] / n);
-    if (pre != 1.0f || s[0] < __int_as_float(0x7f800000)) break;
+    const float square = pre == 1.0f ? s[0] / n + a.eps : shrunk_mean(s[0], n, a.eps);
+    rstd = 1.0f / sqrtf(square);
+    if (pre != 1.0f || !overflows(square)) break;
     pre = kShrink;
   }
   if (threadIdx.x == 0 && !error_word(a.err)) coef[row] = make_float2(rstd * pre, s[1] * rstd / n);
