@@ -324,7 +324,8 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
   }
   if (d_bias && !dx) {
     TraceScope trace("fp8_linear_bwd_db", s, 0.0, 2.0 * yn + 2.0 * out_f);
-    return launched(launch_column_sum(dy, d_bias, 1, static_cast<int>(rows), static_cast<int>(out_f), 0, out_f, dev, s),
+    return launched(launch_fp8_quantize_sum(dy, nullptr, nullptr, d_bias, reinterpret_cast<float*>(base + l.sums), rows,
+                                            static_cast<int>(out_f), dev.err, s),
                     "fp8_linear_bwd");
   }
   return DG_OK;

@@ -560,7 +560,9 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 // ------------------------------------------------------------------ quantise a gradient and sum its columns
 
 // Blocks of 1 x 128 as quant_rows_kernel, one CTA taking a column block and every gridDim.y-th group of 16 rows, so that
-// the column sums of what it reads stay in registers: part[blockIdx.y][column].
+// the column sums of what it reads stay in registers: part[blockIdx.y][column].  Without kCodes the sums alone, added up
+// in the same order.
+template <bool kCodes>
 __global__ void __launch_bounds__(kThreads) quant_rows_sum_kernel(const __nv_bfloat16* __restrict__ x, uint8_t* __restrict__ q,
                                                                   uint8_t* __restrict__ scale, float* __restrict__ part,
                                                                   int64_t rows, int K, int nb) {
@@ -583,11 +585,13 @@ __global__ void __launch_bounds__(kThreads) quant_rows_sum_kernel(const __nv_bfl
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int64_t r = r0 + i * step + group;
-      const uint32_t byte = scale_byte(max16(amax_bits8(v[i])) << 16);
       float f[8];
       unpack8(v[i], f);
-      if (r < rows && c < K) *reinterpret_cast<uint2*>(q + r * K + c) = codes8(f, byte);
-      if (r < rows && sub == 0) scale[r * nb + blockIdx.x] = static_cast<uint8_t>(byte);
+      if (kCodes) {
+        const uint32_t byte = scale_byte(max16(amax_bits8(v[i])) << 16);
+        if (r < rows && c < K) *reinterpret_cast<uint2*>(q + r * K + c) = codes8(f, byte);
+        if (r < rows && sub == 0) scale[r * nb + blockIdx.x] = static_cast<uint8_t>(byte);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += f[e];
     }
@@ -725,9 +729,9 @@ int fp8_quantize_sum_parts(int64_t rows, int K) {
 cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
                                     int K, const uint32_t* err, cudaStream_t s) {
   const int nb = (K + 127) / 128, parts = fp8_quantize_sum_parts(rows, K);
-  cudaError_t e = launch_pdl(quant_rows_sum_kernel, dim3(nb, parts), dim3(kThreads), 0, s,
-                             static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(codes),
-                             static_cast<uint8_t*>(scales), part, rows, K, nb);
+  const auto kern = codes ? quant_rows_sum_kernel<true> : quant_rows_sum_kernel<false>;
+  cudaError_t e = launch_pdl(kern, dim3(nb, parts), dim3(kThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
+                             static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), part, rows, K, nb);
   if (e != cudaSuccess) return e;
   return launch_pdl(sum_parts_kernel, dim3((K + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(part),
                     static_cast<__nv_bfloat16*>(sums), parts, K, err);

@@ -412,8 +412,8 @@ cudaError_t launch_fp8_dequantize(const void* codes, const void* scales, void* x
 // Codes [rows, K] -> [K, rows]; rows and K multiples of 16, rows <= 65535 * 128.
 cudaError_t launch_transpose_codes(const void* in, void* out, int rows, int K, cudaStream_t s);
 
-// x [rows, K] to codes and scales of 1 x 128 blocks and sums [K] = column sums of x, read once;
-// part [fp8_quantize_sum_parts][K] binary32.  err here and below: the error word of the call's workspace.
+// x [rows, K] to codes and scales of 1 x 128 blocks and sums [K] = column sums of x, read once; codes and scales NULL: the
+// sums alone, to the same bits.  part [fp8_quantize_sum_parts][K] binary32.  err here and below: the error word of the call's workspace.
 int fp8_quantize_sum_parts(int64_t rows, int K);
 cudaError_t launch_fp8_quantize_sum(const void* x, void* codes, void* scales, void* sums, float* part, int64_t rows,
                                     int K, const uint32_t* err, cudaStream_t s);

@@ -525,7 +525,7 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
  * need not be kept in any other form):
  *   dx       [rows, in_features]   = q(dy) W, where q(dy) is dy through dg_fp8_quantize with block_rows 1
  *   d_weight [out_features, in_features] = dy^T x    (dy in bf16 and the values of x: both exact)
- *   d_bias   [out_features]        = column sums of dy
+ *   d_bias   [out_features]        = column sums of dy (in an order that the sizes fix, whatever else is asked for)
  * all bf16, overwritten; each may be NULL (not computed).  x_* may be NULL without d_weight, w_* without dx.
  * The quantisers are passed through: dx is the gradient with respect to what x_codes stand for.
  * rows == 0 writes zeros into d_weight and d_bias.
