@@ -327,6 +327,12 @@ def fp8_norm_linear_layer(x: torch.Tensor, norm_weight: torch.Tensor, weight: to
 
 # ------------------------------------------------------------------ bf16 layers that keep 8-bit activations
 
+def _recorded(*tensors) -> bool:
+    """Whether autograd records a call on these inputs.  (Within a Function, needs_input_grad does not say that: it is
+    true under torch.no_grad() too.)"""
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
 class TPLinearKeep8(torch.autograd.Function):
     """tp_linear, its input kept in 8 bits for the weight's gradient."""
 
@@ -349,8 +355,10 @@ class TPLinearKeep8(torch.autograd.Function):
 
 def tp_linear_layer_keep8(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """tp_linear_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: the
-    weight's gradient is dy^T times what the codes stand for, the others are as there.  Of x nothing is kept where the
-    weight is frozen.  in % 16 == 0."""
+    weight's gradient is dy^T times what the codes stand for, the others are as there.  Of x nothing is kept, and
+    nothing quantised, where the weight is frozen or autograd does not record.  in % 16 == 0."""
+    if not _recorded(x, weight, bias):
+        return tp_linear(x, weight, bias)
     return TPLinearKeep8.apply(x, weight, bias)
 
 
@@ -373,5 +381,8 @@ class TPSwiGLUKeep8(torch.autograd.Function):
 
 def tp_swiglu_layer_keep8(x_shards: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
     """tp_swiglu_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: its
-    gradients are tp_swiglu_backward's at what the codes stand for.  d % 16 == 0."""
+    gradients are tp_swiglu_backward's at what the codes stand for.  Where autograd does not record, nothing is
+    quantised.  d % 16 == 0."""
+    if not _recorded(x_shards, w13, w2):
+        return tp_swiglu(x_shards, w13, w2)
     return TPSwiGLUKeep8.apply(x_shards, w13, w2)
