@@ -98,6 +98,7 @@ SIGNATURES = {
     "dg_fp8_linear_bf16_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "dg_fp8_linear_bf16": (ctypes.c_int, [_i64, _i64, _i64] + [_vp] * 6 + [_sz, _vp]),
     "dg_fp8_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "dg_fp8_linear_bwd_workspace_bytes_for": (_sz, [_i64, _i64, _i64, _i32, _i32, _i32]),
     "dg_fp8_linear_bwd": (ctypes.c_int, [_i64, _i64, _i64] + [_vp] * 9 + [_sz, _vp]),
     "dg_rms_norm": (ctypes.c_int, [_i64, _i64, _f32] + [_vp] * 8),
     "dg_rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),

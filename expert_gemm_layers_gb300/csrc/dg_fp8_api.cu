@@ -109,7 +109,8 @@ dg_status run_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x, c
   return run_mx(false, false, rows, out_f, in_f, x, sx, w, sw, bias, y, dev, s, "fp8_linear");
 }
 
-// Workspace of the backward: the error block, dy in 8 bits, partial column sums, the weight's codes turned, x in bf16.
+// Workspace of the backward: the error block, and what the gradients that are asked for need: for dx dy in 8 bits and the
+// weight's codes turned, for d_bias partial column sums, for d_weight x in bf16.
 // With many rows the product for dx takes the weight's codes with the contraction along their rows: as they lie, a
 // CTA's 112 columns of a 224-column tile begin anywhere in a 128-byte line, and the copies cost 25 of 100 of its time
 // (8192 rows, 14336 to 4096: 349 us against 276); turning them costs 2 bytes of traffic a weight, which pays from about
@@ -119,15 +120,21 @@ struct BwdLayout {
   size_t dy_codes, dy_scales, sums, w_turned, x, total;
   bool turn;
 };
-BwdLayout bwd_layout(int64_t rows, int64_t in_f, int64_t out_f) {
+BwdLayout bwd_layout(int64_t rows, int64_t in_f, int64_t out_f, bool dx, bool d_weight, bool d_bias) {
   BwdLayout l;
-  l.dy_codes = DG_ERROR_BLOCK_BYTES;
-  l.dy_scales = round256(l.dy_codes + elements(rows, out_f));
-  l.sums = round256(l.dy_scales + scale_bytes(rows, out_f, 1));
+  size_t at = DG_ERROR_BLOCK_BYTES;
+  auto take = [&](bool wanted, size_t bytes) {
+    const size_t here = at;
+    at = round256(at + (wanted ? bytes : 0));
+    return here;
+  };
   l.turn = rows >= kTurnRows && out_f <= 65535 * 128;
-  l.w_turned = round256(l.sums + 4 * elements(fp8_quantize_sum_parts(rows, static_cast<int>(out_f)), out_f));
-  l.x = round256(l.w_turned + (l.turn ? elements(out_f, in_f) : 0));
-  l.total = round256(l.x + 2 * elements(rows, in_f));
+  l.dy_codes = take(dx, elements(rows, out_f));
+  l.dy_scales = take(dx, scale_bytes(rows, out_f, 1));
+  l.sums = take(d_bias, 4 * elements(fp8_quantize_sum_parts(rows, static_cast<int>(out_f)), out_f));
+  l.w_turned = take(dx && l.turn, elements(out_f, in_f));
+  l.x = take(d_weight, 2 * elements(rows, in_f));
+  l.total = at;
   return l;
 }
 
@@ -240,9 +247,14 @@ dg_status dg_fp8_linear(int64_t rows, int64_t in_f, int64_t out_f, const void* x
                     static_cast<cudaStream_t>(stream));
 }
 
-size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
+size_t dg_fp8_linear_bwd_workspace_bytes_for(int64_t rows, int64_t in_features, int64_t out_features, int32_t dx,
+                                             int32_t d_weight, int32_t d_bias) {
   if (check_linear(rows, in_features, out_features, "fp8_linear_bwd") != DG_OK) return 0;
-  return bwd_layout(rows, in_features, out_features).total;
+  return bwd_layout(rows, in_features, out_features, dx != 0, d_weight != 0, d_bias != 0).total;
+}
+
+size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features) {
+  return dg_fp8_linear_bwd_workspace_bytes_for(rows, in_features, out_features, 1, 1, 1);
 }
 
 dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const void* x_codes, const void* x_scales,
@@ -251,7 +263,7 @@ dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const voi
   dg_status st = check_linear(rows, in_f, out_f, "fp8_linear_bwd");
   if (st != DG_OK) return st;
   const size_t xn = elements(rows, in_f), wn = elements(out_f, in_f), yn = elements(rows, out_f);
-  const BwdLayout l = bwd_layout(rows, in_f, out_f);
+  const BwdLayout l = bwd_layout(rows, in_f, out_f, dx != nullptr, d_weight != nullptr, d_bias != nullptr);
   const bool any = rows > 0;
   const Arg args[] = {{"x_codes", x_codes, xn, !(any && d_weight), false},
                       {"x_scales", x_scales, scale_bytes(rows, in_f, 1), !(any && d_weight), false, true},

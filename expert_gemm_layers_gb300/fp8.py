@@ -160,7 +160,8 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
 
     "x" = q(dy) W, where q(dy) is dy through fp8_quantize, "weight" = dy^T x (dy as it is), "bias" = column sums of
     dy; bf16, None where not needed.  x or weight may be None where its product is not needed (then the other gives
-    the sizes)."""
+    the sizes).  `workspace` (dg_fp8_linear_bwd_workspace_bytes_for) as in fp8_linear; scratch is that of the gradients
+    asked for."""
     lib, (index, lead, rows, out_f) = load(), _activations(dy, "dy")
     xc = xs = wc = ws = None
     if x is None and (need_dw or weight is None) or weight is None and need_dx:
@@ -177,8 +178,9 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
     new = lambda shape: torch.empty(shape, dtype=BF16, device=dy.device)
     g = dict(x=new((*lead, in_f)) if need_dx else None, weight=new((out_f, in_f)) if need_dw else None,
              bias=new((out_f,)) if need_db else None)
-    _launch_with(workspace, lib.dg_fp8_linear_bwd_workspace_bytes(rows, in_f, out_f), lib.dg_fp8_linear_bwd, index, rows,
-                 in_f, out_f, _p(xc), _p(xs), _p(wc), _p(ws), dy.data_ptr(), _p(g["x"]), _p(g["weight"]), _p(g["bias"]))
+    need = lib.dg_fp8_linear_bwd_workspace_bytes_for(rows, in_f, out_f, bool(need_dx), bool(need_dw), bool(need_db))
+    _launch_with(workspace, need, lib.dg_fp8_linear_bwd, index, rows, in_f, out_f, _p(xc), _p(xs), _p(wc), _p(ws),
+                 dy.data_ptr(), _p(g["x"]), _p(g["weight"]), _p(g["bias"]))
     return g
 
 

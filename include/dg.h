@@ -529,6 +529,8 @@ dg_status dg_fp8_dequantize(int64_t rows, int64_t K, int32_t block_rows, const v
  * all bf16, overwritten; each may be NULL (not computed).  x_* may be NULL without d_weight, w_* without dx.
  * The quantisers are passed through: dx is the gradient with respect to what x_codes stand for.
  * rows == 0 writes zeros into d_weight and d_bias.
+ * ws: dg_fp8_linear_bwd_workspace_bytes for any call of these sizes, dg_fp8_linear_bwd_workspace_bytes_for for one that
+ * asks for some of the gradients (nonzero: asked for), which can be far less.
  */
 size_t dg_fp8_linear_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
 
@@ -543,6 +545,9 @@ dg_status dg_fp8_linear_bf16(int64_t rows, int64_t in_features, int64_t out_feat
                              size_t ws_bytes, void* stream);
 
 size_t dg_fp8_linear_bwd_workspace_bytes(int64_t rows, int64_t in_features, int64_t out_features);
+
+size_t dg_fp8_linear_bwd_workspace_bytes_for(int64_t rows, int64_t in_features, int64_t out_features, int32_t dx,
+                                             int32_t d_weight, int32_t d_bias);
 
 dg_status dg_fp8_linear_bwd(int64_t rows, int64_t in_features, int64_t out_features, const void* x_codes,
                             const void* x_scales, const void* w_codes, const void* w_scales, const void* dy, void* dx,
