@@ -1540,9 +1540,11 @@ dg_status dg_tp_linear_bwd(int64_t rows, int64_t in_f, int64_t out_f, const void
                            void* stream) {
   dg_status st = check_linear(rows, in_f, out_f, "tp_linear_bwd");
   if (st != DG_OK) return st;
-  const void* ptrs[] = {x, weight, dy};
-  const char* names[] = {"x", "weight", "dy"};
-  if (const char* n = ptr_name_null(ptrs, names, 3)) return fail(DG_ERR_INVALID_ARGUMENT, "tp_linear_bwd: %s is NULL", n);
+  // x is read for d_weight alone
+  const void* ptrs[] = {weight, dy, x};
+  const char* names[] = {"weight", "dy", "x"};
+  if (const char* n = ptr_name_null(ptrs, names, d_weight ? 3 : 2))
+    return fail(DG_ERR_INVALID_ARGUMENT, "tp_linear_bwd: %s is NULL", n);
   if (const char* n = ptr_name_unaligned(ptrs, names, 3))
     return fail(DG_ERR_INVALID_ARGUMENT, "tp_linear_bwd: %s is not 16-byte aligned", n);
   if ((dx && !aligned16(dx)) || (d_weight && !aligned16(d_weight)) || (d_bias && !aligned16(d_bias)))

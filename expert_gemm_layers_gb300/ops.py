@@ -389,25 +389,28 @@ def tp_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None =
     return out
 
 
-def tp_linear_backward(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, need_dx: bool = True,
+def tp_linear_backward(x: torch.Tensor | None, weight: torch.Tensor, dy: torch.Tensor, need_dx: bool = True,
                        need_dw: bool = True, need_db: bool = False) -> dict:
-    """Gradients of tp_linear: "x" = dy weight, "weight" = dy^T x, "bias" = column sums of dy."""
+    """Gradients of tp_linear: "x" = dy weight, "weight" = dy^T x, "bias" = column sums of dy.  x may be None without
+    need_dw."""
     lib = load()
-    in_f = x.shape[-1]
-    out_f = weight.shape[0]
-    dev = x.device
-    _need(x, "x", torch.bfloat16)
+    if x is None and need_dw:
+        raise ValueError("x is needed for the weight's gradient")
+    out_f, in_f = weight.shape[0], (weight if x is None else x).shape[-1]
+    sizes, name = (dy, "dy") if x is None else (x, "x")
+    _need(sizes, name, torch.bfloat16)
+    lead, dev = sizes.shape[:-1], sizes.device
     _need(weight, "weight", torch.bfloat16, (out_f, in_f), dev)
-    _need(dy, "dy", torch.bfloat16, (*x.shape[:-1], out_f), dev)
-    rows = x.numel() // in_f
+    _need(dy, "dy", torch.bfloat16, (*lead, out_f), dev)
+    rows = dy.numel() // out_f if out_f else 0
     g = {}
-    g["x"] = torch.empty_like(x) if need_dx else None
+    g["x"] = torch.empty((*lead, in_f), dtype=torch.bfloat16, device=dev) if need_dx else None
     g["weight"] = torch.empty_like(weight) if need_dw else None
     g["bias"] = torch.empty(out_f, dtype=torch.bfloat16, device=dev) if need_db else None
     p = lambda t: None if t is None else _ptr(t)
     ws = error_block(dev)
     with torch.cuda.device(dev):
-        check(lib.dg_tp_linear_bwd(rows, in_f, out_f, _ptr(x), _ptr(weight), _ptr(dy), p(g["x"]), p(g["weight"]),
+        check(lib.dg_tp_linear_bwd(rows, in_f, out_f, p(x), _ptr(weight), _ptr(dy), p(g["x"]), p(g["weight"]),
                                    p(g["bias"]), _ptr(ws), ws.numel(), ctypes.c_void_p(_stream(dev))))
     return g
 

@@ -354,7 +354,7 @@ dg_status dg_tp_swiglu_noalloc(int64_t S, int64_t d, int64_t ffn, int32_t W, int
  *   weight [out_features, in_features], bias [out_features] or NULL
  * dg_tp_linear_bwd writes dx = dy weight [rows, in], d_weight = dy^T x
  * [out, in] and d_bias = column sums of dy [out]; any of the three may be NULL
- * (not computed).  Outputs are overwritten.
+ * (not computed); x may be NULL without d_weight.  Outputs are overwritten.
  * Requirements: rows, in_features, out_features >= 1; in_features and
  * out_features multiples of 8; 16-byte aligned tensors; outputs disjoint from
  * each other and from the inputs.  ws: the error block only
