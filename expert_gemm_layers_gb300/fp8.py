@@ -159,19 +159,20 @@ def fp8_linear_backward(x, weight, dy: torch.Tensor, need_dx: bool = True, need_
     """Gradients of fp8_linear from the 8-bit operands that the forward read, given dy [..., out] bf16.
 
     "x" = q(dy) W, where q(dy) is dy through fp8_quantize, "weight" = dy^T x (dy as it is), "bias" = column sums of
-    dy; bf16, None where not needed.  x or weight may be None where its product is not needed (then the other gives
-    the sizes).  `workspace` (dg_fp8_linear_bwd_workspace_bytes_for) as in fp8_linear; scratch is that of the gradients
-    asked for."""
+    dy; bf16, None where not needed.  x and weight may be None where their products are not needed.  `workspace`
+    (dg_fp8_linear_bwd_workspace_bytes_for) as in fp8_linear; scratch is that of the gradients asked for."""
     lib, (index, lead, rows, out_f) = load(), _activations(dy, "dy")
     xc = xs = wc = ws = None
-    if x is None and (need_dw or weight is None) or weight is None and need_dx:
+    if x is None and need_dw or weight is None and need_dx:
         raise ValueError("x is needed for the weight's gradient, weight for that of x")
+    in_f = 16  # where neither is given, for the bias's gradient: it has no part in that
     if x is not None:
         xc, xs, at, *_ = _held(x, "x")
         if xc.shape[:-1] != lead or at != index:
             raise ValueError(f"x codes have shape {tuple(xc.shape)} on device {at} beside dy {tuple(dy.shape)} on {index}")
-    in_f = _size(xc if xc is not None else _pair(weight, "weight")[0], -1)
+        in_f = xc.shape[-1]
     if weight is not None:
+        in_f = in_f if x is not None else _size(_pair(weight, "weight")[0], -1)
         wc, ws, n = _need_weight(weight, "weight", in_f, index)
         if n != out_f:
             raise ValueError(f"weight codes have shape {tuple(wc.shape)} beside dy {tuple(dy.shape)}")
@@ -199,8 +200,7 @@ class FP8Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias):
         x8, w8 = fp8_quantize(x), fp8_quantize(weight, 128)
         need_x, need_w, _ = ctx.needs_input_grad
-        # one of the two at least: the bias's gradient alone takes its sizes from there
-        ctx.save_for_backward(*(x8 if need_w else _NO_PAIR), *(w8 if need_x or not need_w else _NO_PAIR))
+        ctx.save_for_backward(*(x8 if need_w else _NO_PAIR), *(w8 if need_x else _NO_PAIR))
         return fp8_linear(x8, w8, bias)
 
     @staticmethod
@@ -263,8 +263,11 @@ def rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, d
 
 def _norm_grads(h, weight, dy, dh, eps, need):
     """(dx, d_weight, d_residual) of a norm for needs (x, weight, residual); dy or dh None: no gradient came that way."""
-    dy = torch.zeros_like(h) if dy is None else dy.contiguous()
-    g = rms_norm_backward(h, weight, dy, None if dh is None else dh.contiguous(), eps, need[0] or need[2], need[1])
+    dh = None if dh is None else dh.contiguous()
+    if dy is None:  # h alone was used: the sum passes its gradient on
+        g = dict(x=dh, weight=torch.zeros_like(weight) if need[1] else None)
+    else:
+        g = rms_norm_backward(h, weight, dy.contiguous(), dh, eps, need[0] or need[2], need[1])
     return g["x"] if need[0] else None, g["weight"], g["x"] if need[2] else None
 
 
@@ -301,7 +304,11 @@ class FP8NormLinear(torch.autograd.Function):
         n8, h = normed if residual is not None else (normed, x)
         w8 = fp8_quantize(weight, 128)
         y = fp8_linear(n8, w8, bias)
-        ctx.save_for_backward(h, norm_weight, *(n8 if ctx.needs_input_grad[2] else _NO_PAIR), *w8)
+        need_x, need_nw, need_w, need_b, need_r, _ = ctx.needs_input_grad
+        through = need_x or need_nw or need_r
+        ctx.save_for_backward(*((h, norm_weight) if through else _NO_PAIR), *(n8 if need_w else _NO_PAIR),
+                              *(w8 if through else _NO_PAIR))
+        ctx.weight_shape = weight.shape
         return y if residual is None else (y, h)
 
     @staticmethod
@@ -309,10 +316,12 @@ class FP8NormLinear(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         h, norm_weight, nc, ns, wc, ws = ctx.saved_tensors
         need_x, need_nw, need_w, need_b, need_r, _ = ctx.needs_input_grad
-        if dy is None:
-            dy = torch.zeros((*h.shape[:-1], wc.shape[0]), dtype=BF16, device=h.device)
         through = need_x or need_nw or need_r
-        g = fp8_linear_backward(_pair_or_none(nc, ns), (wc, ws), dy.contiguous(), through, need_w, need_b)
+        if dy is None:  # h alone was used
+            new = lambda shape: torch.zeros(shape, dtype=BF16, device=dh.device)
+            g = dict(x=None, weight=new(ctx.weight_shape) if need_w else None, bias=new(ctx.weight_shape[:1]) if need_b else None)
+        else:
+            g = fp8_linear_backward(_pair_or_none(nc, ns), _pair_or_none(wc, ws), dy.contiguous(), through, need_w, need_b)
         dx = dnw = dr = None
         if through:
             dx, dnw, dr = _norm_grads(h, norm_weight, g["x"], dh, ctx.eps, (need_x, need_nw, need_r))
@@ -322,8 +331,8 @@ class FP8NormLinear(torch.autograd.Function):
 def fp8_norm_linear_layer(x: torch.Tensor, norm_weight: torch.Tensor, weight: torch.Tensor,
                           bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, eps: float = 1e-6):
     """Differentiable rms_norm(x + residual) @ weight^T (+ bias), the norm's result in block-scaled e4m3: y, or (y, h)
-    with a residual.  Between forward and backward it keeps h (bf16, the residual stream itself) and 8 bits a value of
-    the norm's result (where the weight is trained) and of the weight."""
+    with a residual.  Between forward and backward it keeps, of h (bf16, the residual stream itself) and of 8 bits a
+    value of the norm's result and of the weight, what the gradients asked for read."""
     return FP8NormLinear.apply(x, norm_weight, weight, bias, residual, eps)
 
 
