@@ -670,6 +670,10 @@ cudaError_t launch_rms_norm(const void* x, const void* res, const void* w, void*
 
 namespace {
 
+// SMs that a grid of partial sums is made for.  Written out, so that the order of the sums and the scratch follow from the
+// sizes alone.
+constexpr int kSms = 152;
+
 // One pass up to 8192 columns; beyond, two (2048 x 16384: 280 us in one with spilled registers, 65 us in two).
 bool norm_bwd_one_pass(int d) { return d <= 8192; }
 
@@ -677,14 +681,14 @@ bool norm_bwd_one_pass(int d) { return d <= 8192; }
 
 int rms_norm_bwd_parts(int64_t rows, int d) {
   if (!norm_bwd_one_pass(d)) {
-    const int64_t across = (d + 2047) / 2048, want = (152 * 4 + across - 1) / across;
+    const int64_t across = (d + 2047) / 2048, want = (kSms * 4 + across - 1) / across;
     return static_cast<int>(rows < want ? rows : want);
   }
-  // as many CTAs as run at once on 152 SMs: 24 warps of 80 registers a thread with one chunk, 16 of 128 with two
+  // as many CTAs as run at once: 24 warps of 80 registers a thread with one chunk, 16 of 128 with two
   // (8192 x 1280: 26 us with a part of the CTAs left for a second turn, 16 us)
   const bool warp = d <= 512;
   const int64_t groups = warp ? (rows + kWarpRows - 1) / kWarpRows : rows;
-  const int64_t most = 152 * (warp ? 2 : d <= 2048 ? 768 / row_threads(d, 1) : 512 / row_threads(d, 2));
+  const int64_t most = kSms * (warp ? 2 : d <= 2048 ? 768 / row_threads(d, 1) : 512 / row_threads(d, 2));
   return static_cast<int>(groups < most ? groups : most);
 }
 
@@ -722,7 +726,7 @@ cudaError_t launch_rms_norm_bwd(const void* h, const void* w, const void* dy, co
 
 int fp8_quantize_sum_parts(int64_t rows, int K) {
   const int64_t nb = (K + 127) / 128, groups = (rows + 15) / 16;
-  const int64_t want = (152 * 8 + nb - 1) / nb;  // CTAs that run at once
+  const int64_t want = (kSms * 8 + nb - 1) / nb;  // CTAs that run at once
   return static_cast<int>(groups < want ? groups : want);
 }
 

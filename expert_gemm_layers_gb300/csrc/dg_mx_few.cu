@@ -6,14 +6,14 @@
 // along the weight.  One CTA takes 128 features and a part of K; the CTAs of a
 // cluster share the features and split K, leave their binary32 sums in shared
 // memory and add them through distributed shared memory in the order of their ranks
-// (the same result every time).  One row, 4096 to 6144: 8 to 9 us with the kernel in
-// front, 25 MB; 4 rows, 4096 to 28672: 22.5 us, 5.2 TB/s.
+// (the same result every time).  One row, 4096 to 6144: 6.6 us from codes, 7.3 from
+// bf16, 25 MB; 4 rows, 4096 to 28672: 22.5 and 24.2 us, 117 MB, 5.2 TB/s.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 MMA issuer, warps 2-5 bring
 // the block scales to TMEM (as in dg_mx.cuh) and then do the epilogue.  Where x comes in
 // bf16 and has at most four rows, they also quantise it into the stages, every CTA its
-// part of K: one launch fewer.  (With up to 32 rows that is too much work for four warps:
-// 24 rows, 14336 to 4096, took 19.7 us against 16.2 with a quantiser in front.)
+// part of K: one launch fewer.  The work grows with the rows that the form provides for; see
+// kMxFewBf16Rows for both sides.
 #include "dg_fp8.cuh"
 #include "dg_internal.h"
 #include "dg_mx.cuh"

@@ -282,9 +282,11 @@ static __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t 
 // attribute); every read of data a preceding kernel may have written comes
 // after it.  griddep_launch_dependents lets the next grid of the stream start
 // launching (its CTAs then run their own prologue up to their griddep_wait);
-// without it that happens as the CTAs exit.  It is issued late, near the end
-// of a CTA's work, so that waiting CTAs of the next grid do not sit beside
-// this one for long.
+// without it that happens as the CTAs exit.  The GEMMs of whole tiles issue it
+// late, near the end of a CTA's work, so that waiting CTAs of the next grid do
+// not sit beside this one for long; short kernels (rows, few-row products)
+// issue it right after their own griddep_wait, so that the next grid's launch
+// and prologue lie beside them.
 static __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 static __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -128,9 +128,9 @@ def fp8_linear(x, weight, bias: torch.Tensor | None = None, out: torch.Tensor | 
 
     x: activations in 8 bits (codes, scales), as fp8_quantize and rms_norm(..., fp8=True) return them, or bf16
     [..., in], which is quantised on the way.  weight: (codes, scales) of fp8_quantize(W [out, in], 128).  Sums in
-    binary32, one rounding to bf16.  `workspace` (dg_fp8_linear_workspace_bytes, or for bf16
-    dg_fp8_linear_bf16_workspace_bytes; its error block zeroed; default: this stream's own) is not shared by calls
-    that run at the same time."""
+    binary32, one rounding to bf16.  Inputs that require gradients are taken as constants (fp8_linear_layer is the
+    differentiable form).  `workspace` (dg_fp8_linear_workspace_bytes, or for bf16 dg_fp8_linear_bf16_workspace_bytes;
+    its error block zeroed; default: this stream's own) is not shared by calls that run at the same time."""
     lib = load()
     if isinstance(x, torch.Tensor):
         index, lead, rows, in_f = _activations(x, "x")
@@ -225,9 +225,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
              fp8: bool = False):
     """y = h / sqrt(mean(h^2) + eps) * weight over the last dimension, h = x + residual (bf16).
 
-    y is bf16, or with fp8 activations in 8 bits (codes, scales) for fp8_linear, from the binary32 values.  Returns y,
-    or (y, h) where a residual is given.  x, residual [..., d], weight [d] bf16; d % 8 == 0 (16 with fp8),
-    d <= 32768, eps >= 1e-30."""
+    y is bf16, or with fp8 activations in 8 bits (codes, scales) for fp8_linear, from the binary32 values.  Inputs that
+    require gradients are taken as constants (rms_norm_layer is the differentiable form).  Returns y, or (y, h) where a
+    residual is given.  x, residual [..., d], weight [d] bf16; d % 8 == 0 (16 with fp8), d <= 32768, eps >= 1e-30."""
     index, lead, rows, d = _activations(x, "x")
     _check(weight, "weight", BF16, (d,), index)
     h = y = codes = scales = None

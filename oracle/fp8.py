@@ -97,7 +97,10 @@ def rms_norm(h: np.ndarray, weight: np.ndarray, eps: float) -> np.ndarray:
 
 
 # Relative error of y in binary32: a thread sums at most 32 squares one after another and at most 37 partial sums
-# follow (half of it, by the root), then quotient, root, reciprocal and two products.
+# follow (half of it, by the root), then quotient, root, reciprocal and two products.  Each addition is counted as a
+# whole unit 2^-23, though it is off by half of one at most.  That covers the backward of long rows, where a thread adds
+# 128 and 13 follow: 141 halves are 70.5 units, fewer than the 32 + 37 + 8 of dx's sum; by the root 35.25, and with
+# quotient and eps (0.25 each), root, reciprocal and product (0.5 each) 37.25, fewer than the 40.5 here.
 NORM_REL = (32 + 37) * UP / 2 + 6 * UP
 
 
