@@ -345,40 +345,38 @@ def _recorded(*tensors) -> bool:
 
 
 class TPLinearKeep8(torch.autograd.Function):
-    """tp_linear, its input kept in 8 bits for the weight's gradient."""
+    """tp_linear, its input kept in 8 bits for the weight's gradient (keep: a backward can follow)."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias):
+    def forward(ctx, x, weight, bias, keep=True):
         y = tp_linear(x, weight, bias)
-        ctx.save_for_backward(*(fp8_quantize(x) if ctx.needs_input_grad[1] else _NO_PAIR), weight)
+        ctx.save_for_backward(*(fp8_quantize(x) if keep and ctx.needs_input_grad[1] else _NO_PAIR), weight)
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         codes, scales, weight = ctx.saved_tensors
-        need = ctx.needs_input_grad
+        need = ctx.needs_input_grad[:3]
         x = None if codes is None else fp8_dequantize(codes, scales)  # with a frozen weight nothing reads x
         g = tp_linear_backward(x, weight, dy.contiguous(), *need)
-        return g["x"], g["weight"], g["bias"]
+        return g["x"], g["weight"], g["bias"], None
 
 
 def tp_linear_layer_keep8(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None) -> torch.Tensor:
     """tp_linear_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: the
     weight's gradient is dy^T times what the codes stand for, the others are as there.  Of x nothing is kept, and
     nothing quantised, where the weight is frozen or autograd does not record.  in % 16 == 0."""
-    if not _recorded(x, weight, bias):
-        return tp_linear(x, weight, bias)
-    return TPLinearKeep8.apply(x, weight, bias)
+    return TPLinearKeep8.apply(x, weight, bias, _recorded(x, weight, bias))
 
 
 class TPSwiGLUKeep8(torch.autograd.Function):
-    """tp_swiglu, its input kept in 8 bits; the backward recomputes [a|b] from these."""
+    """tp_swiglu, its input kept in 8 bits (keep: a backward can follow); the backward recomputes [a|b] from these."""
 
     @staticmethod
-    def forward(ctx, x_shards, w13, w2):
+    def forward(ctx, x_shards, w13, w2, keep=True):
         y = tp_swiglu(x_shards, w13, w2)
-        ctx.save_for_backward(*fp8_quantize(x_shards), w13, w2)
+        ctx.save_for_backward(*(fp8_quantize(x_shards) if keep else _NO_PAIR), w13, w2)
         return y
 
     @staticmethod
@@ -386,13 +384,11 @@ class TPSwiGLUKeep8(torch.autograd.Function):
     def backward(ctx, dy):
         codes, scales, w13, w2 = ctx.saved_tensors
         g = tp_swiglu_backward(fp8_dequantize(codes, scales), w13, w2, dy.contiguous())
-        return g["x"], g["w13"], g["w2"]
+        return g["x"], g["w13"], g["w2"], None
 
 
 def tp_swiglu_layer_keep8(x_shards: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor) -> torch.Tensor:
     """tp_swiglu_layer (the same products, in bf16) that keeps 8 bits a value of x between forward and backward: its
     gradients are tp_swiglu_backward's at what the codes stand for.  Where autograd does not record, nothing is
     quantised.  d % 16 == 0."""
-    if not _recorded(x_shards, w13, w2):
-        return tp_swiglu(x_shards, w13, w2)
-    return TPSwiGLUKeep8.apply(x_shards, w13, w2)
+    return TPSwiGLUKeep8.apply(x_shards, w13, w2, _recorded(x_shards, w13, w2))

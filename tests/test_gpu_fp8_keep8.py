@@ -57,3 +57,25 @@ def test_some_inputs_trained(make, trained):
     assert torch.equal(got.detach(), y) and n == (1 if make is swiglu or 1 in trained else 0)
     for i, g in zip(trained, torch.autograd.grad(got, [args[i] for i in trained], dy)):
         assert torch.equal(g, every[i])
+
+
+@pytest.mark.parametrize("make", [linear, swiglu])
+def test_forward_mode_is_refused(make):
+    """Forward derivatives are not defined: an error, also where nothing is recorded for a backward."""
+    layer, _, args = make()
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(args[0], torch.ones_like(args[0]))
+        for on in (True, False):
+            with torch.set_grad_enabled(on), pytest.raises(RuntimeError):
+                layer(dual, *args[1:])
+
+
+def test_the_functions_take_their_inputs_alone():
+    """TPLinearKeep8 and TPSwiGLUKeep8 are public: called without the layers they keep what a backward reads."""
+    for make, fn in ((linear, dg.TPLinearKeep8), (swiglu, dg.TPSwiGLUKeep8)):
+        layer, y, args = make()
+        for t in args:
+            t.requires_grad_()
+        dy = randn(tuple(y.shape), 9).to(DEV)
+        a, b = (torch.autograd.grad(f(*args), args, dy) for f in (layer, fn.apply))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
